@@ -285,6 +285,83 @@ MAMBA_API int mamba_scan_bwd(const void* u, const void* delta, const float* A, c
                              void* dC, float* dD, void* dz, float* ddelta_bias, float* dinit, const void* saved,
                              size_t saved_bytes, hipStream_t stream);
 
+/* ---- Gated linear recurrence: one state a channel ----
+ *
+ * For batch b and channel d, visiting the tokens in scan order (0..L-1, or
+ * L-1..0 with reverse) with h = 0 (or initial_state) before the first:
+ *   E    = scale·softplus(lam[d])·sigmoid(r[t])     (lam NULL: a = sigmoid(r[t]), scale unused)
+ *   a    = exp(-E)
+ *   beta = sqrt(1 - a²), 1 - a or 1                 (mamba_glr_rule)
+ *   h    = a·h + beta·sigmoid(i[t])·x[t]            (i NULL: the factor sigmoid(i) is 1)
+ *   out[t] = h·silu(z[t])                           (z NULL: h)
+ * Where reset[b][t] is nonzero the token starts a sequence: the h before it (in
+ * scan order) counts as 0, whatever it holds, infinities and NaN included.
+ * 1 - a and sqrt(1 - a²) keep their relative accuracy as a approaches 1.  The
+ * state and every sum are float32.  The results of a call depend on its
+ * arguments alone, bit for bit.
+ */
+typedef enum { MAMBA_GLR_SQRT = 0, MAMBA_GLR_LERP = 1, MAMBA_GLR_UNIT = 2 } mamba_glr_rule;
+
+/* Problem description of the recurrence (host memory). */
+typedef struct {
+  int64_t batch;      /* B >= 1 */
+  int64_t seqlen;     /* L >= 1 tokens (ignored by mamba_glr_step) */
+  int64_t dim;        /* D >= 1 channels, a multiple of 4 */
+  int32_t dtype;      /* mamba_dtype of x, r, i, z, out and their gradients */
+  int32_t input_rule; /* mamba_glr_rule */
+  int32_t reverse;    /* nonzero: the scan runs from token L-1 to 0 */
+  float scale;        /* >= 0 and finite: the decay rate's factor */
+  const float* initial_state; /* optional, [B][D] */
+  const uint8_t* reset;       /* optional, [B][L] */
+  void* workspace;            /* device scratch owned by the caller (may be NULL when the query returns 0) */
+  size_t workspace_bytes;
+} mamba_glr_dims;
+
+/* Bytes of workspace of mamba_glr_fwd (0: none) and mamba_glr_bwd (never 0),
+ * and of the saved states.  Pure functions of the sizes, no HIP call;
+ * (size_t)-1 when the arguments are invalid or unsupported.  The contents of a
+ * workspace need not be initialised. */
+MAMBA_API size_t mamba_glr_fwd_workspace_bytes(const mamba_glr_dims* dims);
+MAMBA_API size_t mamba_glr_bwd_workspace_bytes(const mamba_glr_dims* dims);
+MAMBA_API size_t mamba_glr_saved_bytes(const mamba_glr_dims* dims);
+
+/*
+ * Forward.  x, r, out [B][L][D] dtype; i, z [B][L][D] dtype or NULL; lam [D]
+ * float32 or NULL; last_state [B][D] float32 or NULL (the state after the last
+ * token of the scan); saved: NULL, or the states before every 64th position of
+ * the scan, [B][ceil(L/64)][D] float32, for mamba_glr_bwd.  out must not alias
+ * an input.  Errors: MAMBA_ERR_INVALID (NULL x, r or out, a size <= 0, an
+ * unknown dtype or rule, a negative or infinite scale), MAMBA_ERR_UNSUPPORTED
+ * (D not a multiple of 4, a pointer other than reset not 16-byte aligned,
+ * sizes beyond 32-bit tile counts), MAMBA_ERR_WORKSPACE (workspace or saved too
+ * small), MAMBA_ERR_HIP.
+ */
+MAMBA_API int mamba_glr_fwd(const void* x, const void* r, const void* i, const void* z, const float* lam,
+                            const mamba_glr_dims* dims, void* out, float* last_state, float* saved, size_t saved_bytes,
+                            hipStream_t stream);
+
+/*
+ * Backward: gradients for dout [B][L][D] dtype and dlast [B][D] float32 (of
+ * last_state) or NULL.  dx, dr, di, dz [B][L][D] dtype (di required with i, dz
+ * with z, otherwise ignored); dlam [D] float32 or NULL (ignored without lam);
+ * dinit [B][D] float32 or NULL, the gradient of initial_state.  saved: what
+ * mamba_glr_fwd wrote for the same arguments, or NULL to recompute the states
+ * (the gradients are the same, bit for bit).  No output may alias an input or
+ * another output.  Errors as for mamba_glr_fwd.
+ */
+MAMBA_API int mamba_glr_bwd(const void* x, const void* r, const void* i, const void* z, const float* lam,
+                            const void* dout, const float* dlast, const mamba_glr_dims* dims, void* dx, void* dr,
+                            void* di, void* dz, float* dlam, float* dinit, const float* saved, size_t saved_bytes,
+                            hipStream_t stream);
+
+/*
+ * One token: state [B][D] float32 is updated in place, x_t, r_t, i_t, z_t and
+ * out are [B][D].  dims->seqlen, reverse, initial_state, reset and workspace
+ * are ignored.  Errors as for mamba_glr_fwd.
+ */
+MAMBA_API int mamba_glr_step(float* state, const void* x_t, const void* r_t, const void* i_t, const void* z_t,
+                             const float* lam, const mamba_glr_dims* dims, void* out, hipStream_t stream);
+
 /* Static, human-readable text for a status code (never NULL). */
 MAMBA_API const char* mamba_status_string(int status);
 

@@ -1,8 +1,9 @@
 """Builds libmamba_scan.so (the gfx950 HIP kernels and their C ABI) in-tree.
 
-The kernels are instantiated in eight translation units (the channel-block,
-step and backward kernels, and the row kernels; each per element type x
-input-term rule) compiled in parallel next to the host layer, then linked.
+The scan kernels are instantiated in eight translation units (the
+channel-block, step and backward kernels, and the row kernels; each per element
+type x input-term rule) and the gated-recurrence kernels in four (element type x
+resets), compiled in parallel next to the host layers, then linked.
 """
 from __future__ import annotations
 
@@ -19,9 +20,12 @@ LIB = os.path.join(HERE, "libmamba_scan.so")
 HOST = os.path.join(CSRC, "mamba_scan.hip")
 INST = os.path.join(CSRC, "scan_inst.hip")
 ROWS = os.path.join(CSRC, "row_inst.hip")
-SOURCES = [HOST, INST, ROWS]
+GLR_HOST = os.path.join(CSRC, "glr.hip")
+GLR = os.path.join(CSRC, "glr_inst.hip")
+HOSTS = [HOST, GLR_HOST]
+SOURCES = HOSTS + [INST, ROWS, GLR]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("scan_launch.h", "scan_kernels.h", "scan_row.h", "scan_bwd.h", "conv_kernels.h",
-                                                  "device_math.h")] + [
+                                                  "device_math.h", "glr_kernels.h", "glr_launch.h")] + [
     os.path.join(ROOT, "include", "mamba_scan.h")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # (bf16, exact) flags of the four instantiation units
@@ -51,7 +55,13 @@ def build(force: bool = True, extra_flags=(), out: str | None = None) -> str:
     if not force and os.path.exists(out) and all(os.path.getmtime(out) >= os.path.getmtime(d) for d in DEPS):
         return out
     with tempfile.TemporaryDirectory(prefix="mscan_build_") as tmp:
-        jobs = [[HIPCC] + FLAGS + list(extra_flags) + ["-c", "-o", os.path.join(tmp, "host.o"), HOST]]
+        jobs = [[HIPCC] + FLAGS + list(extra_flags) +
+                ["-c", "-o", os.path.join(tmp, "host_%s.o" % os.path.basename(h).split(".")[0]), h] for h in HOSTS]
+        for bf16 in (1, 0):
+            for reset in (1, 0):
+                jobs.append([HIPCC] + FLAGS + list(extra_flags) +
+                            ["-DMSCAN_INST_BF16=%d" % bf16, "-DMSCAN_INST_RESET=%d" % reset, "-c", "-o",
+                             os.path.join(tmp, "glr_%d%d.o" % (bf16, reset)), GLR])
         for unit in (INST, ROWS):
             for bf16, exact in VARIANTS:
                 obj = os.path.join(tmp, "%s_%d%d.o" % (os.path.basename(unit).split(".")[0], bf16, exact))

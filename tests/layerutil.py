@@ -1,0 +1,86 @@
+"""Plain float64 references of the operators around the scan, for the tests:
+the gated linear recurrence one position after the other, and its gradients by
+the chain rule."""
+import numpy as np
+
+from scanutil import from_dev, to_dev
+from selective_state_space_mamba_amd import inputs as I
+
+
+def rounded(v, dtype):
+    """v as the element type holds it: (storage array for the device, float64 values)."""
+    v = np.asarray(v, np.float32)
+    if dtype == "bf16":
+        bits = I.bf16_bits(v)
+        return bits, I.bf16_to_f32(bits).astype(np.float64)
+    return v, v.astype(np.float64)
+
+
+def sigm(v):
+    with np.errstate(over="ignore"):
+        return 1.0 / (1.0 + np.exp(-v))
+
+
+def softplus(v):
+    return np.logaddexp(0.0, v)
+
+
+def glr_gates(r, lam, scale, rule):
+    """E, a, beta and dbeta/dE."""
+    E = softplus(-r) if lam is None else scale * softplus(lam) * sigm(r)
+    a = np.exp(-E)
+    if rule == "sqrt":
+        beta = np.sqrt(-np.expm1(-2 * E))
+        return E, a, beta, a * a / np.maximum(beta, 1e-150)
+    if rule == "lerp":
+        return E, a, -np.expm1(-E), a
+    return E, a, np.ones_like(E), np.zeros_like(E)
+
+
+def order(L, reverse):
+    return range(L - 1, -1, -1) if reverse else range(L)
+
+
+def glr_ref(x, r, i, z, lam, *, scale=8.0, rule="sqrt", reverse=False, init=None, reset=None):
+    """(out, last_state, h, h_before) in float64."""
+    B, L, D = x.shape
+    E, a, beta, _ = glr_gates(r, lam, scale, rule)
+    v = beta * (x if i is None else sigm(i) * x)
+    h, hp = np.zeros_like(x), np.zeros_like(x)
+    s = np.zeros((B, D)) if init is None else init.astype(np.float64)
+    for t in order(L, reverse):
+        if reset is not None:
+            s = np.where(reset[:, t, None] != 0, 0.0, s)
+        hp[:, t] = s
+        s = a[:, t] * s + v[:, t]
+        h[:, t] = s
+    out = h if z is None else h * (z * sigm(z))
+    return out, s, h, hp
+
+
+def glr_grads(x, r, i, z, lam, dout, dlast=None, *, scale=8.0, rule="sqrt", reverse=False, init=None, reset=None):
+    B, L, D = x.shape
+    E, a, beta, db = glr_gates(r, lam, scale, rule)
+    _, _, h, hp = glr_ref(x, r, i, z, lam, scale=scale, rule=rule, reverse=reverse, init=init, reset=reset)
+    p = np.ones_like(x) if i is None else sigm(i)
+    sz = None if z is None else sigm(z)
+    dh = dout if z is None else dout * z * sz
+    m = np.zeros_like(x)
+    c = np.zeros((B, D)) if dlast is None else dlast.astype(np.float64)
+    for t in reversed(order(L, reverse)):
+        m[:, t] = dh[:, t] + c
+        c = a[:, t] * m[:, t]
+        if reset is not None:
+            c = np.where(reset[:, t, None] != 0, 0.0, c)
+    dE = m * (p * x * db - a * hp)
+    g = dict(dx=m * beta * p, di=None if i is None else m * beta * x * p * (1 - p),
+             dz=None if z is None else dout * h * sz * (1 + z * (1 - sz)), dlam=None, dinit=c)
+    if lam is None:
+        g["dr"] = -dE * sigm(-r)
+    else:
+        g["dr"] = dE * E * (1 - sigm(r))
+        g["dlam"] = (dE * sigm(r)).sum((0, 1)) * scale * sigm(lam)
+    return g
+
+
+__all__ = ["rounded", "sigm", "softplus", "glr_ref", "glr_grads", "from_dev", "to_dev"]

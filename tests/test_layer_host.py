@@ -1,0 +1,122 @@
+"""Host-side checks of the operators around the scan (no GPU work): sizes,
+refusals before any launch, and the float64 references' gradients against
+differences."""
+import ctypes
+import os
+
+import numpy as np
+import pytest
+
+import selective_state_space_mamba_amd as ms
+from selective_state_space_mamba_amd import _binding as E
+
+from layerutil import glr_grads, glr_ref
+
+FAKE = 0x100000  # 16-byte aligned stand-in pointer: every call below fails validation first
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(ms.LIB_PATH):
+        from selective_state_space_mamba_amd import build
+        build.build(force=False)
+    return ms.load_library()
+
+
+def glr_dims(**kw):
+    base = dict(batch=2, seqlen=100, dim=64, dtype=ms.DTYPE_BF16)
+    base.update(kw)
+    return ms.make_glr_dims(base.pop("batch"), base.pop("seqlen"), base.pop("dim"), base.pop("dtype"), **base)
+
+
+def test_glr_sizes(lib):
+    assert ms.glr_fwd_workspace_bytes(glr_dims()) == 0  # one tile: nothing to join
+    assert ms.glr_fwd_workspace_bytes(glr_dims(seqlen=1000)) > 0
+    assert ms.glr_fwd_workspace_bytes(glr_dims(seqlen=1000, batch=4096)) == 0  # enough rows: tiles walked in order
+    assert ms.glr_bwd_workspace_bytes(glr_dims()) > 0
+    assert ms.glr_saved_bytes(glr_dims()) == 2 * 2 * 64 * 4
+    assert ms.glr_saved_bytes(glr_dims(seqlen=128)) == 2 * 2 * 64 * 4
+    assert ms.glr_saved_bytes(glr_dims(seqlen=129)) == 2 * 3 * 64 * 4
+    for bad in (dict(batch=0), dict(seqlen=0), dict(dim=-4), dict(dim=6), dict(dtype=4), dict(input_rule=3),
+                dict(scale=-1.0), dict(scale=float("inf")), dict(scale=float("nan")), dict(dim=1 << 22),
+                dict(seqlen=(1 << 31) - 64), dict(batch=1 << 24, seqlen=1 << 20)):
+        for query in (ms.glr_fwd_workspace_bytes, ms.glr_bwd_workspace_bytes, ms.glr_saved_bytes):
+            with pytest.raises(ms.MambaError):
+                query(glr_dims(**bad))
+
+
+def test_glr_refusals(lib):
+    def fwd(d, **kw):
+        p = dict(x=FAKE, r=FAKE, i=None, z=None, lam=None, out=FAKE, last=None, saved=None, n=0)
+        p.update(kw)
+        return lib.mamba_glr_fwd(p["x"], p["r"], p["i"], p["z"], p["lam"], ctypes.byref(d), p["out"], p["last"],
+                                 p["saved"], p["n"], None)
+
+    for miss in ("x", "r", "out"):
+        assert fwd(glr_dims(), **{miss: None}) == E.MAMBA_ERR_INVALID
+    assert fwd(glr_dims(batch=0)) == E.MAMBA_ERR_INVALID
+    assert fwd(glr_dims(dim=66)) == E.MAMBA_ERR_UNSUPPORTED
+    for odd in ("x", "r", "i", "z", "lam", "out", "last", "saved"):
+        assert fwd(glr_dims(), **{odd: FAKE + 8, "n": 1 << 30}) == E.MAMBA_ERR_UNSUPPORTED
+    assert fwd(glr_dims(), saved=FAKE, n=2 * 2 * 64 * 4 - 1) == E.MAMBA_ERR_WORKSPACE
+    assert fwd(glr_dims(seqlen=1000)) == E.MAMBA_ERR_WORKSPACE
+    need = ms.glr_fwd_workspace_bytes(glr_dims(seqlen=1000))
+    assert fwd(glr_dims(seqlen=1000, workspace=FAKE, workspace_bytes=need - 1)) == E.MAMBA_ERR_WORKSPACE
+
+    def bwd(d, **kw):
+        p = dict(x=FAKE, r=FAKE, i=None, z=None, lam=None, dout=FAKE, dx=FAKE, dr=FAKE, di=None, dz=None, dlam=None,
+                 saved=None, n=0)
+        p.update(kw)
+        return lib.mamba_glr_bwd(p["x"], p["r"], p["i"], p["z"], p["lam"], p["dout"], None, ctypes.byref(d), p["dx"],
+                                 p["dr"], p["di"], p["dz"], p["dlam"], None, p["saved"], p["n"], None)
+
+    for miss in ("x", "r", "dout", "dx", "dr"):
+        assert bwd(glr_dims(), **{miss: None}) == E.MAMBA_ERR_INVALID
+    assert bwd(glr_dims(), i=FAKE) == E.MAMBA_ERR_INVALID  # i's gradient has nowhere to go
+    assert bwd(glr_dims(), z=FAKE) == E.MAMBA_ERR_INVALID
+    assert bwd(glr_dims(), dr=FAKE + 4) == E.MAMBA_ERR_UNSUPPORTED
+    assert bwd(glr_dims()) == E.MAMBA_ERR_WORKSPACE
+    need = ms.glr_bwd_workspace_bytes(glr_dims())
+    assert bwd(glr_dims(workspace=FAKE, workspace_bytes=need - 1)) == E.MAMBA_ERR_WORKSPACE
+    assert bwd(glr_dims(workspace=FAKE, workspace_bytes=need), saved=FAKE, n=16) == E.MAMBA_ERR_WORKSPACE
+
+    def step(d, **kw):
+        p = dict(state=FAKE, x=FAKE, r=FAKE, out=FAKE)
+        p.update(kw)
+        return lib.mamba_glr_step(p["state"], p["x"], p["r"], None, None, None, ctypes.byref(d), p["out"], None)
+
+    for miss in ("state", "x", "r", "out"):
+        assert step(glr_dims(), **{miss: None}) == E.MAMBA_ERR_INVALID
+    assert step(glr_dims(dim=0)) == E.MAMBA_ERR_INVALID
+    assert step(glr_dims(), state=FAKE + 4) == E.MAMBA_ERR_UNSUPPORTED
+    assert lib.mamba_glr_step(FAKE, FAKE, FAKE, None, None, None, None, FAKE, None) == E.MAMBA_ERR_INVALID
+
+
+@pytest.mark.parametrize("rule", ["sqrt", "lerp", "unit"])
+@pytest.mark.parametrize("with_lam", [True, False])
+@pytest.mark.parametrize("reverse", [True, False])
+def test_glr_reference_gradients_against_differences(rule, with_lam, reverse):
+    """Central differences in float64: relative error near eps² = 1e-10 plus 1e-16/eps; 1e-7 is asked."""
+    r = np.random.Generator(np.random.PCG64(9))
+    B, L, D = 2, 13, 3
+    v = {k: r.standard_normal((B, L, D)) for k in ("x", "r", "i", "z")}
+    v["lam"] = r.uniform(-4, 0, D) if with_lam else None
+    v["init"] = r.standard_normal((B, D))
+    dout, dlast = r.standard_normal((B, L, D)), r.standard_normal((B, D))
+    reset = (r.uniform(size=(B, L)) < 0.2).astype(np.uint8)
+
+    def loss(u):
+        out, last, _, _ = glr_ref(u["x"], u["r"], u["i"], u["z"], u["lam"], rule=rule, reverse=reverse,
+                                  init=u["init"], reset=reset)
+        return (out * dout).sum() + (last * dlast).sum()
+
+    g = glr_grads(v["x"], v["r"], v["i"], v["z"], v["lam"], dout, dlast, rule=rule, reverse=reverse, init=v["init"],
+                  reset=reset)
+    for k in ("x", "r", "i", "z", "lam", "init"):
+        if v[k] is None:
+            continue
+        d = r.standard_normal(v[k].shape)
+        eps = 1e-5
+        num = (loss(dict(v, **{k: v[k] + eps * d})) - loss(dict(v, **{k: v[k] - eps * d}))) / (2 * eps)
+        want = (g["d" + k] * d).sum()
+        assert abs(num - want) <= 1e-7 * max(1.0, abs(want)), (k, num, want)
