@@ -362,6 +362,53 @@ MAMBA_API int mamba_glr_bwd(const void* x, const void* r, const void* i, const v
 MAMBA_API int mamba_glr_step(float* state, const void* x_t, const void* r_t, const void* i_t, const void* z_t,
                              const float* lam, const mamba_glr_dims* dims, void* out, hipStream_t stream);
 
+/* Activations of the group normalisation and of the matrix product: none,
+ * max(u, 0), u·sigmoid(u), u·Φ(u) (Φ the standard normal distribution's cdf). */
+typedef enum { MAMBA_ACT_NONE = 0, MAMBA_ACT_RELU = 1, MAMBA_ACT_SILU = 2, MAMBA_ACT_GELU = 3 } mamba_act;
+
+/* ---- Group normalisation with an activation, channels last ----
+ *
+ * The D channels of every item b fall into G groups of D/G neighbours; with
+ * mean and var over the L·D/G values of (b, g),
+ *   out = act((x - mean)·rstd·weight + bias),  rstd = 1/sqrt(var + eps).
+ * seqlen 1 normalises every token by itself (with one group: layer
+ * normalisation; with a group a head: over the heads). */
+typedef struct {
+  int64_t batch;   /* B >= 1 items */
+  int64_t seqlen;  /* L >= 1 positions of an item */
+  int64_t dim;     /* D >= 1 channels, a multiple of 8, at most 8192 */
+  int64_t groups;  /* G >= 1, a divisor of D */
+  int32_t dtype;   /* mamba_dtype of x, out, dout and dx */
+  int32_t act;     /* mamba_act */
+  float eps;       /* >= 0 and finite */
+  void* workspace; /* device scratch owned by the caller (may be NULL when the query returns 0) */
+  size_t workspace_bytes;
+} mamba_norm_dims;
+
+/* Bytes of workspace; pure functions of the sizes, (size_t)-1 when the
+ * arguments are invalid or unsupported.  The contents need not be initialised. */
+MAMBA_API size_t mamba_group_norm_fwd_workspace_bytes(const mamba_norm_dims* dims);
+MAMBA_API size_t mamba_group_norm_bwd_workspace_bytes(const mamba_norm_dims* dims);
+
+/*
+ * Forward.  x, out [B][L][D] dtype; weight, bias [D] float32 or NULL (1 and
+ * 0); mean, rstd [B][G] float32, written, or NULL.  out must not alias x.
+ * Errors: MAMBA_ERR_INVALID (NULL x or out, a size <= 0, G not a divisor of D,
+ * unknown dtype or act, eps negative or not finite), MAMBA_ERR_UNSUPPORTED (D not a multiple of 8 or above 8192, x, out
+ * or workspace not 16-byte aligned), MAMBA_ERR_WORKSPACE, MAMBA_ERR_HIP.
+ */
+MAMBA_API int mamba_group_norm_fwd(const void* x, const float* weight, const float* bias, const mamba_norm_dims* dims,
+                                   void* out, float* mean, float* rstd, hipStream_t stream);
+
+/*
+ * Backward: dx [B][L][D] dtype, dweight and dbias [D] float32 or NULL, for
+ * dout [B][L][D] dtype and the mean and rstd that the forward wrote.  No output
+ * may alias an input.  Sums are float32 and in a fixed order.  Errors as above.
+ */
+MAMBA_API int mamba_group_norm_bwd(const void* x, const float* weight, const float* bias, const void* dout,
+                                   const float* mean, const float* rstd, const mamba_norm_dims* dims, void* dx,
+                                   float* dweight, float* dbias, hipStream_t stream);
+
 /* Static, human-readable text for a status code (never NULL). */
 MAMBA_API const char* mamba_status_string(int status);
 

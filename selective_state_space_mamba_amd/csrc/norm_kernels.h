@@ -1,0 +1,432 @@
+// norm_kernels.h -- gfx950 HIP kernels of group normalisation with an
+// activation over channels-last activations x [B][L][D]: the D channels of an
+// item fall into G groups of C = D/G, and
+//   mean, var over the L·C values of (b, g);  xh = (x - mean)·rstd,  rstd = 1/sqrt(var + eps)
+//   out = act(u),  u = xh·w + bias
+// Backward, with du = dout·act'(u), t = du·w and n = L·C:
+//   dx = rstd·(t - (Σ t)/n - xh·(Σ t·xh)/n),  dw = Σ du·xh,  dbias = Σ du
+//
+// Layout.  Each thread owns one vector of 8 neighbouring channels and walks
+// down the rows, so that a wave reads whole rows and a group may begin and end
+// inside a vector (6 channels a group): statistics are kept per channel until
+// the rows are done and joined to groups through LDS.  A workgroup takes one
+// run of rows with all D channels.
+//
+// Statistics.  Sums of x and x² about the run's first row (a value of the
+// channel itself, so that an offset of the channel costs no bits), turned into
+// mean and sum of squared deviations M per channel; sets are joined by
+//   mean = Σ n_i·mean_i / n,  M = Σ (M_i + n_i·(mean_i - mean)²).
+//
+// What bounds it: bytes.  An item that one workgroup can take is read twice by
+// the same workgroup, the second time from the caches close by; a larger one
+// by two kernels, the second time from the 256 MB last-level cache where it fits.
+#pragma once
+
+#include "act_math.h"
+
+namespace mscan {
+
+constexpr int kNormV = 8;
+constexpr int kNormMaxThreads = 1024;
+constexpr int kNormMaxD = kNormV * kNormMaxThreads;
+
+struct NormParams {
+  const void* x;      // [B][L][D]
+  const float* w;     // [D] or null
+  const float* bias;  // [D] or null
+  void* out;          // [B][L][D]
+  float *mean, *rstd; // [B][G]; written by the forward (may be null), read by the backward
+  const void* dout;   // [B][L][D]
+  void* dx;           // [B][L][D]
+  float2* pg;         // [B][chunks][G]: (mean, M) forward, (Σ t, Σ t·xh) backward
+  float2* pc;         // [rows of partials][D]: (Σ du, Σ du·xh)
+  int B, L, D, G, C, nv, slots, chunks, chunk_len, lpg, lpc, want_dw;
+  float eps;
+};
+
+__device__ __forceinline__ void vstore(uint16_t* p, const float (&y)[8]) { storeV<8>(p, y); }
+__device__ __forceinline__ void vstore(float* p, const float (&y)[8]) { storeV<8>(p, y); }
+
+// Sum over `width` (a power of two up to 64) neighbouring lanes, left in each of them.
+__device__ __forceinline__ float lane_sum(float v, int width) {
+  for (int o = width >> 1; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// ---- pieces of a workgroup's work; red: 2·slots·D floats of LDS ----
+
+// Per-channel mean and M of rows [l0, l1) of item b, left in red[0..D) and red[slots·D..slots·D + D).
+template <typename T>
+__device__ __forceinline__ void rows_stats(const NormParams& p, const T* xb, int l0, int l1, float* red) {
+  const int tid = threadIdx.x, slot = tid / p.nv, col = tid % p.nv;
+  const int D = p.D, n = p.slots * D;
+  const bool on = slot < p.slots;
+  float s[8], q[8], sh[8];
+  if (on) {
+    Vec<T, 8> v;
+    v.load(xb + (int64_t)l0 * D + col * 8);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sh[j] = v.get(j), s[j] = 0.f, q[j] = 0.f;
+    const T* px = xb + (int64_t)(l0 + slot) * D + col * 8;
+    const int64_t step = (int64_t)p.slots * D;
+#pragma unroll 4
+    for (int l = l0 + slot; l < l1; l += p.slots, px += step) {
+      Vec<T, 8> r;
+      r.load(px);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = r.get(j) - sh[j];
+        s[j] += d;
+        q[j] = __builtin_fmaf(d, d, q[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      red[slot * D + col * 8 + j] = s[j];
+      red[n + slot * D + col * 8 + j] = q[j];
+    }
+  }
+  __syncthreads();
+  const float cnt = (float)(l1 - l0), inv = 1.0f / cnt;
+  for (int c = tid; c < D; c += blockDim.x) {
+    float S = 0.f, Q = 0.f;
+    for (int k = 0; k < p.slots; ++k) S += red[k * D + c], Q += red[n + k * D + c];
+    red[c] = to_f32(xb[(int64_t)l0 * D + c]) + S * inv;
+    red[n + c] = __builtin_fmaxf(Q - S * S * inv, 0.f);
+  }
+  __syncthreads();
+}
+
+// The channels' means and Ms of `cnt` rows (as rows_stats leaves them) joined into groups: f(g, mean, M).
+template <typename F>
+__device__ __forceinline__ void join_channels(const NormParams& p, const float* red, float cnt, F f) {
+  const int n = p.slots * p.D, li = threadIdx.x % p.lpg, per = blockDim.x / p.lpg;
+  for (int g0 = 0; g0 < p.G; g0 += per) {
+    const int g = g0 + threadIdx.x / p.lpg;
+    const bool on = g < p.G;
+    float m = 0.f, q = 0.f;
+    if (on)
+      for (int c = li; c < p.C; c += p.lpg) m += red[g * p.C + c];
+    m = lane_sum(m, p.lpg) / (float)p.C;
+    if (on)
+      for (int c = li; c < p.C; c += p.lpg) {
+        const float d = red[g * p.C + c] - m;
+        q += __builtin_fmaf(cnt * d, d, red[n + g * p.C + c]);
+      }
+    q = lane_sum(q, p.lpg);
+    if (on && li == 0) f(g, m, q);
+  }
+}
+
+// Normalises rows [l0, l1); mean and rstd of the item's groups in LDS.
+template <typename T, int ACT>
+__device__ __forceinline__ void rows_apply(const NormParams& p, const T* xb, T* ob, int l0, int l1, const float* sMean,
+                                           const float* sRstd) {
+  const int tid = threadIdx.x, slot = tid / p.nv, col = tid % p.nv, D = p.D;
+  if (slot >= p.slots) return;
+  float mu[8], sc[8], bi[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int d = col * 8 + j, g = d / p.C;
+    mu[j] = sMean[g];
+    sc[j] = sRstd[g] * (p.w ? p.w[d] : 1.f);
+    bi[j] = p.bias ? p.bias[d] : 0.f;
+  }
+  const int64_t step = (int64_t)p.slots * D;
+  int64_t at = (int64_t)(l0 + slot) * D + col * 8;
+#pragma unroll 4
+  for (int l = l0 + slot; l < l1; l += p.slots, at += step) {
+    Vec<T, 8> v;
+    v.load(xb + at);
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = act_f<ACT>(__builtin_fmaf(v.get(j) - mu[j], sc[j], bi[j]));
+    vstore(ob + at, y);
+  }
+}
+
+// ---- forward ----
+
+// One workgroup an item.
+template <typename T, int ACT>
+__global__ void __launch_bounds__(kNormMaxThreads) norm_item_kernel(const NormParams p) {
+  extern __shared__ float lds[];
+  float* const sMean = lds + 2 * p.slots * p.D;
+  float* const sRstd = sMean + p.G;
+  const int b = blockIdx.x;
+  const T* const xb = static_cast<const T*>(p.x) + (int64_t)b * p.L * p.D;
+  rows_stats<T>(p, xb, 0, p.L, lds);
+  const float inv = 1.0f / ((float)p.L * (float)p.C);
+  join_channels(p, lds, (float)p.L, [&](int g, float m, float q) {
+    const float r = 1.0f / __builtin_sqrtf(q * inv + p.eps);
+    sMean[g] = m;
+    sRstd[g] = r;
+    if (p.mean) p.mean[(int64_t)b * p.G + g] = m;
+    if (p.rstd) p.rstd[(int64_t)b * p.G + g] = r;
+  });
+  __syncthreads();
+  rows_apply<T, ACT>(p, xb, static_cast<T*>(p.out) + (int64_t)b * p.L * p.D, 0, p.L, sMean, sRstd);
+}
+
+// Larger items in runs of rows: the runs' statistics, then the rows.
+template <typename T>
+__global__ void __launch_bounds__(kNormMaxThreads) norm_stats_kernel(const NormParams p) {
+  extern __shared__ float lds[];
+  const int b = blockIdx.x / p.chunks, k = blockIdx.x % p.chunks;
+  const int l0 = k * p.chunk_len, l1 = min(p.L, l0 + p.chunk_len);
+  rows_stats<T>(p, static_cast<const T*>(p.x) + (int64_t)b * p.L * p.D, l0, l1, lds);
+  join_channels(p, lds, (float)(l1 - l0),
+                [&](int g, float m, float q) { p.pg[((int64_t)b * p.chunks + k) * p.G + g] = make_float2(m, q); });
+}
+
+template <typename T, int ACT>
+__global__ void __launch_bounds__(kNormMaxThreads) norm_apply_kernel(const NormParams p) {
+  extern __shared__ float lds[];
+  float *const sMean = lds, *const sRstd = lds + p.G;
+  const int b = blockIdx.x / p.chunks, k = blockIdx.x % p.chunks;
+  const int l0 = k * p.chunk_len, l1 = min(p.L, l0 + p.chunk_len);
+  // every workgroup joins the item's runs (the same way, to the same bits)
+  const float2* const pg = p.pg + (int64_t)b * p.chunks * p.G;
+  const int li = threadIdx.x % p.lpc, per = blockDim.x / p.lpc;
+  for (int g0 = 0; g0 < p.G; g0 += per) {
+    const int g = g0 + threadIdx.x / p.lpc;
+    const bool on = g < p.G;
+    float m = 0.f, q = 0.f;
+    if (on)
+      for (int c = li; c < p.chunks; c += p.lpc)
+        m = __builtin_fmaf((float)min(p.chunk_len, p.L - c * p.chunk_len), pg[(int64_t)c * p.G + g].x, m);
+    m = lane_sum(m, p.lpc) / (float)p.L;
+    if (on)
+      for (int c = li; c < p.chunks; c += p.lpc) {
+        const float2 v = pg[(int64_t)c * p.G + g];
+        const float d = v.x - m, cnt = (float)min(p.chunk_len, p.L - c * p.chunk_len) * (float)p.C;
+        q += __builtin_fmaf(cnt * d, d, v.y);
+      }
+    q = lane_sum(q, p.lpc);
+    if (on && li == 0) {
+      const float r = 1.0f / __builtin_sqrtf(q / ((float)p.L * (float)p.C) + p.eps);
+      sMean[g] = m;
+      sRstd[g] = r;
+      if (k == 0 && p.mean) p.mean[(int64_t)b * p.G + g] = m;
+      if (k == 0 && p.rstd) p.rstd[(int64_t)b * p.G + g] = r;
+    }
+  }
+  __syncthreads();
+  const int64_t base = (int64_t)b * p.L * p.D;
+  rows_apply<T, ACT>(p, static_cast<const T*>(p.x) + base, static_cast<T*>(p.out) + base, l0, l1, sMean, sRstd);
+}
+
+// ---- backward ----
+
+struct NormCol {  // a thread's eight channels of one item
+  float mu[8], rs[8], w[8], bi[8];
+  __device__ __forceinline__ void load(const NormParams& p, int b, int col) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int d = col * 8 + j, g = d / p.C;
+      mu[j] = p.mean[(int64_t)b * p.G + g];
+      rs[j] = p.rstd[(int64_t)b * p.G + g];
+      w[j] = p.w ? p.w[d] : 1.f;
+      bi[j] = p.bias ? p.bias[d] : 0.f;
+    }
+  }
+};
+
+// Per-channel Σ du and Σ du·xh of rows [l0, l1), a thread's own rows in s, q.
+template <typename T, int ACT>
+__device__ __forceinline__ void rows_grad_sums(const NormParams& p, const T* xb, const T* yb, int l0, int l1, const NormCol& k,
+                                               float (&s)[8], float (&q)[8]) {
+  const int slot = threadIdx.x / p.nv, col = threadIdx.x % p.nv;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j] = 0.f, q[j] = 0.f;
+  if (slot >= p.slots) return;
+  const int64_t step = (int64_t)p.slots * p.D;
+  int64_t at = (int64_t)(l0 + slot) * p.D + col * 8;
+#pragma unroll 2
+  for (int l = l0 + slot; l < l1; l += p.slots, at += step) {
+    Vec<T, 8> v, dy;
+    v.load(xb + at);
+    dy.load(yb + at);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float xh = (v.get(j) - k.mu[j]) * k.rs[j];
+      const float du = dy.get(j) * act_d<ACT>(__builtin_fmaf(xh, k.w[j], k.bi[j]));
+      s[j] += du;
+      q[j] = __builtin_fmaf(du, xh, q[j]);
+    }
+  }
+}
+
+// The rows' sums of the workgroup joined per channel in red (layout of rows_stats).
+__device__ __forceinline__ void join_slots(const NormParams& p, const float (&s)[8], const float (&q)[8], float* red) {
+  const int tid = threadIdx.x, slot = tid / p.nv, col = tid % p.nv, D = p.D, n = p.slots * D;
+  __syncthreads();
+  if (slot < p.slots) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      red[slot * D + col * 8 + j] = s[j];
+      red[n + slot * D + col * 8 + j] = q[j];
+    }
+  }
+  __syncthreads();
+  for (int c = tid; c < D; c += blockDim.x) {
+    float S = 0.f, Q = 0.f;
+    for (int k = 0; k < p.slots; ++k) S += red[k * D + c], Q += red[n + k * D + c];
+    red[c] = S;
+    red[n + c] = Q;
+  }
+  __syncthreads();
+}
+
+// Σ t and Σ t·xh of every group from the channels' sums: f(g, a, b).
+template <typename F>
+__device__ __forceinline__ void join_grad_groups(const NormParams& p, const float* red, F f) {
+  const int n = p.slots * p.D, li = threadIdx.x % p.lpg, per = blockDim.x / p.lpg;
+  for (int g0 = 0; g0 < p.G; g0 += per) {
+    const int g = g0 + threadIdx.x / p.lpg;
+    float a = 0.f, c2 = 0.f;
+    if (g < p.G)
+      for (int c = li; c < p.C; c += p.lpg) {
+        const int d = g * p.C + c;
+        const float w = p.w ? p.w[d] : 1.f;
+        a = __builtin_fmaf(w, red[d], a);
+        c2 = __builtin_fmaf(w, red[n + d], c2);
+      }
+    a = lane_sum(a, p.lpg);
+    c2 = lane_sum(c2, p.lpg);
+    if (g < p.G && li == 0) f(g, a, c2);
+  }
+}
+
+// dx of rows [l0, l1); sA, sB: (Σ t)/n and (Σ t·xh)/n of the item's groups.
+template <typename T, int ACT>
+__device__ __forceinline__ void rows_dx(const NormParams& p, const T* xb, const T* yb, T* ob, int l0, int l1, const NormCol& k,
+                                        const float* sA, const float* sB) {
+  const int slot = threadIdx.x / p.nv, col = threadIdx.x % p.nv;
+  if (slot >= p.slots) return;
+  float ma[8], mb[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) ma[j] = sA[(col * 8 + j) / p.C], mb[j] = sB[(col * 8 + j) / p.C];
+  const int64_t step = (int64_t)p.slots * p.D;
+  int64_t at = (int64_t)(l0 + slot) * p.D + col * 8;
+#pragma unroll 2
+  for (int l = l0 + slot; l < l1; l += p.slots, at += step) {
+    Vec<T, 8> v, dy;
+    v.load(xb + at);
+    dy.load(yb + at);
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float xh = (v.get(j) - k.mu[j]) * k.rs[j];
+      const float t = dy.get(j) * act_d<ACT>(__builtin_fmaf(xh, k.w[j], k.bi[j])) * k.w[j];
+      y[j] = k.rs[j] * (t - ma[j] - xh * mb[j]);
+    }
+    vstore(ob + at, y);
+  }
+}
+
+// One workgroup walks items blockIdx.x, blockIdx.x + gridDim.x, ...; its share of dw and dbias is one row of pc.
+template <typename T, int ACT>
+__global__ void __launch_bounds__(kNormMaxThreads) norm_bwd_item_kernel(const NormParams p) {
+  extern __shared__ float lds[];
+  float* const sA = lds + 2 * p.slots * p.D;
+  float* const sB = sA + p.G;
+  const int slot = threadIdx.x / p.nv, col = threadIdx.x % p.nv;
+  const float inv = 1.0f / ((float)p.L * (float)p.C);
+  float ts[8], tq[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) ts[j] = 0.f, tq[j] = 0.f;
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const int64_t base = (int64_t)b * p.L * p.D;
+    const T* const xb = static_cast<const T*>(p.x) + base;
+    const T* const yb = static_cast<const T*>(p.dout) + base;
+    NormCol k;
+    if (slot < p.slots) k.load(p, b, col);
+    float s[8], q[8];
+    rows_grad_sums<T, ACT>(p, xb, yb, 0, p.L, k, s, q);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ts[j] += s[j], tq[j] += q[j];
+    join_slots(p, s, q, lds);
+    join_grad_groups(p, lds, [&](int g, float a, float c) { sA[g] = a * inv, sB[g] = c * inv; });
+    __syncthreads();
+    rows_dx<T, ACT>(p, xb, yb, static_cast<T*>(p.dx) + base, 0, p.L, k, sA, sB);
+  }
+  if (p.want_dw) {
+    join_slots(p, ts, tq, lds);
+    const int n = p.slots * p.D;
+    for (int c = threadIdx.x; c < p.D; c += blockDim.x) p.pc[(int64_t)blockIdx.x * p.D + c] = make_float2(lds[c], lds[n + c]);
+  }
+}
+
+template <typename T, int ACT>
+__global__ void __launch_bounds__(kNormMaxThreads) norm_bwd_sums_kernel(const NormParams p) {
+  extern __shared__ float lds[];
+  const int b = blockIdx.x / p.chunks, ch = blockIdx.x % p.chunks;
+  const int l0 = ch * p.chunk_len, l1 = min(p.L, l0 + p.chunk_len);
+  const int64_t base = (int64_t)b * p.L * p.D;
+  NormCol k;
+  if (threadIdx.x / p.nv < p.slots) k.load(p, b, threadIdx.x % p.nv);
+  float s[8], q[8];
+  rows_grad_sums<T, ACT>(p, static_cast<const T*>(p.x) + base, static_cast<const T*>(p.dout) + base, l0, l1, k, s, q);
+  join_slots(p, s, q, lds);
+  if (p.want_dw) {
+    const int n = p.slots * p.D;
+    for (int c = threadIdx.x; c < p.D; c += blockDim.x) p.pc[(int64_t)blockIdx.x * p.D + c] = make_float2(lds[c], lds[n + c]);
+  }
+  join_grad_groups(p, lds, [&](int g, float a, float c) { p.pg[(int64_t)blockIdx.x * p.G + g] = make_float2(a, c); });
+}
+
+template <typename T, int ACT>
+__global__ void __launch_bounds__(kNormMaxThreads) norm_bwd_dx_kernel(const NormParams p) {
+  extern __shared__ float lds[];
+  float *const sA = lds, *const sB = lds + p.G;
+  const int b = blockIdx.x / p.chunks, ch = blockIdx.x % p.chunks;
+  const int l0 = ch * p.chunk_len, l1 = min(p.L, l0 + p.chunk_len);
+  const float inv = 1.0f / ((float)p.L * (float)p.C);
+  const float2* const pg = p.pg + (int64_t)b * p.chunks * p.G;
+  const int li = threadIdx.x % p.lpc, per = blockDim.x / p.lpc;
+  for (int g0 = 0; g0 < p.G; g0 += per) {
+    const int g = g0 + threadIdx.x / p.lpc;
+    float a = 0.f, c2 = 0.f;
+    if (g < p.G)
+      for (int c = li; c < p.chunks; c += p.lpc) {
+        const float2 v = pg[(int64_t)c * p.G + g];
+        a += v.x;
+        c2 += v.y;
+      }
+    a = lane_sum(a, p.lpc);
+    c2 = lane_sum(c2, p.lpc);
+    if (g < p.G && li == 0) sA[g] = a * inv, sB[g] = c2 * inv;
+  }
+  __syncthreads();
+  const int64_t base = (int64_t)b * p.L * p.D;
+  NormCol k;
+  if (threadIdx.x / p.nv < p.slots) k.load(p, b, threadIdx.x % p.nv);
+  rows_dx<T, ACT>(p, static_cast<const T*>(p.x) + base, static_cast<const T*>(p.dout) + base, static_cast<T*>(p.dx) + base, l0, l1, k,
+                  sA, sB);
+}
+
+// dbias[d], dweight[d] = Σ over the partial rows: 64 channels a workgroup, 16 threads down the rows of each, joined in a fixed order.
+static __global__ void __launch_bounds__(1024) norm_dw_kernel(const float2* pc, int rows, int D, float* dw, float* db) {
+  __shared__ float2 acc[16][64];
+  const int c = threadIdx.x & 63, t = threadIdx.x >> 6, d = blockIdx.x * 64 + c;
+  float2 s = make_float2(0.f, 0.f);
+  if (d < D) {
+#pragma unroll 4
+    for (int k = t; k < rows; k += 16) {
+      const float2 v = pc[(int64_t)k * D + d];
+      s.x += v.x;
+      s.y += v.y;
+    }
+  }
+  acc[t][c] = s;
+  __syncthreads();
+  if (t == 0 && d < D) {
+#pragma unroll
+    for (int k = 1; k < 16; ++k) s.x += acc[k][c].x, s.y += acc[k][c].y;
+    if (db) db[d] = s.x;
+    if (dw) dw[d] = s.y;
+  }
+}
+
+}  // namespace mscan

@@ -84,3 +84,40 @@ def glr_grads(x, r, i, z, lam, dout, dlast=None, *, scale=8.0, rule="sqrt", reve
 
 
 __all__ = ["rounded", "sigm", "softplus", "glr_ref", "glr_grads", "from_dev", "to_dev"]
+
+
+def act_ref(u, act):
+    """The activation and its derivative, float64."""
+    from scipy.special import ndtr
+    if act == "relu":
+        return np.maximum(u, 0.0), (u > 0).astype(np.float64)
+    if act == "silu":
+        q = sigm(u)
+        return u * q, q * (1 + u * (1 - q))
+    if act == "gelu":
+        return u * ndtr(u), ndtr(u) + u * np.exp(-0.5 * u * u) / np.sqrt(2 * np.pi)
+    return u, np.ones_like(u)
+
+
+def norm_ref(x, G, w, b, act, eps, dout=None):
+    """out, mean, rstd and, for dout, the gradients."""
+    B, L, D = x.shape
+    v = x.reshape(B, L, G, D // G)
+    mean = v.mean((1, 3))
+    var = ((v - mean[:, None, :, None]) ** 2).mean((1, 3))
+    rstd = 1 / np.sqrt(var + eps)
+    xh = ((v - mean[:, None, :, None]) * rstd[:, None, :, None]).reshape(B, L, D)
+    w = np.ones(D) if w is None else w
+    b = np.zeros(D) if b is None else b
+    y, dy = act_ref(xh * w + b, act)
+    if dout is None:
+        return y, mean, rstd
+    du = dout * dy
+    t = (du * w).reshape(B, L, G, D // G)
+    xg = xh.reshape(B, L, G, D // G)
+    m1, m2 = t.mean((1, 3), keepdims=True), (t * xg).mean((1, 3), keepdims=True)
+    dx = rstd[:, None, :, None] * (t - m1 - xg * m2)
+    return y, mean, rstd, dict(dx=dx.reshape(B, L, D), dweight=(du * xh).sum((0, 1)), dbias=du.sum((0, 1)))
+
+
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}

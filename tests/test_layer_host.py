@@ -120,3 +120,69 @@ def test_glr_reference_gradients_against_differences(rule, with_lam, reverse):
         num = (loss(dict(v, **{k: v[k] + eps * d})) - loss(dict(v, **{k: v[k] - eps * d}))) / (2 * eps)
         want = (g["d" + k] * d).sum()
         assert abs(num - want) <= 1e-7 * max(1.0, abs(want)), (k, num, want)
+
+
+def norm_dims(**kw):
+    base = dict(batch=2, seqlen=100, dim=64, groups=8, dtype=ms.DTYPE_BF16)
+    base.update(kw)
+    return ms.make_norm_dims(base.pop("batch"), base.pop("seqlen"), base.pop("dim"), base.pop("groups"),
+                             base.pop("dtype"), **base)
+
+
+def test_norm_sizes(lib):
+    assert ms.group_norm_fwd_workspace_bytes(norm_dims(seqlen=1)) == 0
+    assert ms.group_norm_fwd_workspace_bytes(norm_dims(seqlen=100000)) > 0
+    assert ms.group_norm_bwd_workspace_bytes(norm_dims(seqlen=1)) >= 2 * 64 * 8
+    for bad in (dict(batch=0), dict(seqlen=0), dict(dim=0), dict(groups=0), dict(groups=7), dict(dim=60, groups=4),
+                dict(dim=8200, groups=1), dict(act=4), dict(act=-1), dict(dtype=3), dict(eps=-1.0),
+                dict(eps=float("nan")), dict(eps=float("inf")), dict(seqlen=1 << 31), dict(batch=1 << 31)):
+        for query in (ms.group_norm_fwd_workspace_bytes, ms.group_norm_bwd_workspace_bytes):
+            with pytest.raises(ms.MambaError):
+                query(norm_dims(**bad))
+
+
+def test_norm_refusals(lib):
+    def fwd(d, x=FAKE, w=None, b=None, out=FAKE, mean=None):
+        return lib.mamba_group_norm_fwd(x, w, b, ctypes.byref(d), out, mean, None, None)
+
+    assert fwd(norm_dims(), x=None) == E.MAMBA_ERR_INVALID
+    assert fwd(norm_dims(), out=None) == E.MAMBA_ERR_INVALID
+    assert fwd(norm_dims(groups=7)) == E.MAMBA_ERR_INVALID
+    assert fwd(norm_dims(dim=60, groups=4)) == E.MAMBA_ERR_UNSUPPORTED
+    assert fwd(norm_dims(), x=FAKE + 8) == E.MAMBA_ERR_UNSUPPORTED
+    assert fwd(norm_dims(), out=FAKE + 2) == E.MAMBA_ERR_UNSUPPORTED
+    assert fwd(norm_dims(), w=FAKE + 2) == E.MAMBA_ERR_UNSUPPORTED
+    assert fwd(norm_dims(), mean=FAKE + 1) == E.MAMBA_ERR_UNSUPPORTED
+    assert fwd(norm_dims(seqlen=100000)) == E.MAMBA_ERR_WORKSPACE
+    need = ms.group_norm_fwd_workspace_bytes(norm_dims(seqlen=100000))
+    assert fwd(norm_dims(seqlen=100000, workspace=FAKE, workspace_bytes=need - 1)) == E.MAMBA_ERR_WORKSPACE
+    assert lib.mamba_group_norm_fwd(FAKE, None, None, None, FAKE, None, None, None) == E.MAMBA_ERR_INVALID
+
+    def bwd(d, **kw):
+        p = dict(x=FAKE, dout=FAKE, mean=FAKE, rstd=FAKE, dx=FAKE)
+        p.update(kw)
+        return lib.mamba_group_norm_bwd(p["x"], None, None, p["dout"], p["mean"], p["rstd"], ctypes.byref(d), p["dx"],
+                                        None, None, None)
+
+    for miss in ("x", "dout", "mean", "rstd", "dx"):
+        assert bwd(norm_dims(), **{miss: None}) == E.MAMBA_ERR_INVALID
+    for odd in ("x", "dout", "dx"):
+        assert bwd(norm_dims(), **{odd: FAKE + 8}) == E.MAMBA_ERR_UNSUPPORTED
+    assert bwd(norm_dims()) == E.MAMBA_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu"])
+def test_norm_reference_gradients_against_differences(act):
+    from layerutil import norm_ref
+    r = np.random.Generator(np.random.PCG64(4))
+    B, L, D, G = 2, 5, 12, 3
+    v = dict(x=r.standard_normal((B, L, D)), w=r.standard_normal(D), b=r.standard_normal(D))
+    dout = r.standard_normal((B, L, D))
+    g = norm_ref(v["x"], G, v["w"], v["b"], act, 1e-5, dout)[3]
+    for k, gk in (("x", "dx"), ("w", "dweight"), ("b", "dbias")):
+        d = r.standard_normal(v[k].shape)
+        eps = 1e-6 if act == "relu" else 1e-5
+        f = lambda s: (norm_ref(**{**{"G": G, "act": act, "eps": 1e-5}, **v, k: v[k] + s * d})[0] * dout).sum()  # noqa: E731
+        num = (f(eps) - f(-eps)) / (2 * eps)
+        want = (g[gk] * d).sum()
+        assert abs(num - want) <= 1e-6 * max(1.0, abs(want)), (k, num, want)
