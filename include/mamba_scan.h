@@ -409,6 +409,49 @@ MAMBA_API int mamba_group_norm_bwd(const void* x, const float* weight, const flo
                                    const float* mean, const float* rstd, const mamba_norm_dims* dims, void* dx,
                                    float* dweight, float* dbias, hipStream_t stream);
 
+/* ---- Matrix product with bias, activation and residual ----
+ *
+ *   pre = x·Wᵀ + bias,  out = act(pre) + residual
+ * Sums, bias, activation and residual are taken in float32 and rounded once. */
+typedef struct {
+  int64_t rows;    /* M >= 1: rows of x (tokens) */
+  int64_t in_dim;  /* K >= 1, a multiple of 8 */
+  int64_t out_dim; /* N >= 1, a multiple of 8 */
+  int32_t dtype;   /* mamba_dtype of x, weight, residual, out, pre and the gradients but dbias */
+  int32_t act;     /* mamba_act */
+  void* workspace; /* device scratch owned by the caller (may be NULL when the query returns 0) */
+  size_t workspace_bytes;
+} mamba_linear_dims;
+
+/* Bytes of workspace; pure functions of the sizes, (size_t)-1 when the
+ * arguments are invalid or unsupported.  The contents need not be initialised. */
+MAMBA_API size_t mamba_linear_fwd_workspace_bytes(const mamba_linear_dims* dims);
+MAMBA_API size_t mamba_linear_bwd_workspace_bytes(const mamba_linear_dims* dims);
+
+/*
+ * Forward.  x [M][K], weight [N][K], out [M][N] dtype; bias [N] float32 or
+ * NULL; residual [M][N] dtype or NULL, which may be out itself; pre [M][N]
+ * dtype or NULL: written for the backward of an activation.  No other output
+ * may alias an input.  Errors: MAMBA_ERR_INVALID (NULL x, weight or out, a
+ * size <= 0, unknown dtype or act), MAMBA_ERR_UNSUPPORTED (K or N not a
+ * multiple of 8 or above 2^20, M above 2^29, a pointer not 16-byte aligned),
+ * MAMBA_ERR_WORKSPACE, MAMBA_ERR_HIP.
+ */
+MAMBA_API int mamba_linear_fwd(const void* x, const void* weight, const float* bias, const void* residual,
+                               const mamba_linear_dims* dims, void* out, void* pre, hipStream_t stream);
+
+/*
+ * Backward for dout [M][N] dtype: dx [M][K] and dweight [N][K] dtype, dbias
+ * [N] float32; each may be NULL (not computed), not all three.  weight is read
+ * for dx, x for dweight, and pre (of the forward) with an activation.  The
+ * residual's gradient is dout itself.  dout·act'(pre) is rounded to dtype
+ * before the products; dbias sums it unrounded.  Sums run in a fixed order.
+ * No output may alias an input.  Errors as for mamba_linear_fwd.
+ */
+MAMBA_API int mamba_linear_bwd(const void* x, const void* weight, const void* pre, const void* dout,
+                               const mamba_linear_dims* dims, void* dx, void* dweight, float* dbias,
+                               hipStream_t stream);
+
 /* Static, human-readable text for a status code (never NULL). */
 MAMBA_API const char* mamba_status_string(int status);
 

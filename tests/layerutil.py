@@ -121,3 +121,14 @@ def norm_ref(x, G, w, b, act, eps, dout=None):
 
 
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+
+
+def linear_ref(x, w, b, res, act, dout=None):
+    """out, pre and, for dout, the gradients."""
+    pre = x @ w.T + (0.0 if b is None else b)
+    y, dy = act_ref(pre, act)
+    out = y if res is None else y + res
+    if dout is None:
+        return out, pre
+    dp = dout * dy
+    return out, pre, dict(dx=dp @ w, dweight=dp.T @ x, dbias=dp.sum(0))

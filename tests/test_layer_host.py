@@ -186,3 +186,68 @@ def test_norm_reference_gradients_against_differences(act):
         num = (f(eps) - f(-eps)) / (2 * eps)
         want = (g[gk] * d).sum()
         assert abs(num - want) <= 1e-6 * max(1.0, abs(want)), (k, num, want)
+
+
+def linear_dims(**kw):
+    base = dict(rows=100, in_dim=64, out_dim=32, dtype=ms.DTYPE_BF16)
+    base.update(kw)
+    return ms.make_linear_dims(base.pop("rows"), base.pop("in_dim"), base.pop("out_dim"), base.pop("dtype"), **base)
+
+
+def test_linear_sizes(lib):
+    assert ms.linear_fwd_workspace_bytes(linear_dims()) == 0
+    assert ms.linear_fwd_workspace_bytes(linear_dims(rows=8, in_dim=65536)) == 0  # few rows: no scratch
+    assert ms.linear_fwd_workspace_bytes(linear_dims(rows=200, in_dim=65536)) > 0  # split contraction
+    assert ms.linear_bwd_workspace_bytes(linear_dims(act=ms.ACT_SILU)) > 100 * 32 * 2
+    for bad in (dict(rows=0), dict(in_dim=0), dict(out_dim=-8), dict(in_dim=12), dict(out_dim=20), dict(dtype=2),
+                dict(act=4), dict(in_dim=(1 << 20) + 8), dict(out_dim=(1 << 20) + 8), dict(rows=(1 << 29) + 1)):
+        for query in (ms.linear_fwd_workspace_bytes, ms.linear_bwd_workspace_bytes):
+            with pytest.raises(ms.MambaError):
+                query(linear_dims(**bad))
+
+
+def test_linear_refusals(lib):
+    def fwd(d, x=FAKE, w=FAKE, b=None, res=None, out=FAKE, pre=None):
+        return lib.mamba_linear_fwd(x, w, b, res, ctypes.byref(d), out, pre, None)
+
+    for miss in ("x", "w", "out"):
+        assert fwd(linear_dims(), **{miss: None}) == E.MAMBA_ERR_INVALID
+    assert fwd(linear_dims(act=-1)) == E.MAMBA_ERR_INVALID
+    assert fwd(linear_dims(in_dim=4)) == E.MAMBA_ERR_UNSUPPORTED
+    for odd in ("x", "w", "res", "out", "pre"):
+        assert fwd(linear_dims(), **{odd: FAKE + 8}) == E.MAMBA_ERR_UNSUPPORTED
+    assert fwd(linear_dims(), b=FAKE + 2) == E.MAMBA_ERR_UNSUPPORTED
+    assert fwd(linear_dims(rows=200, in_dim=65536)) == E.MAMBA_ERR_WORKSPACE
+    assert lib.mamba_linear_fwd(FAKE, FAKE, None, None, None, FAKE, None, None) == E.MAMBA_ERR_INVALID
+
+    def bwd(d, **kw):
+        p = dict(x=FAKE, w=FAKE, pre=None, dout=FAKE, dx=FAKE, dw=FAKE, db=FAKE)
+        p.update(kw)
+        return lib.mamba_linear_bwd(p["x"], p["w"], p["pre"], p["dout"], ctypes.byref(d), p["dx"], p["dw"], p["db"],
+                                    None)
+
+    for miss in ("x", "w", "dout"):
+        assert bwd(linear_dims(), **{miss: None}) == E.MAMBA_ERR_INVALID
+    assert bwd(linear_dims(), dx=None, dw=None, db=None) == E.MAMBA_ERR_INVALID
+    assert bwd(linear_dims(act=ms.ACT_GELU)) == E.MAMBA_ERR_INVALID  # no pre
+    assert bwd(linear_dims(), dw=FAKE + 8) == E.MAMBA_ERR_UNSUPPORTED
+    assert bwd(linear_dims()) == E.MAMBA_ERR_WORKSPACE
+    need = ms.linear_bwd_workspace_bytes(linear_dims())
+    assert bwd(linear_dims(workspace=FAKE, workspace_bytes=need - 1)) == E.MAMBA_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu"])
+def test_linear_reference_gradients_against_differences(act):
+    from layerutil import linear_ref
+    r = np.random.Generator(np.random.PCG64(14))
+    v = dict(x=r.standard_normal((5, 12)), w=r.standard_normal((7, 12)), b=r.standard_normal(7))
+    dout = r.standard_normal((5, 7))
+    pre, g = linear_ref(v["x"], v["w"], v["b"], None, act, dout)[1:]
+    eps = 1e-6
+    assert np.abs(pre).min() > 100 * eps  # no step crosses relu's kink
+    for k, gk in (("x", "dx"), ("w", "dweight"), ("b", "dbias")):
+        d = r.standard_normal(v[k].shape)
+        f = lambda s: (linear_ref(**{"res": None, "act": act, **v, k: v[k] + s * d})[0] * dout).sum()  # noqa: E731
+        num = (f(eps) - f(-eps)) / (2 * eps)
+        want = (g[gk] * d).sum()
+        assert abs(num - want) <= 1e-6 * max(1.0, abs(want)), (k, num, want)
