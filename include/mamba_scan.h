@@ -417,7 +417,7 @@ typedef struct {
   int64_t rows;    /* M >= 1: rows of x (tokens) */
   int64_t in_dim;  /* K >= 1, a multiple of 8 */
   int64_t out_dim; /* N >= 1, a multiple of 8 */
-  int32_t dtype;   /* mamba_dtype of x, weight, residual, out, pre and the gradients but dbias */
+  int32_t dtype;   /* mamba_dtype of x, weight, residual, out, dout, dx and dweight */
   int32_t act;     /* mamba_act */
   void* workspace; /* device scratch owned by the caller (may be NULL when the query returns 0) */
   size_t workspace_bytes;
@@ -431,14 +431,14 @@ MAMBA_API size_t mamba_linear_bwd_workspace_bytes(const mamba_linear_dims* dims)
 /*
  * Forward.  x [M][K], weight [N][K], out [M][N] dtype; bias [N] float32 or
  * NULL; residual [M][N] dtype or NULL, which may be out itself; pre [M][N]
- * dtype or NULL: written for the backward of an activation.  No other output
+ * float32 or NULL: written for the backward of an activation.  No other output
  * may alias an input.  Errors: MAMBA_ERR_INVALID (NULL x, weight or out, a
  * size <= 0, unknown dtype or act), MAMBA_ERR_UNSUPPORTED (K or N not a
  * multiple of 8 or above 2^20, M above 2^29, a pointer not 16-byte aligned),
  * MAMBA_ERR_WORKSPACE, MAMBA_ERR_HIP.
  */
 MAMBA_API int mamba_linear_fwd(const void* x, const void* weight, const float* bias, const void* residual,
-                               const mamba_linear_dims* dims, void* out, void* pre, hipStream_t stream);
+                               const mamba_linear_dims* dims, void* out, float* pre, hipStream_t stream);
 
 /*
  * Backward for dout [M][N] dtype: dx [M][K] and dweight [N][K] dtype, dbias
@@ -448,7 +448,7 @@ MAMBA_API int mamba_linear_fwd(const void* x, const void* weight, const float* b
  * before the products; dbias sums it unrounded.  Sums run in a fixed order.
  * No output may alias an input.  Errors as for mamba_linear_fwd.
  */
-MAMBA_API int mamba_linear_bwd(const void* x, const void* weight, const void* pre, const void* dout,
+MAMBA_API int mamba_linear_bwd(const void* x, const void* weight, const float* pre, const void* dout,
                                const mamba_linear_dims* dims, void* dx, void* dweight, float* dbias,
                                hipStream_t stream);
 

@@ -55,8 +55,8 @@ def linear_fwd(x, weight, bias=None, residual=None, *, act=ACT_NONE, out=None, p
                workspace=None, stream=None):
     """mamba_linear_fwd on torch tensors: x [..., K], weight [N][K], bias [N]
     float32, residual and out [..., N] (out may be residual).  Returns (out,
-    pre); pre is the product before the activation, which linear_bwd takes
-    (None unless want_pre or a buffer for it is given)."""
+    pre); pre is the product before the activation, [..., N] float32, which
+    linear_bwd takes (None unless want_pre or a buffer for it is given)."""
     import torch
     ts = _b._foreign_stream(stream)
     if ts is not None:
@@ -71,9 +71,9 @@ def linear_fwd(x, weight, bias=None, residual=None, *, act=ACT_NONE, out=None, p
     workspace = _workspace(dims, linear_fwd_workspace_bytes(dims), workspace, dev)
     out = torch.empty(shape, dtype=x.dtype, device=dev) if out is None else out
     if pre is None and want_pre:
-        pre = torch.empty(shape, dtype=x.dtype, device=dev)
+        pre = torch.empty(shape, dtype=torch.float32, device=dev)
     _b._check(out, "out", shape, x.dtype, dev)
-    _b._check(pre, "pre", shape, x.dtype, dev)
+    _b._check(pre, "pre", shape, torch.float32, dev)
     rc = lib.mamba_linear_fwd(_b._ptr(x), _b._ptr(weight), _b._ptr(bias), _b._ptr(residual), ctypes.byref(dims),
                               _b._ptr(out), _b._ptr(pre), _b._stream(stream))
     if rc != _b.MAMBA_OK:
@@ -95,7 +95,7 @@ def linear_bwd(x, weight, *, dout, pre=None, act=ACT_NONE, want_dx=True, want_dw
     lib = _b.load_library()
     M, K, N, shape, dt, dev = _check_inputs(x, weight)
     _b._check(dout, "dout", shape, x.dtype, dev)
-    _b._check(pre, "pre", shape, x.dtype, dev)
+    _b._check(pre, "pre", shape, torch.float32, dev)
     dims = make_linear_dims(M, K, N, dt, act=act)
     workspace = _workspace(dims, linear_bwd_workspace_bytes(dims), workspace, dev)
     g = dict(dx=torch.empty_like(x) if want_dx else None, dweight=torch.empty_like(weight) if want_dweight else None,

@@ -32,4 +32,22 @@ __device__ __forceinline__ float act_d(float u) {
   return 1.f;
 }
 
+// The same with the activation known at run time (one for the whole launch).
+__device__ __forceinline__ float act_any(float u, int act) {
+  switch (act) {
+    case ACT_RELU: return act_f<ACT_RELU>(u);
+    case ACT_SILU: return act_f<ACT_SILU>(u);
+    case ACT_GELU: return act_f<ACT_GELU>(u);
+    default: return u;
+  }
+}
+__device__ __forceinline__ float act_d_any(float u, int act) {
+  switch (act) {
+    case ACT_RELU: return act_d<ACT_RELU>(u);
+    case ACT_SILU: return act_d<ACT_SILU>(u);
+    case ACT_GELU: return act_d<ACT_GELU>(u);
+    default: return 1.f;
+  }
+}
+
 }  // namespace mscan

@@ -166,7 +166,7 @@ int mamba_glr_bwd(const void* x, const void* r, const void* i, const void* z, co
   if (e != hipSuccess) return MAMBA_ERR_HIP;
   if (p.dlam_part) {
     const int64_t rows = (int64_t)p.B * (pl.bwd_chain ? pl.bwd_tiles : 1);
-    glr_dlam_kernel<<<(unsigned)((p.D + 63) / 64), 1024, 0, stream>>>(part, rows, p.D, p.scale, lam, dlam);
+    colsum_kernel<float><<<(unsigned)((p.D + 15) / 16), 1024, 0, stream>>>(part, rows, p.D, DlamStore{dlam, lam, p.scale});
     if (hipGetLastError() != hipSuccess) return MAMBA_ERR_HIP;
   }
   return MAMBA_OK;

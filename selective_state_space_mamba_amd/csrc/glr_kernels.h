@@ -24,6 +24,7 @@
 // registers between the composition and the second sweep over its positions.
 #pragma once
 
+#include "colsum.h"
 #include "device_math.h"
 
 namespace mscan {
@@ -625,25 +626,13 @@ __global__ void __launch_bounds__(kGlrThreads) glr_bwd_kernel(const GlrParams p)
   }
 }
 
-// dlam[d] = scale·sigmoid(lam_d)·Σ over the partial rows: 64 channels a
-// workgroup, 16 threads down the rows of each, joined in a fixed order.
-static __global__ void __launch_bounds__(1024) glr_dlam_kernel(const float* part, int64_t rows, int D, float scale, const float* lam,
-                                                               float* dlam) {
-  __shared__ float acc[16][64];
-  const int c = threadIdx.x & 63, t = threadIdx.x >> 6, d = blockIdx.x * 64 + c;
-  float s = 0.f;
-  if (d < D) {
-#pragma unroll 4
-    for (int64_t k = t; k < rows; k += 16) s += part[k * D + d];
-  }
-  acc[t][c] = s;
-  __syncthreads();
-  if (t == 0 && d < D) {
-#pragma unroll
-    for (int k = 1; k < 16; ++k) s += acc[k][c];
-    dlam[d] = scale * sigm(lam[d]) * s;
-  }
-}
+// dlam[d] = scale·sigmoid(lam_d)·Σ over the partial rows.
+struct DlamStore {
+  float* dlam;
+  const float* lam;
+  float scale;
+  __device__ __forceinline__ void operator()(int d, float s) const { dlam[d] = scale * sigm(lam[d]) * s; }
+};
 
 // Clears the chain's words and its ticket (a kernel, so that it can be recorded in a graph).
 static __global__ void __launch_bounds__(256) glr_clear_kernel(uint4* p, int64_t n) {

@@ -17,6 +17,11 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 constexpr int kRowsMax = 64;  // rows that linear_rows_kernel takes
 
+#ifndef MSCAN_LINEAR_TILE
+#define MSCAN_LINEAR_TILE 128, 128, 2, 2
+#endif
+constexpr int kTile[4] = {MSCAN_LINEAR_TILE};
+
 #ifndef MSCAN_LINEAR_WGS
 #define MSCAN_LINEAR_WGS 512  // workgroups wanted before a contraction is left whole
 #endif
@@ -30,7 +35,7 @@ struct ProductPlan {
 ProductPlan plan_product(int64_t M, int64_t N, int64_t K, bool bf16) {
   ProductPlan pl;
   const int bk = bf16 ? 64 : 32;
-  pl.bm = pl.bn = 128;
+  pl.bm = kTile[0], pl.bn = kTile[1];
   pl.tiles_m = ceil_div(M, pl.bm);
   pl.tiles_n = ceil_div(N, pl.bn);
   const int64_t tiles = (int64_t)pl.tiles_m * pl.tiles_n;
@@ -85,7 +90,7 @@ hipError_t product(LinearParams p, const ProductPlan& pl, hipStream_t stream) {
   p.tiles_m = pl.tiles_m, p.tiles_n = pl.tiles_n, p.splits = pl.splits, p.kt_per_split = pl.kt_per_split;
   if (pl.splits == 1) p.part = nullptr;
   const dim3 grid((unsigned)((int64_t)pl.tiles_m * pl.tiles_n), (unsigned)pl.splits);
-  linear_tile_kernel<T, TA, TB, 128, 128, 2, 2><<<grid, 256, 0, stream>>>(p);
+  linear_tile_kernel<T, TA, TB, MSCAN_LINEAR_TILE><<<grid, 64 * kTile[2] * kTile[3], 0, stream>>>(p);
   if (pl.splits > 1) {
     const int64_t quads = (int64_t)p.M * p.N / 4;
     linear_join_kernel<T><<<(unsigned)((quads + 255) / 256), 256, 0, stream>>>(p);
@@ -138,7 +143,7 @@ size_t mamba_linear_bwd_workspace_bytes(const mamba_linear_dims* dims) {
 }
 
 int mamba_linear_fwd(const void* x, const void* weight, const float* bias, const void* residual, const mamba_linear_dims* dims,
-                     void* out, void* pre, hipStream_t stream) {
+                     void* out, float* pre, hipStream_t stream) {
   if (!x || !weight || !out) return MAMBA_ERR_INVALID;
   const int rc = check(dims);
   if (rc != MAMBA_OK) return rc;
@@ -157,13 +162,13 @@ int mamba_linear_fwd(const void* x, const void* weight, const float* bias, const
   return e == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
 }
 
-int mamba_linear_bwd(const void* x, const void* weight, const void* pre, const void* dout, const mamba_linear_dims* dims, void* dx,
+int mamba_linear_bwd(const void* x, const void* weight, const float* pre, const void* dout, const mamba_linear_dims* dims, void* dx,
                      void* dweight, float* dbias, hipStream_t stream) {
   if (!dout || (dx && !weight) || (dweight && !x) || (!dx && !dweight && !dbias)) return MAMBA_ERR_INVALID;
   const int rc = check(dims);
   if (rc != MAMBA_OK) return rc;
   if (dims->act != MAMBA_ACT_NONE && !pre) return MAMBA_ERR_INVALID;
-  for (const void* q : {x, weight, pre, dout, (const void*)dx, (const void*)dweight, (const void*)dims->workspace})
+  for (const void* q : {x, weight, (const void*)pre, dout, (const void*)dx, (const void*)dweight, (const void*)dims->workspace})
     if (!aligned(q, 16)) return MAMBA_ERR_UNSUPPORTED;
   if (!aligned(dbias, 4)) return MAMBA_ERR_UNSUPPORTED;
   if (!dims->workspace || dims->workspace_bytes < mamba_linear_bwd_workspace_bytes(dims)) return MAMBA_ERR_WORKSPACE;
@@ -179,7 +184,7 @@ int mamba_linear_bwd(const void* x, const void* weight, const void* pre, const v
     g.M = (int)dims->rows, g.N = (int)dims->out_dim, g.chunk = gp.chunk;
     e = bf16 ? grad<uint16_t>(g, dims->act, (unsigned)gp.chunks, stream) : grad<float>(g, dims->act, (unsigned)gp.chunks, stream);
     if (e == hipSuccess && dbias) {
-      linear_dbias_kernel<<<(unsigned)((g.N + 63) / 64), 1024, 0, stream>>>(g.part, gp.chunks, g.N, dbias);
+      colsum_kernel<float><<<(unsigned)((g.N + 15) / 16), 1024, 0, stream>>>(g.part, gp.chunks, g.N, ColStore{dbias, nullptr});
       e = hipGetLastError();
     }
   }

@@ -17,6 +17,7 @@
 #pragma once
 
 #include "act_math.h"
+#include "colsum.h"
 
 namespace mscan {
 
@@ -34,19 +35,10 @@ struct LinearParams {
   const float* bias;     // [N] or null
   const void* residual;  // [M][N] or null
   void* out;             // [M][N]
-  void* pre;             // [M][N] or null
+  float* pre;            // [M][N] or null
   float* part;           // [splits][M][N] or null: sums of a share of the contraction
   int act, splits, kt_per_split, tiles_m, tiles_n;
 };
-
-__device__ __forceinline__ float act_any(float u, int act) {
-  switch (act) {
-    case ACT_RELU: return act_f<ACT_RELU>(u);
-    case ACT_SILU: return act_f<ACT_SILU>(u);
-    case ACT_GELU: return act_f<ACT_GELU>(u);
-    default: return u;
-  }
-}
 
 // One output quadruple: columns n..n+3 of row m.
 template <typename T>
@@ -56,7 +48,7 @@ __device__ __forceinline__ void linear_finish(const LinearParams& p, int m, int 
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] += p.bias[n + j];
   }
-  if (p.pre) storeV<4>(static_cast<T*>(p.pre) + at, v);
+  if (p.pre) storeV<4>(p.pre + at, v);
   if (p.act != ACT_NONE) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = act_any(v[j], p.act);
@@ -315,9 +307,13 @@ __global__ void __launch_bounds__(512) linear_rows_kernel(const LinearParams p) 
 // ---- backward's first pass ----
 // dP = dout·act'(pre), rounded to the element type (the matrix instructions
 // take no wider operand; it adds one rounding of 2^-9 a term in bf16), and the
-// column sums of the unrounded dP over a run of rows.
+// column sums of the unrounded dP over a run of rows.  pre is float32: rounded
+// to bf16 it would put 2^-9 of error into act'(pre), and with it 3e-3 into
+// dbias, which is a float32 sum; it costs 2 bytes more an output, written and
+// read once.
 struct LinearGradParams {
-  const void *dout, *pre;  // [M][N]; pre null without activation
+  const void* dout;        // [M][N]
+  const float* pre;        // [M][N]; null without activation
   void* dp;                // [M][N] or null
   float* part;             // [chunks][N] or null
   int M, N, chunk;
@@ -336,9 +332,10 @@ __global__ void __launch_bounds__(256) linear_grad_kernel(const LinearGradParams
 #pragma unroll 4
     for (int m = m0 + wave; m < m1; m += 4) {
       const int64_t at = (int64_t)m * p.N + n;
-      Vec<T, 8> dy, u;
+      Vec<T, 8> dy;
+      Vec<float, 8> u;
       dy.load(static_cast<const T*>(p.dout) + at);
-      if constexpr (ACT != ACT_NONE) u.load(static_cast<const T*>(p.pre) + at);
+      if constexpr (ACT != ACT_NONE) u.load(p.pre + at);
       float v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -357,23 +354,6 @@ __global__ void __launch_bounds__(256) linear_grad_kernel(const LinearGradParams
       const int col = blockIdx.x * 512 + c;
       if (col < p.N) p.part[(int64_t)blockIdx.y * p.N + col] = ((red[0][c] + red[1][c]) + red[2][c]) + red[3][c];
     }
-  }
-}
-
-static __global__ void __launch_bounds__(1024) linear_dbias_kernel(const float* part, int rows, int N, float* db) {
-  __shared__ float acc[16][64];
-  const int c = threadIdx.x & 63, t = threadIdx.x >> 6, n = blockIdx.x * 64 + c;
-  float s = 0.f;
-  if (n < N) {
-#pragma unroll 4
-    for (int k = t; k < rows; k += 16) s += part[(int64_t)k * N + n];
-  }
-  acc[t][c] = s;
-  __syncthreads();
-  if (t == 0 && n < N) {
-#pragma unroll
-    for (int k = 1; k < 16; ++k) s += acc[k][c];
-    db[n] = s;
   }
 }
 

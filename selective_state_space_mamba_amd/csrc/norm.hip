@@ -28,7 +28,38 @@ int pow2_at_least(int n) {
 struct NormPlan {
   int nv, threads, slots, chunks, chunk_len, bwd_rows;
   size_t lds, pg, pc;  // bytes
+  int v, nvec, lanes;  // single tokens: vector width, vectors a lane, lanes a group (v = 0: not this way)
+  int64_t stride;      // and the backward's lane groups
 };
+
+#ifndef MSCAN_NORM_ROW_WAVES
+#define MSCAN_NORM_ROW_WAVES 4096  // waves of the single-token backward, each with partial sums of its own
+#endif
+
+// Single tokens: groups as rows in registers, up to 16 vectors of 8 values or
+// 4 of fewer (a group that is no multiple of 8 values starts at any of them).
+void row_plan(const mamba_norm_dims* g, NormPlan* pl) {
+  pl->v = 0;
+  if (g->seqlen != 1) return;
+  const int C = (int)(g->dim / g->groups);
+  const int v = C % 8 == 0 ? 8 : C % 4 == 0 ? 4 : C % 2 == 0 ? 2 : 1;
+  const int vecs = C / v;
+  pl->lanes = pow2_at_least(vecs < 64 ? vecs : 64);
+  int nvec = pow2_at_least((vecs + pl->lanes - 1) / pl->lanes);
+  if (v < 8 && nvec > 1) nvec = 4;
+  if ((v == 8 && nvec > 16) || (v < 8 && vecs > 4 * pl->lanes)) return;
+  pl->v = v;
+  pl->nvec = nvec;
+  const int64_t rows = g->batch * g->groups;
+  int64_t s = (int64_t)MSCAN_NORM_ROW_WAVES * 64 / pl->lanes;
+  if (s > rows) s = rows;
+  s = (s + g->groups - 1) / g->groups * g->groups;
+  pl->stride = s;
+  if (nvec <= 4) {
+    pl->bwd_rows = (int)(s / g->groups);
+    pl->pc = up256((size_t)pl->bwd_rows * g->dim * sizeof(float2));
+  }
+}
 
 // Validates the sizes and derives the launch plan; a pure function of dims.
 int norm_plan(const mamba_norm_dims* g, NormPlan* pl) {
@@ -54,11 +85,13 @@ int norm_plan(const mamba_norm_dims* g, NormPlan* pl) {
   const int64_t len = (g->seqlen + chunks - 1) / chunks;
   pl->chunk_len = (int)len;
   pl->chunks = (int)((g->seqlen + len - 1) / len);
-  if (g->batch * pl->chunks > INT32_MAX) return MAMBA_ERR_UNSUPPORTED;
+  if (g->batch * pl->chunks > INT32_MAX || g->batch * g->groups > ((int64_t)1 << 32)) return MAMBA_ERR_UNSUPPORTED;
   pl->bwd_rows = (int)(pl->chunks > 1 ? g->batch * pl->chunks : g->batch < 2 * MSCAN_NORM_BLOCKS ? g->batch : 2 * MSCAN_NORM_BLOCKS);
   pl->lds = ((size_t)2 * pl->slots * g->dim + 2 * g->groups) * sizeof(float);
   pl->pg = pl->chunks > 1 ? up256((size_t)g->batch * pl->chunks * g->groups * sizeof(float2)) : 0;
   pl->pc = up256((size_t)pl->bwd_rows * g->dim * sizeof(float2));
+  row_plan(g, pl);
+  if (pl->v > 0) pl->chunks = 1, pl->chunk_len = 1, pl->pg = 0;
   return MAMBA_OK;
 }
 
@@ -82,6 +115,35 @@ void by_type_act(const mamba_norm_dims* g, F f) {
   };
   if (g->dtype == MAMBA_DTYPE_BF16) by_act((uint16_t*)nullptr);
   else by_act((float*)nullptr);
+}
+
+template <typename F>
+void by_row_shape(const mamba_norm_dims* g, const NormPlan& pl, F f) {
+  auto by_v = [&](auto* t) {
+    auto c = [](auto i) { return i; };
+    using std::integral_constant;
+    auto small = [&](auto v) {
+      if (pl.nvec == 1) f(t, v, c(integral_constant<int, 1>{}));
+      else f(t, v, c(integral_constant<int, 4>{}));
+    };
+    if (pl.v == 1) small(integral_constant<int, 1>{});
+    else if (pl.v == 2) small(integral_constant<int, 2>{});
+    else if (pl.v == 4) small(integral_constant<int, 4>{});
+    else if (pl.nvec == 1) f(t, integral_constant<int, 8>{}, integral_constant<int, 1>{});
+    else if (pl.nvec == 2) f(t, integral_constant<int, 8>{}, integral_constant<int, 2>{});
+    else if (pl.nvec == 4) f(t, integral_constant<int, 8>{}, integral_constant<int, 4>{});
+    else if (pl.nvec == 8) f(t, integral_constant<int, 8>{}, integral_constant<int, 8>{});
+    else f(t, integral_constant<int, 8>{}, integral_constant<int, 16>{});
+  };
+  if (g->dtype == MAMBA_DTYPE_BF16) by_v((uint16_t*)nullptr);
+  else by_v((float*)nullptr);
+}
+
+NormRowParams row_params(const mamba_norm_dims* g, const NormPlan& pl) {
+  NormRowParams r{};
+  r.rows = g->batch * g->groups, r.stride = pl.stride;
+  r.C = (int)(g->dim / g->groups), r.G = (int)g->groups, r.lanes = pl.lanes, r.act = g->act, r.eps = g->eps;
+  return r;
 }
 
 // Group statistics (and, where an item is one workgroup's, the channel sums) can
@@ -121,6 +183,16 @@ int mamba_group_norm_fwd(const void* x, const float* weight, const float* bias, 
   norm_params(dims, pl, &p);
   p.x = x, p.w = weight, p.bias = bias, p.out = out, p.mean = mean, p.rstd = rstd;
   p.pg = static_cast<float2*>(dims->workspace);
+  if (pl.v > 0) {
+    NormRowParams r = row_params(dims, pl);
+    r.x = x, r.w = weight, r.bias = bias, r.out = out, r.mean = mean, r.rstd = rstd;
+    by_row_shape(dims, pl, [&](auto* t, auto v, auto nv) {
+      using T = std::remove_pointer_t<decltype(t)>;
+      const int64_t per = 256 / pl.lanes;
+      norm_rows_kernel<T, decltype(v)::value, decltype(nv)::value><<<(unsigned)((r.rows + per - 1) / per), 256, 0, stream>>>(r);
+    });
+    return hipGetLastError() == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
+  }
   const unsigned grid = (unsigned)(p.B * p.chunks);
   bool ok = true;
   by_type_act(dims, [&](auto* t, auto act) {
@@ -157,7 +229,18 @@ int mamba_group_norm_bwd(const void* x, const float* weight, const float* bias, 
   p.pc = reinterpret_cast<float2*>(static_cast<char*>(dims->workspace) + pl.pg);
   p.want_dw = dweight || dbias;
   bool ok = true;
-  by_type_act(dims, [&](auto* t, auto act) {
+  if (pl.v > 0 && pl.nvec <= 4) {
+    NormRowParams r = row_params(dims, pl);
+    r.x = x, r.dout = dout, r.w = weight, r.bias = bias, r.out = dx, r.mean = p.mean, r.rstd = p.rstd;
+    r.pc = p.pc, r.want_dw = p.want_dw;
+    by_row_shape(dims, pl, [&](auto* t, auto v, auto nv) {
+      using T = std::remove_pointer_t<decltype(t)>;
+      constexpr int NV = decltype(nv)::value;
+      const int64_t per = 256 / pl.lanes;
+      if constexpr (NV <= 4)
+        norm_rows_bwd_kernel<T, decltype(v)::value, NV><<<(unsigned)((pl.stride + per - 1) / per), 256, 0, stream>>>(r);
+    });
+  } else by_type_act(dims, [&](auto* t, auto act) {
     using T = std::remove_pointer_t<decltype(t)>;
     constexpr int A = decltype(act)::value;
     if (p.chunks == 1) {
@@ -172,7 +255,7 @@ int mamba_group_norm_bwd(const void* x, const float* weight, const float* bias, 
   });
   if (!ok || hipGetLastError() != hipSuccess) return MAMBA_ERR_HIP;
   if (p.want_dw) {
-    norm_dw_kernel<<<(unsigned)((p.D + 63) / 64), 1024, 0, stream>>>(p.pc, pl.bwd_rows, p.D, dweight, dbias);
+    colsum_kernel<float2><<<(unsigned)((p.D + 15) / 16), 1024, 0, stream>>>(p.pc, pl.bwd_rows, p.D, ColStore{dbias, dweight});
     if (hipGetLastError() != hipSuccess) return MAMBA_ERR_HIP;
   }
   return MAMBA_OK;

@@ -23,6 +23,7 @@
 #pragma once
 
 #include "act_math.h"
+#include "colsum.h"
 
 namespace mscan {
 
@@ -406,26 +407,161 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_bwd_dx_kernel(const Norm
                   sA, sB);
 }
 
-// dbias[d], dweight[d] = Σ over the partial rows: 64 channels a workgroup, 16 threads down the rows of each, joined in a fixed order.
-static __global__ void __launch_bounds__(1024) norm_dw_kernel(const float2* pc, int rows, int D, float* dw, float* db) {
-  __shared__ float2 acc[16][64];
-  const int c = threadIdx.x & 63, t = threadIdx.x >> 6, d = blockIdx.x * 64 + c;
-  float2 s = make_float2(0.f, 0.f);
-  if (d < D) {
-#pragma unroll 4
-    for (int k = t; k < rows; k += 16) {
-      const float2 v = pc[(int64_t)k * D + d];
-      s.x += v.x;
-      s.y += v.y;
+// ---- single tokens ----
+// With one position an item, the groups are rows of C neighbouring values, one
+// after the other in memory.  `lanes` (a power of two) neighbouring lanes take
+// one, NV vectors of V values each, and keep it in registers: one pass, the
+// deviations taken from the mean itself.
+template <typename T, int V>
+__device__ __forceinline__ void row_load(const T* p, float (&f)[V]) {
+  if constexpr (V == 1) {
+    f[0] = load1(p);
+  } else {
+    Vec<T, V> v;
+    v.load(p);
+#pragma unroll
+    for (int j = 0; j < V; ++j) f[j] = v.get(j);
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void row_store(T* p, const float (&f)[V]) {
+  if constexpr (V == 1) store1(p, f[0]);
+  else storeV<V>(p, f);
+}
+template <int V>
+__device__ __forceinline__ void row_param(const float* p, int d, float fill, float (&f)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) f[j] = p ? p[d + j] : fill;
+}
+
+struct NormRowParams {
+  const void *x, *dout;
+  const float *w, *bias;
+  void* out;  // out or dx
+  float *mean, *rstd;
+  float2* pc;
+  int64_t rows, stride;  // B·G; lane groups in the launch (backward: a multiple of G)
+  int C, G, lanes, act, want_dw;
+  float eps;
+};
+
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(256) norm_rows_kernel(const NormRowParams p) {
+  const int li = threadIdx.x & (p.lanes - 1);
+  const int64_t u = ((int64_t)blockIdx.x * 256 + threadIdx.x) / p.lanes;
+  const bool on = u < p.rows;
+  const T* const x = static_cast<const T*>(p.x) + u * p.C;
+  const int c0 = (int)(u % p.G) * p.C;
+  float f[NV][V], s = 0.f, q = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * p.lanes + li) * V;
+    if (on && c < p.C) {
+      row_load<T, V>(x + c, f[i]);
+#pragma unroll
+      for (int j = 0; j < V; ++j) s += f[i][j];
     }
   }
-  acc[t][c] = s;
-  __syncthreads();
-  if (t == 0 && d < D) {
+  const float inv = 1.0f / (float)p.C, mu = lane_sum(s, p.lanes) * inv;
 #pragma unroll
-    for (int k = 1; k < 16; ++k) s.x += acc[k][c].x, s.y += acc[k][c].y;
-    if (db) db[d] = s.x;
-    if (dw) dw[d] = s.y;
+  for (int i = 0; i < NV; ++i) {
+    if ((i * p.lanes + li) * V < p.C) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        f[i][j] -= mu;
+        q = __builtin_fmaf(f[i][j], f[i][j], q);
+      }
+    }
+  }
+  const float rs = 1.0f / __builtin_sqrtf(lane_sum(q, p.lanes) * inv + p.eps);
+  if (!on) return;
+  if (li == 0) {
+    if (p.mean) p.mean[u] = mu;
+    if (p.rstd) p.rstd[u] = rs;
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * p.lanes + li) * V;
+    if (c < p.C) {
+      float w[V], b[V];
+      row_param<V>(p.w, c0 + c, 1.f, w);
+      row_param<V>(p.bias, c0 + c, 0.f, b);
+#pragma unroll
+      for (int j = 0; j < V; ++j) f[i][j] = act_any(__builtin_fmaf(f[i][j] * rs, w[j], b[j]), p.act);
+      row_store<T, V>(static_cast<T*>(p.out) + u * p.C + c, f[i]);
+    }
+  }
+}
+
+// A lane group takes the rows u, u + stride, ...: always the same group of
+// channels, whose dw and dbias it sums; one row of partial sums for every G lane groups.
+template <typename T, int V, int NV>
+__global__ void __launch_bounds__(256) norm_rows_bwd_kernel(const NormRowParams p) {
+  const int li = threadIdx.x & (p.lanes - 1);
+  const int64_t u0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) / p.lanes;
+  if (u0 >= p.stride) return;  // (whole lane groups)
+  const int g = (int)(u0 % p.G), c0 = g * p.C;
+  const float inv = 1.0f / (float)p.C;
+  float w[NV][V], b[NV][V], ts[NV][V], tq[NV][V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * p.lanes + li) * V;
+#pragma unroll
+    for (int j = 0; j < V; ++j) w[i][j] = 1.f, b[i][j] = ts[i][j] = tq[i][j] = 0.f;
+    if (c < p.C) {
+      row_param<V>(p.w, c0 + c, 1.f, w[i]);
+      row_param<V>(p.bias, c0 + c, 0.f, b[i]);
+    }
+  }
+  for (int64_t u = u0; u < p.rows; u += p.stride) {
+    const T* const x = static_cast<const T*>(p.x) + u * p.C;
+    const T* const dy = static_cast<const T*>(p.dout) + u * p.C;
+    const float mu = p.mean[u], rs = p.rstd[u];
+    float xh[NV][V], t[NV][V], sa = 0.f, sb = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * p.lanes + li) * V;
+      if (c < p.C) {
+        row_load<T, V>(x + c, xh[i]);
+        row_load<T, V>(dy + c, t[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if ((i * p.lanes + li) * V < p.C) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          xh[i][j] = (xh[i][j] - mu) * rs;
+          const float du = t[i][j] * act_d_any(__builtin_fmaf(xh[i][j], w[i][j], b[i][j]), p.act);
+          ts[i][j] += du;
+          tq[i][j] = __builtin_fmaf(du, xh[i][j], tq[i][j]);
+          t[i][j] = du * w[i][j];
+          sa += t[i][j];
+          sb = __builtin_fmaf(t[i][j], xh[i][j], sb);
+        }
+      }
+    }
+    const float ma = lane_sum(sa, p.lanes) * inv, mb = lane_sum(sb, p.lanes) * inv;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * p.lanes + li) * V;
+      if (c < p.C) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) t[i][j] = rs * (t[i][j] - ma - xh[i][j] * mb);
+        row_store<T, V>(static_cast<T*>(p.out) + u * p.C + c, t[i]);
+      }
+    }
+  }
+  if (p.want_dw) {
+    float2* const pc = p.pc + (u0 / p.G) * ((int64_t)p.G * p.C) + c0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * p.lanes + li) * V;
+      if (c < p.C) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) pc[c + j] = make_float2(ts[i][j], tq[i][j]);
+      }
+    }
   }
 }
 

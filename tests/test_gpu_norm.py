@@ -68,6 +68,16 @@ CASES = [
     (2500, 3, 24, 3, "bf16", "silu"),
     (3000, 1, 64, 8, "f32", "gelu"),
     (1030, 40, 16, 2, "f32", "silu"),
+    # single tokens: each vector width, several vectors a lane, groups too wide for a lane group
+    (7, 1, 40, 8, "bf16", "silu"),
+    (5000, 1, 48, 12, "f32", "relu"),
+    (70, 1, 1032, 3, "f32", "silu"),
+    (9, 1, 4128, 3, "bf16", "gelu"),
+    (4, 1, 8192, 1, "f32", "silu"),
+    (4, 1, 8192, 2, "bf16", "none"),
+    (3, 1, 3000, 8, "f32", "silu"),
+    (3, 1, 1000, 8, "bf16", "silu"),
+    (9000, 1, 256, 4, "bf16", "none"),
 ]
 
 
