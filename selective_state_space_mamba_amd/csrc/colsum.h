@@ -23,7 +23,7 @@ __device__ __forceinline__ void col_add(float2& a, float2 b) { a.x += b.x, a.y +
 // 16 columns a workgroup, 64 threads down the rows of each: at the usual 1000
 // to 2000 rows a thread has some 20 loads, and a few hundred columns are enough
 // for dozens of workgroups (64 columns and 16 threads each took 8.5 us for 1024
-// rows of 192 columns, this 3.7).
+// rows of 192 columns, this 4.8).
 template <typename S, typename F>
 __global__ void __launch_bounds__(1024) colsum_kernel(const S* part, int64_t rows, int cols, F store) {
   __shared__ S acc[64][17];

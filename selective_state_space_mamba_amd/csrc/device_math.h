@@ -103,6 +103,11 @@ struct Vec<uint16_t, V> {  // bfloat16 bit patterns, V/2 dwords
     const uint32_t x = w[j >> 1];
     return __uint_as_float((j & 1) ? (x & 0xffff0000u) : (x << 16));
   }
+  // Hides where the bits came from, so that what is computed from them again is not kept in registers instead.
+  __device__ __forceinline__ void opaque() {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) asm volatile("" : "+v"(w[i]));
+  }
 };
 
 template <int V>
@@ -126,6 +131,10 @@ struct Vec<float, V> {
     }
   }
   __device__ __forceinline__ float get(int j) const { return f[j]; }
+  __device__ __forceinline__ void opaque() {
+#pragma unroll
+    for (int i = 0; i < V; ++i) asm volatile("" : "+v"(f[i]));
+  }
 };
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -166,6 +175,34 @@ __device__ __forceinline__ void storeV(float* p, const float (&y)[V]) {
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4n __attribute__((ext_vector_type(4)));
+
+// The same stores past the caches, for outputs that nothing here reads again.
+template <int V>
+__device__ __forceinline__ void storeV_nt(uint16_t* p, const float (&y)[V]) {
+  if constexpr (V == 8) {
+    const u32x4 v = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7])};
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
+  } else if constexpr (V == 4) {
+    const u32x2 v = {pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x2*>(p));
+  } else {
+    __builtin_nontemporal_store(pack_bf16x2(y[0], y[1]), reinterpret_cast<uint32_t*>(p));
+  }
+}
+template <int V>
+__device__ __forceinline__ void storeV_nt(float* p, const float (&y)[V]) {
+  if constexpr (V == 2) {
+    const f32x2 v = {y[0], y[1]};
+    __builtin_nontemporal_store(v, reinterpret_cast<f32x2*>(p));
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      const f32x4n v = {y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]};
+      __builtin_nontemporal_store(v, reinterpret_cast<f32x4n*>(p) + i);
+    }
+  }
+}
 
 // ---- E (1, 2 or 4) consecutive elements of B / C, kept as raw bits until used ----
 template <typename T, int E>

@@ -35,13 +35,21 @@ constexpr int kGlrV = 4;         // channels of a thread
 constexpr int kGlrLanes = 16;    // lanes side by side along the channels
 constexpr int kGlrCB = kGlrV * kGlrLanes;  // channels of a workgroup
 constexpr int kGlrSegs = 64 / kGlrLanes;   // runs of a wave
-constexpr int kGlrWaves = 4;
-constexpr int kGlrThreads = 64 * kGlrWaves;
-constexpr int kGlrFwdP = 8;  // positions of a thread, forward
-constexpr int kGlrBwdP = 4;  // and backward
-constexpr int kGlrFwdTile = kGlrFwdP * kGlrSegs * kGlrWaves;  // 128
-constexpr int kGlrBwdTile = kGlrBwdP * kGlrSegs * kGlrWaves;  // 64: also the spacing of the saved states
-static_assert(kGlrFwdTile % kGlrBwdTile == 0 && kGlrBwdTile % (kGlrFwdP * kGlrSegs) == 0, "states saved at wave starts");
+constexpr int kGlrFwdTile = 128;           // positions of a workgroup, forward
+constexpr int kGlrBwdTile = 64;            // and backward: also the spacing of the saved states
+
+// Positions of a thread: what its inputs and their gates take in registers sets
+// the waves that fit.  Forward, 4 positions leave 4 waves a SIMD (8 x 2048 x
+// 1536 in bf16: 61 us, with 8 positions and 2 waves 64); backward, 4 in bf16
+// and 2 in float32, 3 waves (2 in bf16: 168 us against 133, the joins then
+// weigh twice as much).
+template <typename T>
+struct GlrGeom {
+  static constexpr int FP = 4, BP = sizeof(T) == 2 ? 4 : 2;
+  static constexpr int FW = kGlrFwdTile / (FP * kGlrSegs), BW = kGlrBwdTile / (BP * kGlrSegs);  // waves
+  static_assert(FP * FW * kGlrSegs == kGlrFwdTile && BP * BW * kGlrSegs == kGlrBwdTile, "whole tiles");
+  static_assert(kGlrBwdTile % (FP * kGlrSegs) == 0, "states saved at wave starts");
+};
 
 struct GlrParams {
   const void *x, *r, *i, *z;  // [B][L][D]; i, z may be null
@@ -98,20 +106,38 @@ __device__ __forceinline__ float one_minus_exp(float y, float direct) {
   return y < 0.25f ? y * s : direct;
 }
 
-// Decay and input factor from sigmoid(r) = q (and omq = 1 - q without lam);
-// rate = scale·softplus(lam), rl2 = rate·log2 e.
+// sigmoid(r) for the decay; 1 - sigmoid(r) to full relative accuracy only
+// without lam, where it is the factor itself (with lam it just scales dr, to
+// which its absolute accuracy of 2^-24 matters, and costs three instructions less).
+template <bool LAM>
+__device__ __forceinline__ void glr_sigm(float r, float& q, float& omq) {
+  if constexpr (LAM) {
+    q = sigm(r);
+    omq = 1.0f - q;
+  } else {
+    sigm2(r, q, omq);
+  }
+}
+
+// Decay a and the input factor's base from sigmoid(r): beta² for RULE_SQRT,
+// otherwise beta (glr_beta turns it into beta); rate = scale·softplus(lam),
+// rl2 = rate·log2 e.
 template <int RULE, bool LAM>
-__device__ __forceinline__ void glr_decay(float q, float omq, float rate, float rl2, float& a, float& beta) {
+__device__ __forceinline__ void glr_decay(float q, float omq, float rate, float rl2, float& a, float& base) {
   if constexpr (LAM) {
     a = ex2(-rl2 * q);
-    if constexpr (RULE == RULE_SQRT) beta = __builtin_amdgcn_sqrtf(one_minus_exp(2.0f * rate * q, __builtin_fmaf(-a, a, 1.0f)));
-    if constexpr (RULE == RULE_LERP) beta = one_minus_exp(rate * q, 1.0f - a);
+    if constexpr (RULE == RULE_SQRT) base = one_minus_exp(2.0f * rate * q, __builtin_fmaf(-a, a, 1.0f));
+    if constexpr (RULE == RULE_LERP) base = one_minus_exp(rate * q, 1.0f - a);
   } else {
     a = q;
-    if constexpr (RULE == RULE_SQRT) beta = __builtin_amdgcn_sqrtf(omq * (1.0f + q));
-    if constexpr (RULE == RULE_LERP) beta = omq;
+    if constexpr (RULE == RULE_SQRT) base = omq * (1.0f + q);
+    if constexpr (RULE == RULE_LERP) base = omq;
   }
-  if constexpr (RULE == RULE_UNIT) beta = 1.0f;
+  if constexpr (RULE == RULE_UNIT) base = 1.0f;
+}
+template <int RULE>
+__device__ __forceinline__ float glr_beta(float base) {
+  return RULE == RULE_SQRT ? __builtin_amdgcn_sqrtf(base) : base;
 }
 
 // ---- runs ----
@@ -136,12 +162,16 @@ __device__ __forceinline__ float run_mul(float A, float B) {
 // 64-bit word {1 : value}, stored and loaded atomically at agent scope, so a
 // word that is there is whole and no fence (which would write back the L2) is
 // needed; the words start at zero.  A tile takes the nearest state that is
-// there within kGlrWindow tiles behind it and applies the runs in between, in
+// there within a window of tiles behind it and applies the runs in between, in
 // order; since a state is made by exactly that operation, the result does not
 // depend on how far the others have come: every call gives the same bits.
 // Tickets hand the tiles out in the order of the chain, so a workgroup only
 // ever waits for one that has already started, and every wait ends.
-constexpr int kGlrWindow = 8;
+// (The window costs registers in a kernel that has none to spare, and saves
+// waits where few rows make many tiles wait at once: forward, 3 x 4133 x 392 in
+// float32 took 37, 31, 28.7 and 28.4 us with 1, 2, 3 and 4 tiles; backward, 8 x
+// 2048 x 1536 in bf16 took 124 us with 3 and 113 with 2.)
+constexpr int kGlrFwdWindow = 3, kGlrBwdWindow = 2;
 
 __device__ __forceinline__ void word_put(uint64_t* p, float v) {
   __hip_atomic_store(p, ((uint64_t)1 << 32) | __float_as_uint(v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -155,7 +185,7 @@ __device__ __forceinline__ float word_val(uint64_t w) { return __uint_as_float((
 // One wave, one channel a lane.  step: the tile's place in the chain; first:
 // the state that enters place 0.  Returns the state that enters this tile and
 // publishes the one that leaves it.
-template <bool RESET>
+template <bool RESET, int WINDOW>
 __device__ __forceinline__ float chain_carry(const GlrParams& p, int row, int step, int lane, float A, float H, float first) {
   const int64_t stride = (int64_t)p.B * p.nblk * p.ntiles * kGlrCB;
   uint64_t* const inc = p.words + ((int64_t)row * p.ntiles + step) * kGlrCB + lane;
@@ -168,9 +198,9 @@ __device__ __forceinline__ float chain_carry(const GlrParams& p, int row, int st
       word_put(wa, A);
       word_put(wh, H);
       for (;;) {
-        uint64_t si[kGlrWindow], sa[kGlrWindow], sh[kGlrWindow];
+        uint64_t si[WINDOW], sa[WINDOW], sh[WINDOW];
 #pragma unroll
-        for (int k = 0; k < kGlrWindow; ++k) {
+        for (int k = 0; k < WINDOW; ++k) {
           const int back = min(k + 1, step) * kGlrCB;
           si[k] = word_get(inc - back);
           sa[k] = word_get(wa - back);
@@ -178,7 +208,7 @@ __device__ __forceinline__ float chain_carry(const GlrParams& p, int row, int st
         }
         bool ok = false;
 #pragma unroll
-        for (int k = kGlrWindow - 1; k >= 0; --k) {
+        for (int k = WINDOW - 1; k >= 0; --k) {
           if (k + 1 <= step) {
             const float next = run_apply<RESET>(word_val(sa[k]), word_val(sh[k]), v);
             const bool run = word_there(sa[k]) && word_there(sh[k]), have = word_there(si[k]);
@@ -198,44 +228,64 @@ __device__ __forceinline__ float chain_carry(const GlrParams& p, int row, int st
 }
 
 // ---- forward ----
+
+// The tile a workgroup takes: its row of 64 channels and its place(s) along the scan.
+template <bool CHAIN>
+__device__ __forceinline__ void glr_tile(const GlrParams& p, uint32_t* sTicket, int& row, int& step, int& step_end) {
+  if constexpr (CHAIN) {
+    if (threadIdx.x == 0) *sTicket = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    const uint32_t t = __builtin_amdgcn_readfirstlane(*sTicket);
+    const uint32_t rows = (uint32_t)(p.B * p.nblk);
+    step = (int)(t / rows);
+    row = (int)(t % rows);
+    step_end = step + 1;
+  } else {
+    row = blockIdx.x;
+    step = 0;
+    step_end = p.ntiles;
+  }
+}
+
+// A tile's element by its byte offset: a scalar base and a 32-bit offset are an address as they are.
+template <typename T>
+__device__ __forceinline__ const T* at_byte(const T* base, uint32_t off) {
+  return reinterpret_cast<const T*>(reinterpret_cast<const char*>(base) + off);
+}
+template <typename T>
+__device__ __forceinline__ T* at_byte(T* base, uint32_t off) {
+  return reinterpret_cast<T*>(reinterpret_cast<char*>(base) + off);
+}
+
+__device__ __forceinline__ void lds_put(float* at, const float (&v)[4]) { *reinterpret_cast<float4*>(at) = make_float4(v[0], v[1], v[2], v[3]); }
+__device__ __forceinline__ void lds_get(const float* at, float (&v)[4]) {
+  const float4 f = *reinterpret_cast<const float4*>(at);
+  v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+}
+
 // A workgroup takes 64 channels and tiles of 128 positions: the 16 lanes of a
-// row segment cover 128 bytes (bf16), each thread a run of 8 positions.
+// row segment cover 128 bytes (bf16), each thread a run of FP positions.  Wave
+// 0 joins the waves (and, in a chain, the tiles), a channel a lane.
 template <typename T, int RULE, bool LAM, bool RESET, bool CHAIN>
-__global__ void __launch_bounds__(kGlrThreads) glr_fwd_kernel(const GlrParams p) {
-  constexpr int V = kGlrV, P = kGlrFwdP, NW = kGlrWaves, TT = kGlrFwdTile;
-  __shared__ float sA[2][NW][kGlrCB], sH[2][NW][kGlrCB], sC[kGlrCB];
+__global__ void __launch_bounds__(64 * GlrGeom<T>::FW) glr_fwd_kernel(const GlrParams p) {
+  constexpr int V = kGlrV, P = GlrGeom<T>::FP, NW = GlrGeom<T>::FW, TT = kGlrFwdTile;
+  __shared__ __align__(16) float sA[NW][kGlrCB], sH[NW][kGlrCB], sC[NW][kGlrCB];
   __shared__ uint32_t sTicket;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int seg = lane / kGlrLanes, cl = lane % kGlrLanes;
   int row, tile, tile_end;
-  if constexpr (CHAIN) {
-    if (threadIdx.x == 0) sTicket = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    const uint32_t t = __builtin_amdgcn_readfirstlane(sTicket);
-    const uint32_t rows = (uint32_t)(p.B * p.nblk);
-    tile = (int)(t / rows);
-    row = (int)(t % rows);
-    tile_end = tile + 1;
-  } else {
-    row = blockIdx.x;
-    tile = 0;
-    tile_end = p.ntiles;
-  }
+  glr_tile<CHAIN>(p, &sTicket, row, tile, tile_end);
   const int b = row / p.nblk, dblk = (row % p.nblk) * kGlrCB;
   const bool dok = dblk + cl * V < p.D;
   const int d0 = dok ? dblk + cl * V : 0;  // lanes past the last channel repeat the first four and store nothing
   const int L = p.L, D = p.D;
   const int64_t bbase = (int64_t)b * L * D;
+  // wave 0: the channel of a lane, and the state that enters the next tile
+  const bool cok = dblk + lane < D;
+  const int64_t bd = (int64_t)b * D + dblk + lane;
+  float carry = wave == 0 && p.init && cok ? p.init[bd] : 0.f;
 
-  float rate[V], rl2[V], carry[V];
-#pragma unroll
-  for (int c = 0; c < V; ++c) {
-    rate[c] = LAM ? p.scale * softplus_rel(p.lam[d0 + c]) : 0.f;
-    rl2[c] = rate[c] * kLog2e;
-    carry[c] = !CHAIN && p.init ? p.init[(int64_t)b * D + d0 + c] : 0.f;
-  }
-
-  for (int buf = 0; tile < tile_end; ++tile, buf ^= 1) {
+  for (; tile < tile_end; ++tile) {
     const int s0 = tile * TT, sp = s0 + (wave * kGlrSegs + seg) * P;
     // the tile's lowest token, the base of its 32-bit offsets
     const int tb = p.reverse ? max(L - s0 - TT, 0) : s0;
@@ -245,54 +295,70 @@ __global__ void __launch_bounds__(kGlrThreads) glr_fwd_kernel(const GlrParams p)
 #pragma unroll
     for (int k = 0; k < P; ++k) {
       const int s = min(sp + k, L - 1), t = (p.reverse ? L - 1 - s : s) - tb;
-      off[k] = (uint32_t)t * (uint32_t)D + (uint32_t)d0;
+      off[k] = ((uint32_t)t * (uint32_t)D + (uint32_t)d0) * (uint32_t)sizeof(T);
       rst[k] = RESET && p.reset[(int64_t)b * L + tb + t] != 0;
     }
+    Vec<T, V> x[P], r[P], g[P], z[P];
     const T* const xb = static_cast<const T*>(p.x) + base;
     const T* const rb = static_cast<const T*>(p.r) + base;
-    Vec<T, V> x[P], r[P], g[P], z[P];
 #pragma unroll
-    for (int k = 0; k < P; ++k) x[k].load(xb + off[k]);
+    for (int k = 0; k < P; ++k) r[k].load(at_byte(rb, off[k]));
 #pragma unroll
-    for (int k = 0; k < P; ++k) r[k].load(rb + off[k]);
+    for (int k = 0; k < P; ++k) x[k].load(at_byte(xb, off[k]));
     if (p.i) {
       const T* const ib = static_cast<const T*>(p.i) + base;
 #pragma unroll
-      for (int k = 0; k < P; ++k) g[k].load(ib + off[k]);
+      for (int k = 0; k < P; ++k) g[k].load(at_byte(ib, off[k]));
     }
     if (p.z && p.out) {
       const T* const zb = static_cast<const T*>(p.z) + base;
 #pragma unroll
-      for (int k = 0; k < P; ++k) z[k].load(zb + off[k]);
+      for (int k = 0; k < P; ++k) z[k].load(at_byte(zb, off[k]));
     }
     float a[P][V], h[P][V];
     float A[V], H[V];
 #pragma unroll
-    for (int c = 0; c < V; ++c) A[c] = 1.f, H[c] = 0.f;
+    for (int c = 0; c < V; ++c) {
+      const float rate = LAM ? p.scale * softplus_rel(p.lam[d0 + c]) : 0.f, rl2 = rate * kLog2e;
 #pragma unroll
-    for (int k = 0; k < P; ++k) {
-      const bool in = sp + k < L;
+      for (int k = 0; k < P; ++k) {
+        float q, omq, base;
+        glr_sigm<LAM>(r[k].get(c), q, omq);
+        glr_decay<RULE, LAM>(q, omq, rate, rl2, a[k][c], base);
+        h[k][c] = glr_beta<RULE>(base) * x[k].get(c);
+      }
+    }
+    if (p.i) {
 #pragma unroll
-      for (int c = 0; c < V; ++c) {
-        float q, omq = 0.f, beta, v = x[k].get(c);
-        if constexpr (LAM) q = sigm(r[k].get(c));
-        else sigm2(r[k].get(c), q, omq);
-        glr_decay<RULE, LAM>(q, omq, rate[c], rl2[c], a[k][c], beta);
-        if (p.i) v *= sigm(g[k].get(c));
-        h[k][c] = in ? beta * v : 0.f;
-        a[k][c] = in ? a[k][c] : 1.f;
-        if constexpr (RESET) {
-          const bool cut = in && rst[k];
-          a[k][c] = cut ? 0.f : a[k][c];
-          H[c] = cut ? h[k][c] : __builtin_fmaf(a[k][c], H[c], h[k][c]);
-          A[c] = run_mul<true>(A[c], a[k][c]);
-        } else {
-          H[c] = __builtin_fmaf(a[k][c], H[c], h[k][c]);
-          A[c] *= a[k][c];
+      for (int k = 0; k < P; ++k)
+#pragma unroll
+        for (int c = 0; c < V; ++c) h[k][c] *= sigm(g[k].get(c));
+    }
+    if (s0 + TT > L) {  // positions past the end pass the state on
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        const bool in = sp + k < L;
+        rst[k] = rst[k] && in;
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+          a[k][c] = in ? a[k][c] : 1.f;
+          h[k][c] = in ? h[k][c] : 0.f;
         }
       }
     }
-    // the runs of the wave, inclusive
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      if constexpr (RESET) a[0][c] = rst[0] ? 0.f : a[0][c];
+      A[c] = a[0][c];
+      H[c] = h[0][c];
+#pragma unroll
+      for (int k = 1; k < P; ++k) {
+        if constexpr (RESET) a[k][c] = rst[k] ? 0.f : a[k][c];
+        H[c] = run_apply<RESET>(a[k][c], h[k][c], H[c]);
+        A[c] = run_mul<RESET>(A[c], a[k][c]);
+      }
+    }
+    // the runs of the wave, inclusive; then what lies before this thread's
 #pragma unroll
     for (int o = kGlrLanes; o < 64; o *= 2) {
 #pragma unroll
@@ -305,44 +371,43 @@ __global__ void __launch_bounds__(kGlrThreads) glr_fwd_kernel(const GlrParams p)
       }
     }
     if (seg == kGlrSegs - 1) {
-#pragma unroll
-      for (int c = 0; c < V; ++c) {
-        sA[buf][wave][cl * V + c] = A[c];
-        sH[buf][wave][cl * V + c] = H[c];
-      }
+      lds_put(&sA[wave][cl * V], A);
+      lds_put(&sH[wave][cl * V], H);
     }
-    __syncthreads();
-    if constexpr (CHAIN) {
-      if (wave == 0) {
-        float At = sA[buf][0][lane], Ht = sH[buf][0][lane];
-#pragma unroll
-        for (int w = 1; w < NW; ++w) {
-          Ht = run_apply<RESET>(sA[buf][w][lane], sH[buf][w][lane], Ht);
-          At = run_mul<RESET>(At, sA[buf][w][lane]);
-        }
-        const int d = dblk + lane;
-        const float first = p.init && d < D ? p.init[(int64_t)b * D + d] : 0.f;
-        sC[lane] = chain_carry<RESET>(p, row, tile, lane, At, Ht, first);
-      }
-      __syncthreads();
-#pragma unroll
-      for (int c = 0; c < V; ++c) carry[c] = sC[cl * V + c];
-    }
-    float hs[V];  // the state that enters this thread's run
 #pragma unroll
     for (int c = 0; c < V; ++c) {
-      hs[c] = carry[c];
+      A[c] = __shfl_up(A[c], kGlrLanes);
+      H[c] = __shfl_up(H[c], kGlrLanes);
+    }
+    __syncthreads();
+    if (wave == 0) {
+      if constexpr (CHAIN) {
+        float At = sA[0][lane], Ht = sH[0][lane];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) {
+          Ht = run_apply<RESET>(sA[w][lane], sH[w][lane], Ht);
+          At = run_mul<RESET>(At, sA[w][lane]);
+        }
+        carry = chain_carry<RESET, kGlrFwdWindow>(p, row, tile, lane, At, Ht, carry);
+      }
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        if (w == wave) hs[c] = carry[c];
-        carry[c] = run_apply<RESET>(sA[buf][w][cl * V + c], sH[buf][w][cl * V + c], carry[c]);
+        constexpr int kWave = P * kGlrSegs;  // positions of a wave
+        sC[w][lane] = carry;
+        if (w * kWave % kGlrBwdTile == 0 && p.saved && cok && s0 + w * kWave < L)
+          p.saved[((int64_t)b * ((L + kGlrBwdTile - 1) / kGlrBwdTile) + (s0 + w * kWave) / kGlrBwdTile) * D + dblk + lane] = carry;
+        carry = run_apply<RESET>(sA[w][lane], sH[w][lane], carry);
       }
-      const float A1 = __shfl_up(A[c], kGlrLanes), H1 = __shfl_up(H[c], kGlrLanes);
-      if (p.saved && seg == 0 && dok && (sp % kGlrBwdTile) == 0 && sp < L)
-        p.saved[((int64_t)b * ((L + kGlrBwdTile - 1) / kGlrBwdTile) + sp / kGlrBwdTile) * D + d0 + c] = hs[c];
-      if (seg > 0) hs[c] = run_apply<RESET>(A1, H1, hs[c]);
+      if (p.last && tile == p.ntiles - 1 && cok) p.last[bd] = carry;
     }
+    __syncthreads();
     if (p.out) {
+      float hs[V];  // the state that enters this thread's run
+      lds_get(&sC[wave][cl * V], hs);
+      if (seg > 0) {
+#pragma unroll
+        for (int c = 0; c < V; ++c) hs[c] = run_apply<RESET>(A[c], H[c], hs[c]);
+      }
       T* const ob = static_cast<T*>(p.out) + base;
 #pragma unroll
       for (int k = 0; k < P; ++k) {
@@ -356,12 +421,8 @@ __global__ void __launch_bounds__(kGlrThreads) glr_fwd_kernel(const GlrParams p)
 #pragma unroll
           for (int c = 0; c < V; ++c) y[c] *= silu_f(z[k].get(c));
         }
-        if (dok && sp + k < L) storeV<V>(ob + off[k], y);
+        if (dok && sp + k < L) storeV_nt<V>(at_byte(ob, off[k]), y);
       }
-    }
-    if (p.last && tile == p.ntiles - 1 && wave == 0 && seg == 0 && dok) {
-#pragma unroll
-      for (int c = 0; c < V; ++c) p.last[(int64_t)b * D + d0 + c] = carry[c];
     }
   }
 }
@@ -373,126 +434,137 @@ __global__ void __launch_bounds__(kGlrThreads) glr_fwd_kernel(const GlrParams p)
 // tiles like the forward's state.  Every gradient leaves from the same
 // registers:
 //   m = dout·silu(z) + c,  c' = a·m
-//   dx = m·beta·p (p = sigmoid(i)),  di = dx·x·(1 - p),  dz = dout·h·silu'(z)
+//   dx = m·w (w = beta·p, p = sigmoid(i)),  di = dx·x·(1 - p),  dz = dout·h·silu'(z)
 //   dE = m·(p·x·dbeta/dE - a·h_prev),  dbeta/dE = a²/beta | a | 0
 //   dr = dE·E·(1 - q) with lam;  without it dE/dr = -(1 - q)
 //   dlam = Σ dE·q·scale·sigmoid(lam)
 // For RULE_SQRT, a²/beta grows without bound as E -> 0 while E·a²/beta and
-// (1 - q)·a²/beta go to 0 like sqrt(E): the guard on beta keeps their product
+// (1 - q)·a²/beta go to 0 like sqrt(E): the guard on beta² keeps their product
 // finite where E has underflowed.
+//
+// Registers decide how many waves a SIMD holds, so across the two joins a
+// thread keeps a, w, beta (or beta²) and m beside its raw inputs, and computes
+// the sigmoids of r, i and z a second time at the end (six of the
+// transcendentals, against 48 registers).  In a chain, w and m wait in LDS of
+// the thread's own while wave 0 looks back: 155 registers without spilling,
+// against 193 (two waves a SIMD) or 25 spilled; 8 x 2048 x 1536 in bf16 113 us
+// against 133 and 155.
 template <typename T, int RULE, bool LAM, bool RESET, bool CHAIN>
-__global__ void __launch_bounds__(kGlrThreads) glr_bwd_kernel(const GlrParams p) {
-  constexpr int V = kGlrV, P = kGlrBwdP, NW = kGlrWaves, TT = kGlrBwdTile;
-  __shared__ float sA[2][NW][kGlrCB], sH[2][NW][kGlrCB], sG[2][NW][kGlrCB], sC[kGlrCB];
+__global__ void __launch_bounds__(64 * GlrGeom<T>::BW, 3) glr_bwd_kernel(const GlrParams p) {
+  constexpr int V = kGlrV, P = GlrGeom<T>::BP, NW = GlrGeom<T>::BW, TT = kGlrBwdTile;
+  __shared__ __align__(16) float sA[NW][kGlrCB], sH[NW][kGlrCB], sG[NW][kGlrCB], sC[NW][kGlrCB], sD[NW][kGlrCB];
+  __shared__ __align__(16) float sM[CHAIN ? P : 1][64 * NW * V], sW[CHAIN ? P : 1][64 * NW * V];
   __shared__ uint32_t sTicket;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int seg = lane / kGlrLanes, cl = lane % kGlrLanes;
   int row, step, step_end;  // step 0 is the last tile of the scan
-  if constexpr (CHAIN) {
-    if (threadIdx.x == 0) sTicket = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    const uint32_t t = __builtin_amdgcn_readfirstlane(sTicket);
-    const uint32_t rows = (uint32_t)(p.B * p.nblk);
-    step = (int)(t / rows);
-    row = (int)(t % rows);
-    step_end = step + 1;
-  } else {
-    row = blockIdx.x;
-    step = 0;
-    step_end = p.ntiles;
-  }
+  glr_tile<CHAIN>(p, &sTicket, row, step, step_end);
   const int b = row / p.nblk, dblk = (row % p.nblk) * kGlrCB;
   const bool dok = dblk + cl * V < p.D;
   const int d0 = dok ? dblk + cl * V : 0;
   const int L = p.L, D = p.D;
   const int64_t bbase = (int64_t)b * L * D;
-
-  float rate[V], rl2[V], carry[V], dlam[V];
+  const bool cok = dblk + lane < D;
+  const int64_t bd = (int64_t)b * D + dblk + lane;
+  float carry = wave == 0 && p.dlast && cok ? p.dlast[bd] : 0.f;
+  float dlam[V];
 #pragma unroll
-  for (int c = 0; c < V; ++c) {
-    rate[c] = LAM ? p.scale * softplus_rel(p.lam[d0 + c]) : 0.f;
-    rl2[c] = rate[c] * kLog2e;
-    carry[c] = !CHAIN && p.dlast ? p.dlast[(int64_t)b * D + d0 + c] : 0.f;
-    dlam[c] = 0.f;
-  }
+  for (int c = 0; c < V; ++c) dlam[c] = 0.f;
 
-  for (int buf = 0; step < step_end; ++step, buf ^= 1) {
+  for (; step < step_end; ++step) {
     const int tile = p.ntiles - 1 - step;
     const int s0 = tile * TT, sp = s0 + (wave * kGlrSegs + seg) * P;
     const int tb = p.reverse ? max(L - s0 - TT, 0) : s0;
     const int64_t base = bbase + (int64_t)tb * D;
     uint32_t off[P];
-    bool rst[P];
+    bool rst[P], in[P];
 #pragma unroll
     for (int k = 0; k < P; ++k) {
       const int s = min(sp + k, L - 1), t = (p.reverse ? L - 1 - s : s) - tb;
-      off[k] = (uint32_t)t * (uint32_t)D + (uint32_t)d0;
-      rst[k] = RESET && p.reset[(int64_t)b * L + tb + t] != 0;
+      in[k] = sp + k < L;
+      off[k] = ((uint32_t)t * (uint32_t)D + (uint32_t)d0) * (uint32_t)sizeof(T);
+      rst[k] = RESET && in[k] && p.reset[(int64_t)b * L + tb + t] != 0;
     }
     Vec<T, V> x[P], r[P], g[P], z[P], dy[P];
     const T* const xb = static_cast<const T*>(p.x) + base;
     const T* const rb = static_cast<const T*>(p.r) + base;
     const T* const yb = static_cast<const T*>(p.dout) + base;
 #pragma unroll
-    for (int k = 0; k < P; ++k) x[k].load(xb + off[k]);
+    for (int k = 0; k < P; ++k) r[k].load(at_byte(rb, off[k]));
 #pragma unroll
-    for (int k = 0; k < P; ++k) r[k].load(rb + off[k]);
+    for (int k = 0; k < P; ++k) x[k].load(at_byte(xb, off[k]));
     if (p.i) {
       const T* const ib = static_cast<const T*>(p.i) + base;
 #pragma unroll
-      for (int k = 0; k < P; ++k) g[k].load(ib + off[k]);
+      for (int k = 0; k < P; ++k) g[k].load(at_byte(ib, off[k]));
     }
+#pragma unroll
+    for (int k = 0; k < P; ++k) dy[k].load(at_byte(yb, off[k]));
     if (p.z) {
       const T* const zb = static_cast<const T*>(p.z) + base;
 #pragma unroll
-      for (int k = 0; k < P; ++k) z[k].load(zb + off[k]);
+      for (int k = 0; k < P; ++k) z[k].load(at_byte(zb, off[k]));
     }
+    float state = 0.f;  // wave 0: the state that enters the tile
+    if (wave == 0 && cok) state = p.saved[((int64_t)b * p.ntiles + tile) * D + dblk + lane];
+    float rate[V];
 #pragma unroll
-    for (int k = 0; k < P; ++k) dy[k].load(yb + off[k]);
-    float h0[V];  // the state that enters the tile
-#pragma unroll
-    for (int c = 0; c < V; ++c) h0[c] = p.saved[((int64_t)b * p.ntiles + tile) * D + d0 + c];
-    // a, beta, sigmoids and, from the start of the tile, the states; the
-    // adjoint's own terms dout·silu(z)
-    float a[P][V], bt[P][V], q[P][V], omq[P][V], pi[P][V], h[P][V], m[P][V];
-    float A[V], H[V], G[V];
-#pragma unroll
-    for (int c = 0; c < V; ++c) A[c] = 1.f, H[c] = 0.f, G[c] = 0.f;
+    for (int c = 0; c < V; ++c) rate[c] = LAM ? p.scale * softplus_rel(p.lam[d0 + c]) : 0.f;
+
+    float a[P][V], w[P][V], bt[P][V], m[P][V];
+    float A[V], H[V], G[V], A2[V];
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-      const bool in = sp + k < L;
 #pragma unroll
       for (int c = 0; c < V; ++c) {
-        sigm2(r[k].get(c), q[k][c], omq[k][c]);
-        glr_decay<RULE, LAM>(q[k][c], omq[k][c], rate[c], rl2[c], a[k][c], bt[k][c]);
-        pi[k][c] = p.i ? sigm(g[k].get(c)) : 1.f;
-        a[k][c] = in ? a[k][c] : 1.f;
-        const float v = in ? bt[k][c] * pi[k][c] * x[k].get(c) : 0.f;
-        if constexpr (RESET) {
-          const bool cut = in && rst[k];
-          H[c] = cut ? v : __builtin_fmaf(a[k][c], H[c], v);
-          A[c] = cut ? 0.f : run_mul<true>(A[c], a[k][c]);
-        } else {
-          H[c] = __builtin_fmaf(a[k][c], H[c], v);
-          A[c] *= a[k][c];
-        }
-        const float gate = p.z ? silu_f(z[k].get(c)) : 1.f;
-        m[k][c] = in ? dy[k].get(c) * gate : 0.f;
+        float q, omq;
+        glr_sigm<LAM>(r[k].get(c), q, omq);
+        glr_decay<RULE, LAM>(q, omq, rate[c], rate[c] * kLog2e, a[k][c], bt[k][c]);
+        w[k][c] = glr_beta<RULE>(bt[k][c]);
+        m[k][c] = dy[k].get(c);
       }
     }
-    // the adjoint's run, from its end
+    if (p.i) {
 #pragma unroll
-    for (int k = P - 1; k >= 0; --k) {
+      for (int k = 0; k < P; ++k)
 #pragma unroll
-      for (int c = 0; c < V; ++c) {
-        G[c] = a[k][c] * (m[k][c] + G[c]);
-        if constexpr (RESET) G[c] = (sp + k < L && rst[k]) ? 0.f : G[c];
+        for (int c = 0; c < V; ++c) w[k][c] *= sigm(g[k].get(c));
+    }
+    if (p.z) {
+#pragma unroll
+      for (int k = 0; k < P; ++k)
+#pragma unroll
+        for (int c = 0; c < V; ++c) m[k][c] *= silu_f(z[k].get(c));
+    }
+    if (s0 + TT > L) {  // positions past the end pass both on
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        if (!in[k]) {
+          x[k].zero();
+#pragma unroll
+          for (int c = 0; c < V; ++c) a[k][c] = 1.f, w[k][c] = m[k][c] = 0.f;
+        }
       }
+    }
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      A[c] = 1.f;
+      H[c] = G[c] = 0.f;
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        // (a stays what it is where a sequence starts: the input factor's derivative takes it)
+        const float v = w[k][c] * x[k].get(c), ak = RESET && rst[k] ? 0.f : a[k][c];
+        H[c] = k == 0 ? v : run_apply<RESET>(ak, v, H[c]);
+        A[c] = k == 0 ? ak : run_mul<RESET>(A[c], ak);
+      }
+#pragma unroll
+      for (int k = P - 1; k >= 0; --k) {
+        G[c] = a[k][c] * (m[k][c] + G[c]);
+        if constexpr (RESET) G[c] = rst[k] ? 0.f : G[c];
+      }
+      A2[c] = A[c];
     }
     // both scans over the runs of the wave: states upwards, adjoints downwards
-    float A2[V];
-#pragma unroll
-    for (int c = 0; c < V; ++c) A2[c] = A[c];
 #pragma unroll
     for (int o = kGlrLanes; o < 64; o *= 2) {
 #pragma unroll
@@ -510,116 +582,141 @@ __global__ void __launch_bounds__(kGlrThreads) glr_bwd_kernel(const GlrParams p)
       }
     }
     if (seg == kGlrSegs - 1) {
-#pragma unroll
-      for (int c = 0; c < V; ++c) {
-        sA[buf][wave][cl * V + c] = A[c];
-        sH[buf][wave][cl * V + c] = H[c];
-      }
+      lds_put(&sA[wave][cl * V], A);
+      lds_put(&sH[wave][cl * V], H);
     }
-    if (seg == 0) {
-#pragma unroll
-      for (int c = 0; c < V; ++c) sG[buf][wave][cl * V + c] = G[c];
-    }
-    __syncthreads();
+    if (seg == 0) lds_put(&sG[wave][cl * V], G);
     if constexpr (CHAIN) {
-      if (wave == 0) {
-        float At = sA[buf][NW - 1][lane], Gt = sG[buf][NW - 1][lane];
 #pragma unroll
-        for (int w = NW - 2; w >= 0; --w) {
-          Gt = run_apply<RESET>(sA[buf][w][lane], sG[buf][w][lane], Gt);
-          At = run_mul<RESET>(At, sA[buf][w][lane]);
-        }
-        const int d = dblk + lane;
-        const float first = p.dlast && d < D ? p.dlast[(int64_t)b * D + d] : 0.f;
-        sC[lane] = chain_carry<RESET>(p, row, step, lane, At, Gt, first);
+      for (int k = 0; k < P; ++k) {
+        lds_put(&sM[k][threadIdx.x * V], m[k]);
+        lds_put(&sW[k][threadIdx.x * V], w[k]);
       }
-      __syncthreads();
-#pragma unroll
-      for (int c = 0; c < V; ++c) carry[c] = sC[cl * V + c];
     }
-    float hs[V], cs[V];  // what enters this thread's run: the state, and the adjoint from behind
 #pragma unroll
     for (int c = 0; c < V; ++c) {
-      hs[c] = h0[c];
-#pragma unroll
-      for (int w = 0; w < NW; ++w)
-        if (w < wave) hs[c] = run_apply<RESET>(sA[buf][w][cl * V + c], sH[buf][w][cl * V + c], hs[c]);
-      cs[c] = carry[c];
-#pragma unroll
-      for (int w = NW - 1; w >= 0; --w) {
-        if (w == wave) cs[c] = carry[c];
-        carry[c] = run_apply<RESET>(sA[buf][w][cl * V + c], sG[buf][w][cl * V + c], carry[c]);
-      }
-      const float A1 = __shfl_up(A[c], kGlrLanes), H1 = __shfl_up(H[c], kGlrLanes);
-      const float A3 = __shfl_down(A2[c], kGlrLanes), G3 = __shfl_down(G[c], kGlrLanes);
-      if (seg > 0) hs[c] = run_apply<RESET>(A1, H1, hs[c]);
-      if (seg < kGlrSegs - 1) cs[c] = run_apply<RESET>(A3, G3, cs[c]);
+      A[c] = __shfl_up(A[c], kGlrLanes);
+      H[c] = __shfl_up(H[c], kGlrLanes);
+      A2[c] = __shfl_down(A2[c], kGlrLanes);
+      G[c] = __shfl_down(G[c], kGlrLanes);
     }
-    // the states before each position
+    __syncthreads();
+    if (wave == 0) {
+#pragma unroll
+      for (int u = 0; u < NW; ++u) {
+        sC[u][lane] = state;
+        state = run_apply<RESET>(sA[u][lane], sH[u][lane], state);
+      }
+      if constexpr (CHAIN) {
+        float At = sA[NW - 1][lane], Gt = sG[NW - 1][lane];
+#pragma unroll
+        for (int u = NW - 2; u >= 0; --u) {
+          Gt = run_apply<RESET>(sA[u][lane], sG[u][lane], Gt);
+          At = run_mul<RESET>(At, sA[u][lane]);
+        }
+        carry = chain_carry<RESET, kGlrBwdWindow>(p, row, step, lane, At, Gt, carry);
+      }
+#pragma unroll
+      for (int u = NW - 1; u >= 0; --u) {
+        sD[u][lane] = carry;
+        carry = run_apply<RESET>(sA[u][lane], sG[u][lane], carry);
+      }
+      if (p.dinit && tile == 0 && cok) p.dinit[bd] = carry;
+    }
+    __syncthreads();
+    float hs[V], cs[V];  // what enters this thread's run: the state, and the adjoint from behind
+    lds_get(&sC[wave][cl * V], hs);
+    lds_get(&sD[wave][cl * V], cs);
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      if (seg > 0) hs[c] = run_apply<RESET>(A[c], H[c], hs[c]);
+      if (seg < kGlrSegs - 1) cs[c] = run_apply<RESET>(A2[c], G[c], cs[c]);
+    }
+    // (opaque to the compiler, which would otherwise keep the sigmoids, and bf16 inputs widened, since the first sweep)
 #pragma unroll
     for (int k = 0; k < P; ++k) {
+      r[k].opaque();
+      x[k].opaque();
+      dy[k].opaque();
+      if (p.i) g[k].opaque();
+      if (p.z) z[k].opaque();
+    }
+    if constexpr (CHAIN) {
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        lds_get(&sM[k][threadIdx.x * V], m[k]);
+        lds_get(&sW[k][threadIdx.x * V], w[k]);
+      }
+    }
+    // the adjoints, from the end, in the place of dout·silu(z)
+#pragma unroll
+    for (int k = P - 1; k >= 0; --k) {
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        m[k][c] += cs[c];
+        cs[c] = a[k][c] * m[k][c];
+        if constexpr (RESET) cs[c] = rst[k] ? 0.f : cs[c];
+      }
+    }
+    // and from the start, with the state before each position, the gradients
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      float t[V], u[V], dx[V], hv[V];
 #pragma unroll
       for (int c = 0; c < V; ++c) {
         if constexpr (RESET) hs[c] = rst[k] ? 0.f : hs[c];
-        h[k][c] = hs[c];
-        hs[c] = __builtin_fmaf(a[k][c], hs[c], bt[k][c] * pi[k][c] * x[k].get(c));
-      }
-    }
-#pragma unroll
-    for (int k = P - 1; k >= 0; --k) {
-      const bool in = sp + k < L;
-      float dx[V], dr[V], di[V], dz[V];
-#pragma unroll
-      for (int c = 0; c < V; ++c) {
-        const float xv = x[k].get(c), av = a[k][c], mv = m[k][c] + cs[c], v = pi[k][c] * xv;
-        cs[c] = av * mv;
-        if constexpr (RESET) cs[c] = (in && rst[k]) ? 0.f : cs[c];
-        dx[c] = mv * bt[k][c] * pi[k][c];
-        di[c] = dx[c] * xv * (1.f - pi[k][c]);
-        float de;
-        if constexpr (RULE == RULE_SQRT) de = mv * (v * av * av * rcp(__builtin_fmaxf(bt[k][c], 1e-18f)) - av * h[k][c]);
-        else if constexpr (RULE == RULE_LERP) de = mv * av * (v - h[k][c]);
-        else de = -mv * av * h[k][c];
+        const float xv = x[k].get(c), av = a[k][c], mv = m[k][c], v = w[k][c] * xv;
+        hv[c] = __builtin_fmaf(av, hs[c], v);
+        dx[c] = mv * w[k][c];
+        float q, omq;
+        glr_sigm<LAM>(r[k].get(c), q, omq);
+        float de;  // the factor beside m·a
+        if constexpr (RULE == RULE_SQRT)
+          de = __builtin_fmaf(v * av, rcp(__builtin_fmaxf(bt[k][c], 1e-36f)), -hs[c]);
+        else if constexpr (RULE == RULE_LERP)
+          de = (p.i ? sigm(g[k].get(c)) * xv : xv) - hs[c];
+        else
+          de = -hs[c];
+        de *= mv * av;
         if constexpr (LAM) {
-          dr[c] = de * (rate[c] * q[k][c]) * omq[k][c];
-          dlam[c] += in ? de * q[k][c] : 0.f;
+          u[c] = de * (rate[c] * q) * omq;
+          dlam[c] += in[k] ? de * q : 0.f;
         } else {
-          dr[c] = -de * omq[k][c];
+          u[c] = -de * omq;
         }
+        hs[c] = hv[c];
       }
-      if (in && dok) {
-        storeV<V>(static_cast<T*>(p.dx) + base + off[k], dx);
-        storeV<V>(static_cast<T*>(p.dr) + base + off[k], dr);
-        if (p.di) storeV<V>(static_cast<T*>(p.di) + base + off[k], di);
+      if (in[k] && dok) {
+        storeV_nt<V>(at_byte(static_cast<T*>(p.dx) + base, off[k]), dx);
+        storeV_nt<V>(at_byte(static_cast<T*>(p.dr) + base, off[k]), u);
+        if (p.di) {
+#pragma unroll
+          for (int c = 0; c < V; ++c) t[c] = dx[c] * x[k].get(c) * (1.f - sigm(g[k].get(c)));
+          storeV_nt<V>(at_byte(static_cast<T*>(p.di) + base, off[k]), t);
+        }
         if (p.dz) {
 #pragma unroll
           for (int c = 0; c < V; ++c) {
             const float zv = z[k].get(c), sz = sigm(zv);
-            const float hv = __builtin_fmaf(a[k][c], h[k][c], bt[k][c] * pi[k][c] * x[k].get(c));
-            dz[c] = dy[k].get(c) * hv * (sz * __builtin_fmaf(zv, 1.f - sz, 1.f));
+            t[c] = dy[k].get(c) * hv[c] * (sz * __builtin_fmaf(zv, 1.f - sz, 1.f));
           }
-          storeV<V>(static_cast<T*>(p.dz) + base + off[k], dz);
+          storeV_nt<V>(at_byte(static_cast<T*>(p.dz) + base, off[k]), t);
         }
       }
     }
-    if (p.dinit && tile == 0 && wave == 0 && seg == 0 && dok) {
-#pragma unroll
-      for (int c = 0; c < V; ++c) p.dinit[(int64_t)b * D + d0 + c] = carry[c];
-    }
     if (LAM && p.dlam_part && step + 1 == step_end) {
-      // sum over the positions of the workgroup, in a fixed order
-      __syncthreads();
+      // sum over the positions of the workgroup, in a fixed order (sG was last read before the second barrier)
 #pragma unroll
       for (int c = 0; c < V; ++c) {
         dlam[c] += __shfl_down(dlam[c], 32);
         dlam[c] += __shfl_down(dlam[c], 16);
-        if (seg == 0) sG[buf][wave][cl * V + c] = dlam[c];
       }
+      if (seg == 0) lds_put(&sG[wave][cl * V], dlam);
       __syncthreads();
-      if (wave == 0 && dblk + lane < D) {
-        float s = sG[buf][0][lane];
+      if (wave == 0 && cok) {
+        float s = sG[0][lane];
 #pragma unroll
-        for (int w = 1; w < NW; ++w) s += sG[buf][w][lane];
+        for (int u = 1; u < NW; ++u) s += sG[u][lane];
         p.dlam_part[((int64_t)b * (CHAIN ? p.ntiles : 1) + (CHAIN ? step : 0)) * D + dblk + lane] = s;
       }
     }
@@ -660,12 +757,12 @@ __global__ void __launch_bounds__(256) glr_step_kernel(float* state, const void*
   float h[V], y[V];
 #pragma unroll
   for (int c = 0; c < V; ++c) {
-    float q, omq, a, beta, v = xv.get(c);
-    sigm2(rv.get(c), q, omq);
+    float q, omq, a, base, v = xv.get(c);
+    glr_sigm<LAM>(rv.get(c), q, omq);
     const float rate = LAM ? scale * softplus_rel(lam[d + c]) : 0.f;
-    glr_decay<RULE, LAM>(q, omq, rate, rate * kLog2e, a, beta);
+    glr_decay<RULE, LAM>(q, omq, rate, rate * kLog2e, a, base);
     if (i) v *= sigm(iv.get(c));
-    h[c] = __builtin_fmaf(a, hv.get(c), beta * v);
+    h[c] = __builtin_fmaf(a, hv.get(c), glr_beta<RULE>(base) * v);
     y[c] = z ? h[c] * silu_f(zv.get(c)) : h[c];
   }
   storeV<V>(state + e, h);

@@ -88,7 +88,7 @@ int norm_plan(const mamba_norm_dims* g, NormPlan* pl) {
   if (g->batch * pl->chunks > INT32_MAX || g->batch * g->groups > ((int64_t)1 << 32)) return MAMBA_ERR_UNSUPPORTED;
   pl->bwd_rows = (int)(pl->chunks > 1 ? g->batch * pl->chunks : g->batch < 2 * MSCAN_NORM_BLOCKS ? g->batch : 2 * MSCAN_NORM_BLOCKS);
   pl->lds = ((size_t)2 * pl->slots * g->dim + 2 * g->groups) * sizeof(float);
-  pl->pg = pl->chunks > 1 ? up256((size_t)g->batch * pl->chunks * g->groups * sizeof(float2)) : 0;
+  pl->pg = pl->chunks > 1 ? up256((size_t)g->batch * (pl->chunks + 1) * g->groups * sizeof(float2)) : 0;
   pl->pc = up256((size_t)pl->bwd_rows * g->dim * sizeof(float2));
   row_plan(g, pl);
   if (pl->v > 0) pl->chunks = 1, pl->chunk_len = 1, pl->pg = 0;
@@ -99,7 +99,6 @@ void norm_params(const mamba_norm_dims* g, const NormPlan& pl, NormParams* p) {
   p->B = (int)g->batch, p->L = (int)g->seqlen, p->D = (int)g->dim, p->G = (int)g->groups, p->C = p->D / p->G;
   p->nv = pl.nv, p->slots = pl.slots, p->chunks = pl.chunks, p->chunk_len = pl.chunk_len;
   p->lpg = pow2_at_least(p->C < 64 ? p->C : 64);
-  p->lpc = pow2_at_least(p->chunks < 64 ? p->chunks : 64);
   p->eps = g->eps;
 }
 
@@ -183,6 +182,7 @@ int mamba_group_norm_fwd(const void* x, const float* weight, const float* bias, 
   norm_params(dims, pl, &p);
   p.x = x, p.w = weight, p.bias = bias, p.out = out, p.mean = mean, p.rstd = rstd;
   p.pg = static_cast<float2*>(dims->workspace);
+  p.st = p.pg + (size_t)p.B * p.G * p.chunks;
   if (pl.v > 0) {
     NormRowParams r = row_params(dims, pl);
     r.x = x, r.w = weight, r.bias = bias, r.out = out, r.mean = mean, r.rstd = rstd;
@@ -204,7 +204,8 @@ int mamba_group_norm_fwd(const void* x, const float* weight, const float* bias, 
     } else {
       ok = lds_ok(norm_stats_kernel<T>, pl.lds);
       if (ok) norm_stats_kernel<T><<<grid, pl.threads, pl.lds, stream>>>(p);
-      if (ok) norm_apply_kernel<T, A><<<grid, pl.threads, 2 * p.G * sizeof(float), stream>>>(p);
+      if (ok) norm_join_kernel<<<(unsigned)(((int64_t)p.B * p.G + 3) / 4), 256, 0, stream>>>(p);
+      if (ok) norm_apply_kernel<T, A><<<grid, pl.threads, 0, stream>>>(p);
     }
   });
   return ok && hipGetLastError() == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
@@ -226,6 +227,7 @@ int mamba_group_norm_bwd(const void* x, const float* weight, const float* bias, 
   p.x = x, p.w = weight, p.bias = bias, p.dout = dout, p.dx = dx;
   p.mean = const_cast<float*>(mean), p.rstd = const_cast<float*>(rstd);
   p.pg = static_cast<float2*>(dims->workspace);
+  p.st = p.pg + (size_t)p.B * p.G * p.chunks;
   p.pc = reinterpret_cast<float2*>(static_cast<char*>(dims->workspace) + pl.pg);
   p.want_dw = dweight || dbias;
   bool ok = true;
@@ -250,7 +252,8 @@ int mamba_group_norm_bwd(const void* x, const float* weight, const float* bias, 
       const unsigned grid = (unsigned)(p.B * p.chunks);
       ok = lds_ok(norm_bwd_sums_kernel<T, A>, pl.lds);
       if (ok) norm_bwd_sums_kernel<T, A><<<grid, pl.threads, pl.lds, stream>>>(p);
-      if (ok) norm_bwd_dx_kernel<T, A><<<grid, pl.threads, 2 * p.G * sizeof(float), stream>>>(p);
+      if (ok) norm_bwd_join_kernel<<<(unsigned)(((int64_t)p.B * p.G + 3) / 4), 256, 0, stream>>>(p);
+      if (ok) norm_bwd_dx_kernel<T, A><<<grid, pl.threads, 0, stream>>>(p);
     }
   });
   if (!ok || hipGetLastError() != hipSuccess) return MAMBA_ERR_HIP;

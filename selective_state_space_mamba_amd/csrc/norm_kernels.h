@@ -39,20 +39,70 @@ struct NormParams {
   float *mean, *rstd; // [B][G]; written by the forward (may be null), read by the backward
   const void* dout;   // [B][L][D]
   void* dx;           // [B][L][D]
-  float2* pg;         // [B][chunks][G]: (mean, M) forward, (Σ t, Σ t·xh) backward
+  float2* pg;         // [B][G][chunks]: (mean, M) forward, (Σ t, Σ t·xh) backward
+  float2* st;         // [B][G]: (mean, rstd) forward, (Σ t, Σ t·xh)/n backward
   float2* pc;         // [rows of partials][D]: (Σ du, Σ du·xh)
-  int B, L, D, G, C, nv, slots, chunks, chunk_len, lpg, lpc, want_dw;
+  int B, L, D, G, C, nv, slots, chunks, chunk_len, lpg, want_dw;
   float eps;
 };
 
-__device__ __forceinline__ void vstore(uint16_t* p, const float (&y)[8]) { storeV<8>(p, y); }
-__device__ __forceinline__ void vstore(float* p, const float (&y)[8]) { storeV<8>(p, y); }
+__device__ __forceinline__ void vstore(uint16_t* p, const float (&y)[8]) { storeV_nt<8>(p, y); }
+__device__ __forceinline__ void vstore(float* p, const float (&y)[8]) { storeV_nt<8>(p, y); }
 
 // Sum over `width` (a power of two up to 64) neighbouring lanes, left in each of them.
 __device__ __forceinline__ float lane_sum(float v, int width) {
   for (int o = width >> 1; o > 0; o >>= 1) v += __shfl_xor(v, o);
   return v;
 }
+
+// The rows l0 + slot, l0 + slot + slots, ... below l1 of one column of vectors
+// (of two tensors of the same layout where NS = 2), U rows at a time: the next
+// rows' loads are issued before the current ones are used, and the first ones
+// by start(), before whatever else a kernel has to fetch.  Rows past the end
+// repeat the last one and are not used.
+template <typename T, int NS, int U>
+struct RowWalk {
+  const T* src[NS];
+  int64_t at, step;  // first row's vector, distance between a thread's rows (elements)
+  int n;             // rows of this thread
+  Vec<T, 8> cur[NS][U], nxt[NS][U];
+
+  __device__ __forceinline__ void fetch(Vec<T, 8> (&v)[NS][U], int r) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t a = at + min(r + u, n - 1) * step;
+#pragma unroll
+      for (int k = 0; k < NS; ++k) v[k][u].load(src[k] + a);
+    }
+  }
+  __device__ __forceinline__ void start(const NormParams& p, const T* a, const T* b, int l0, int l1) {
+    const int slot = threadIdx.x / p.nv, col = threadIdx.x % p.nv;
+    src[0] = a;
+    if constexpr (NS > 1) src[1] = b;
+    at = (int64_t)(l0 + slot) * p.D + col * 8;
+    step = (int64_t)p.slots * p.D;
+    n = slot < p.slots && l0 + slot < l1 ? (l1 - l0 - slot + p.slots - 1) / p.slots : 0;
+    if (n > 0) fetch(cur, 0);
+  }
+  // f(vectors of one row, its element offset)
+  template <typename F>
+  __device__ __forceinline__ void walk(F f) {
+    for (int r = 0; r < n; r += U) {
+      if (r + U < n) fetch(nxt, r + U);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (r + u < n) {
+          if constexpr (NS > 1) f(cur[0][u], cur[1][u], at + (r + u) * step);
+          else f(cur[0][u], at + (r + u) * step);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < NS; ++k)
+#pragma unroll
+        for (int u = 0; u < U; ++u) cur[k][u] = nxt[k][u];
+    }
+  }
+};
 
 // ---- pieces of a workgroup's work; red: 2·slots·D floats of LDS ----
 
@@ -64,23 +114,20 @@ __device__ __forceinline__ void rows_stats(const NormParams& p, const T* xb, int
   const bool on = slot < p.slots;
   float s[8], q[8], sh[8];
   if (on) {
+    RowWalk<T, 1, 4> rows;
+    rows.start(p, xb, nullptr, l0, l1);
     Vec<T, 8> v;
     v.load(xb + (int64_t)l0 * D + col * 8);
 #pragma unroll
     for (int j = 0; j < 8; ++j) sh[j] = v.get(j), s[j] = 0.f, q[j] = 0.f;
-    const T* px = xb + (int64_t)(l0 + slot) * D + col * 8;
-    const int64_t step = (int64_t)p.slots * D;
-#pragma unroll 4
-    for (int l = l0 + slot; l < l1; l += p.slots, px += step) {
-      Vec<T, 8> r;
-      r.load(px);
+    rows.walk([&](const Vec<T, 8>& r, int64_t) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float d = r.get(j) - sh[j];
         s[j] += d;
         q[j] = __builtin_fmaf(d, d, q[j]);
       }
-    }
+    });
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       red[slot * D + col * 8 + j] = s[j];
@@ -119,31 +166,28 @@ __device__ __forceinline__ void join_channels(const NormParams& p, const float* 
   }
 }
 
-// Normalises rows [l0, l1); mean and rstd of the item's groups in LDS.
-template <typename T, int ACT>
-__device__ __forceinline__ void rows_apply(const NormParams& p, const T* xb, T* ob, int l0, int l1, const float* sMean,
-                                           const float* sRstd) {
-  const int tid = threadIdx.x, slot = tid / p.nv, col = tid % p.nv, D = p.D;
-  if (slot >= p.slots) return;
+// Normalises rows [l0, l1); stats(g): mean and rstd of a group of the item.
+template <typename T, int ACT, typename F>
+__device__ __forceinline__ void rows_apply(const NormParams& p, const T* xb, T* ob, int l0, int l1, F stats) {
+  if ((int)threadIdx.x / p.nv >= p.slots) return;
+  const int col = threadIdx.x % p.nv;
+  RowWalk<T, 1, 4> rows;
+  rows.start(p, xb, nullptr, l0, l1);
   float mu[8], sc[8], bi[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int d = col * 8 + j, g = d / p.C;
-    mu[j] = sMean[g];
-    sc[j] = sRstd[g] * (p.w ? p.w[d] : 1.f);
+    const int d = col * 8 + j;
+    const float2 st = stats(d / p.C);
+    mu[j] = st.x;
+    sc[j] = st.y * (p.w ? p.w[d] : 1.f);
     bi[j] = p.bias ? p.bias[d] : 0.f;
   }
-  const int64_t step = (int64_t)p.slots * D;
-  int64_t at = (int64_t)(l0 + slot) * D + col * 8;
-#pragma unroll 4
-  for (int l = l0 + slot; l < l1; l += p.slots, at += step) {
-    Vec<T, 8> v;
-    v.load(xb + at);
+  rows.walk([&](const Vec<T, 8>& v, int64_t at) {
     float y[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] = act_f<ACT>(__builtin_fmaf(v.get(j) - mu[j], sc[j], bi[j]));
     vstore(ob + at, y);
-  }
+  });
 }
 
 // ---- forward ----
@@ -166,7 +210,8 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_item_kernel(const NormPa
     if (p.rstd) p.rstd[(int64_t)b * p.G + g] = r;
   });
   __syncthreads();
-  rows_apply<T, ACT>(p, xb, static_cast<T*>(p.out) + (int64_t)b * p.L * p.D, 0, p.L, sMean, sRstd);
+  rows_apply<T, ACT>(p, xb, static_cast<T*>(p.out) + (int64_t)b * p.L * p.D, 0, p.L,
+                     [&](int g) { return make_float2(sMean[g], sRstd[g]); });
 }
 
 // Larger items in runs of rows: the runs' statistics, then the rows.
@@ -177,44 +222,41 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_stats_kernel(const NormP
   const int l0 = k * p.chunk_len, l1 = min(p.L, l0 + p.chunk_len);
   rows_stats<T>(p, static_cast<const T*>(p.x) + (int64_t)b * p.L * p.D, l0, l1, lds);
   join_channels(p, lds, (float)(l1 - l0),
-                [&](int g, float m, float q) { p.pg[((int64_t)b * p.chunks + k) * p.G + g] = make_float2(m, q); });
+                [&](int g, float m, float q) { p.pg[((int64_t)b * p.G + g) * p.chunks + k] = make_float2(m, q); });
+}
+
+// Joins the runs of every item: a wave a group.  (Doing it at the start of
+// every workgroup of the next kernel saves the launch, and cost 5 us of loads
+// and sums one after the other for 32 runs, 60 for 512.)
+static __global__ void __launch_bounds__(256) norm_join_kernel(const NormParams p) {
+  const int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (u >= (int64_t)p.B * p.G) return;
+  const int lane = threadIdx.x & 63;
+  const float2* const pg = p.pg + u * p.chunks;
+  float m = 0.f, q = 0.f;
+  for (int c = lane; c < p.chunks; c += 64) m = __builtin_fmaf((float)min(p.chunk_len, p.L - c * p.chunk_len), pg[c].x, m);
+  m = lane_sum(m, 64) / (float)p.L;
+  for (int c = lane; c < p.chunks; c += 64) {
+    const float2 v = pg[c];
+    const float d = v.x - m, cnt = (float)min(p.chunk_len, p.L - c * p.chunk_len) * (float)p.C;
+    q += __builtin_fmaf(cnt * d, d, v.y);
+  }
+  q = lane_sum(q, 64);
+  if (lane == 0) {
+    const float r = 1.0f / __builtin_sqrtf(q / ((float)p.L * (float)p.C) + p.eps);
+    p.st[u] = make_float2(m, r);
+    if (p.mean) p.mean[u] = m;
+    if (p.rstd) p.rstd[u] = r;
+  }
 }
 
 template <typename T, int ACT>
 __global__ void __launch_bounds__(kNormMaxThreads) norm_apply_kernel(const NormParams p) {
-  extern __shared__ float lds[];
-  float *const sMean = lds, *const sRstd = lds + p.G;
   const int b = blockIdx.x / p.chunks, k = blockIdx.x % p.chunks;
-  const int l0 = k * p.chunk_len, l1 = min(p.L, l0 + p.chunk_len);
-  // every workgroup joins the item's runs (the same way, to the same bits)
-  const float2* const pg = p.pg + (int64_t)b * p.chunks * p.G;
-  const int li = threadIdx.x % p.lpc, per = blockDim.x / p.lpc;
-  for (int g0 = 0; g0 < p.G; g0 += per) {
-    const int g = g0 + threadIdx.x / p.lpc;
-    const bool on = g < p.G;
-    float m = 0.f, q = 0.f;
-    if (on)
-      for (int c = li; c < p.chunks; c += p.lpc)
-        m = __builtin_fmaf((float)min(p.chunk_len, p.L - c * p.chunk_len), pg[(int64_t)c * p.G + g].x, m);
-    m = lane_sum(m, p.lpc) / (float)p.L;
-    if (on)
-      for (int c = li; c < p.chunks; c += p.lpc) {
-        const float2 v = pg[(int64_t)c * p.G + g];
-        const float d = v.x - m, cnt = (float)min(p.chunk_len, p.L - c * p.chunk_len) * (float)p.C;
-        q += __builtin_fmaf(cnt * d, d, v.y);
-      }
-    q = lane_sum(q, p.lpc);
-    if (on && li == 0) {
-      const float r = 1.0f / __builtin_sqrtf(q / ((float)p.L * (float)p.C) + p.eps);
-      sMean[g] = m;
-      sRstd[g] = r;
-      if (k == 0 && p.mean) p.mean[(int64_t)b * p.G + g] = m;
-      if (k == 0 && p.rstd) p.rstd[(int64_t)b * p.G + g] = r;
-    }
-  }
-  __syncthreads();
   const int64_t base = (int64_t)b * p.L * p.D;
-  rows_apply<T, ACT>(p, static_cast<const T*>(p.x) + base, static_cast<T*>(p.out) + base, l0, l1, sMean, sRstd);
+  const float2* const st = p.st + (int64_t)b * p.G;
+  rows_apply<T, ACT>(p, static_cast<const T*>(p.x) + base, static_cast<T*>(p.out) + base, k * p.chunk_len,
+                     min(p.L, (k + 1) * p.chunk_len), [&](int g) { return st[g]; });
 }
 
 // ---- backward ----
@@ -235,19 +277,15 @@ struct NormCol {  // a thread's eight channels of one item
 
 // Per-channel Σ du and Σ du·xh of rows [l0, l1), a thread's own rows in s, q.
 template <typename T, int ACT>
-__device__ __forceinline__ void rows_grad_sums(const NormParams& p, const T* xb, const T* yb, int l0, int l1, const NormCol& k,
+__device__ __forceinline__ void rows_grad_sums(const NormParams& p, int b, const T* xb, const T* yb, int l0, int l1, NormCol& k,
                                                float (&s)[8], float (&q)[8]) {
-  const int slot = threadIdx.x / p.nv, col = threadIdx.x % p.nv;
 #pragma unroll
   for (int j = 0; j < 8; ++j) s[j] = 0.f, q[j] = 0.f;
-  if (slot >= p.slots) return;
-  const int64_t step = (int64_t)p.slots * p.D;
-  int64_t at = (int64_t)(l0 + slot) * p.D + col * 8;
-#pragma unroll 2
-  for (int l = l0 + slot; l < l1; l += p.slots, at += step) {
-    Vec<T, 8> v, dy;
-    v.load(xb + at);
-    dy.load(yb + at);
+  if ((int)threadIdx.x / p.nv >= p.slots) return;
+  RowWalk<T, 2, 2> rows;
+  rows.start(p, xb, yb, l0, l1);
+  k.load(p, b, threadIdx.x % p.nv);
+  rows.walk([&](const Vec<T, 8>& v, const Vec<T, 8>& dy, int64_t) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float xh = (v.get(j) - k.mu[j]) * k.rs[j];
@@ -255,7 +293,7 @@ __device__ __forceinline__ void rows_grad_sums(const NormParams& p, const T* xb,
       s[j] += du;
       q[j] = __builtin_fmaf(du, xh, q[j]);
     }
-  }
+  });
 }
 
 // The rows' sums of the workgroup joined per channel in red (layout of rows_stats).
@@ -299,22 +337,23 @@ __device__ __forceinline__ void join_grad_groups(const NormParams& p, const floa
   }
 }
 
-// dx of rows [l0, l1); sA, sB: (Σ t)/n and (Σ t·xh)/n of the item's groups.
-template <typename T, int ACT>
-__device__ __forceinline__ void rows_dx(const NormParams& p, const T* xb, const T* yb, T* ob, int l0, int l1, const NormCol& k,
-                                        const float* sA, const float* sB) {
-  const int slot = threadIdx.x / p.nv, col = threadIdx.x % p.nv;
-  if (slot >= p.slots) return;
+// dx of rows [l0, l1); sums(g): (Σ t)/n and (Σ t·xh)/n of a group of the item.
+template <typename T, int ACT, typename F>
+__device__ __forceinline__ void rows_dx(const NormParams& p, int b, const T* xb, const T* yb, T* ob, int l0, int l1, F sums) {
+  if ((int)threadIdx.x / p.nv >= p.slots) return;
+  const int col = threadIdx.x % p.nv;
+  RowWalk<T, 2, 2> rows;
+  rows.start(p, xb, yb, l0, l1);
+  NormCol k;
+  k.load(p, b, col);
   float ma[8], mb[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) ma[j] = sA[(col * 8 + j) / p.C], mb[j] = sB[(col * 8 + j) / p.C];
-  const int64_t step = (int64_t)p.slots * p.D;
-  int64_t at = (int64_t)(l0 + slot) * p.D + col * 8;
-#pragma unroll 2
-  for (int l = l0 + slot; l < l1; l += p.slots, at += step) {
-    Vec<T, 8> v, dy;
-    v.load(xb + at);
-    dy.load(yb + at);
+  for (int j = 0; j < 8; ++j) {
+    const float2 v = sums((col * 8 + j) / p.C);
+    ma[j] = v.x;
+    mb[j] = v.y;
+  }
+  rows.walk([&](const Vec<T, 8>& v, const Vec<T, 8>& dy, int64_t at) {
     float y[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -323,7 +362,7 @@ __device__ __forceinline__ void rows_dx(const NormParams& p, const T* xb, const 
       y[j] = k.rs[j] * (t - ma[j] - xh * mb[j]);
     }
     vstore(ob + at, y);
-  }
+  });
 }
 
 // One workgroup walks items blockIdx.x, blockIdx.x + gridDim.x, ...; its share of dw and dbias is one row of pc.
@@ -332,7 +371,6 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_bwd_item_kernel(const No
   extern __shared__ float lds[];
   float* const sA = lds + 2 * p.slots * p.D;
   float* const sB = sA + p.G;
-  const int slot = threadIdx.x / p.nv, col = threadIdx.x % p.nv;
   const float inv = 1.0f / ((float)p.L * (float)p.C);
   float ts[8], tq[8];
 #pragma unroll
@@ -342,15 +380,15 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_bwd_item_kernel(const No
     const T* const xb = static_cast<const T*>(p.x) + base;
     const T* const yb = static_cast<const T*>(p.dout) + base;
     NormCol k;
-    if (slot < p.slots) k.load(p, b, col);
     float s[8], q[8];
-    rows_grad_sums<T, ACT>(p, xb, yb, 0, p.L, k, s, q);
+    rows_grad_sums<T, ACT>(p, b, xb, yb, 0, p.L, k, s, q);
 #pragma unroll
     for (int j = 0; j < 8; ++j) ts[j] += s[j], tq[j] += q[j];
     join_slots(p, s, q, lds);
     join_grad_groups(p, lds, [&](int g, float a, float c) { sA[g] = a * inv, sB[g] = c * inv; });
     __syncthreads();
-    rows_dx<T, ACT>(p, xb, yb, static_cast<T*>(p.dx) + base, 0, p.L, k, sA, sB);
+    rows_dx<T, ACT>(p, b, xb, yb, static_cast<T*>(p.dx) + base, 0, p.L,
+                    [&](int g) { return make_float2(sA[g], sB[g]); });
   }
   if (p.want_dw) {
     join_slots(p, ts, tq, lds);
@@ -366,45 +404,39 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_bwd_sums_kernel(const No
   const int l0 = ch * p.chunk_len, l1 = min(p.L, l0 + p.chunk_len);
   const int64_t base = (int64_t)b * p.L * p.D;
   NormCol k;
-  if (threadIdx.x / p.nv < p.slots) k.load(p, b, threadIdx.x % p.nv);
   float s[8], q[8];
-  rows_grad_sums<T, ACT>(p, static_cast<const T*>(p.x) + base, static_cast<const T*>(p.dout) + base, l0, l1, k, s, q);
+  rows_grad_sums<T, ACT>(p, b, static_cast<const T*>(p.x) + base, static_cast<const T*>(p.dout) + base, l0, l1, k, s, q);
   join_slots(p, s, q, lds);
   if (p.want_dw) {
     const int n = p.slots * p.D;
     for (int c = threadIdx.x; c < p.D; c += blockDim.x) p.pc[(int64_t)blockIdx.x * p.D + c] = make_float2(lds[c], lds[n + c]);
   }
-  join_grad_groups(p, lds, [&](int g, float a, float c) { p.pg[(int64_t)blockIdx.x * p.G + g] = make_float2(a, c); });
+  join_grad_groups(p, lds, [&](int g, float a, float c) { p.pg[((int64_t)b * p.G + g) * p.chunks + ch] = make_float2(a, c); });
+}
+
+static __global__ void __launch_bounds__(256) norm_bwd_join_kernel(const NormParams p) {
+  const int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (u >= (int64_t)p.B * p.G) return;
+  const int lane = threadIdx.x & 63;
+  float a = 0.f, c2 = 0.f;
+  for (int c = lane; c < p.chunks; c += 64) {
+    const float2 v = p.pg[u * p.chunks + c];
+    a += v.x;
+    c2 += v.y;
+  }
+  a = lane_sum(a, 64);
+  c2 = lane_sum(c2, 64);
+  const float inv = 1.0f / ((float)p.L * (float)p.C);
+  if (lane == 0) p.st[u] = make_float2(a * inv, c2 * inv);
 }
 
 template <typename T, int ACT>
 __global__ void __launch_bounds__(kNormMaxThreads) norm_bwd_dx_kernel(const NormParams p) {
-  extern __shared__ float lds[];
-  float *const sA = lds, *const sB = lds + p.G;
   const int b = blockIdx.x / p.chunks, ch = blockIdx.x % p.chunks;
-  const int l0 = ch * p.chunk_len, l1 = min(p.L, l0 + p.chunk_len);
-  const float inv = 1.0f / ((float)p.L * (float)p.C);
-  const float2* const pg = p.pg + (int64_t)b * p.chunks * p.G;
-  const int li = threadIdx.x % p.lpc, per = blockDim.x / p.lpc;
-  for (int g0 = 0; g0 < p.G; g0 += per) {
-    const int g = g0 + threadIdx.x / p.lpc;
-    float a = 0.f, c2 = 0.f;
-    if (g < p.G)
-      for (int c = li; c < p.chunks; c += p.lpc) {
-        const float2 v = pg[(int64_t)c * p.G + g];
-        a += v.x;
-        c2 += v.y;
-      }
-    a = lane_sum(a, p.lpc);
-    c2 = lane_sum(c2, p.lpc);
-    if (g < p.G && li == 0) sA[g] = a * inv, sB[g] = c2 * inv;
-  }
-  __syncthreads();
   const int64_t base = (int64_t)b * p.L * p.D;
-  NormCol k;
-  if (threadIdx.x / p.nv < p.slots) k.load(p, b, threadIdx.x % p.nv);
-  rows_dx<T, ACT>(p, static_cast<const T*>(p.x) + base, static_cast<const T*>(p.dout) + base, static_cast<T*>(p.dx) + base, l0, l1, k,
-                  sA, sB);
+  const float2* const st = p.st + (int64_t)b * p.G;
+  rows_dx<T, ACT>(p, b, static_cast<const T*>(p.x) + base, static_cast<const T*>(p.dout) + base, static_cast<T*>(p.dx) + base,
+                  ch * p.chunk_len, min(p.L, (ch + 1) * p.chunk_len), [&](int g) { return st[g]; });
 }
 
 // ---- single tokens ----
@@ -426,7 +458,7 @@ __device__ __forceinline__ void row_load(const T* p, float (&f)[V]) {
 template <typename T, int V>
 __device__ __forceinline__ void row_store(T* p, const float (&f)[V]) {
   if constexpr (V == 1) store1(p, f[0]);
-  else storeV<V>(p, f);
+  else storeV_nt<V>(p, f);
 }
 template <int V>
 __device__ __forceinline__ void row_param(const float* p, int d, float fill, float (&f)[V]) {

@@ -87,6 +87,8 @@ CASES = [
     # enough rows for one workgroup to walk all its tiles
     (40, 200, 1664, "bf16", "sqrt", False, {}),
     (33, 131, 2052, "f32", "lerp", True, dict(reset=0.02)),
+    (64, 140, 2080, "f32", "unit", False, dict(reset=0.02)),
+    (64, 70, 2052, "bf16", "sqrt", True, dict(lam=False)),
 ]
 
 
