@@ -17,41 +17,53 @@ int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 constexpr int kRowsMax = 64;  // rows that linear_rows_kernel takes
 
-#ifndef MSCAN_LINEAR_TILE
-#define MSCAN_LINEAR_TILE 128, 128, 2, 2
-#endif
-constexpr int kTile[4] = {MSCAN_LINEAR_TILE};
-
-#ifndef MSCAN_LINEAR_WGS
-#define MSCAN_LINEAR_WGS 512  // workgroups wanted before a contraction is left whole
-#endif
-
 // How one product of the three is run.
+enum { TILE_128 = 0, TILE_256x192 = 1, TILE_256x256 = 2 };
 struct ProductPlan {
-  int bm, bn, tiles_m, tiles_n, splits, kt_per_split;
+  int tile, tiles_m, tiles_n, splits, kt_per_split;
   size_t part;  // bytes
 };
 
+#ifndef MSCAN_LINEAR_FORCE
+#define MSCAN_LINEAR_FORCE -1
+#endif
+
+// The tile and the number of shares of the contraction with the least expected
+// time.  A round of workgroups (two a compute unit with the small tile, one
+// with the large ones; 256 compute units) takes, in us, a start and an end plus
+// a time for each contraction element, as measured on MI355X in bf16:
+//   128 x 128   5.8 + 0.0158 K   (16384 x 768 x 1536: 3 rounds, 53.8; 65536 x 2048 x 2048: 16 rounds, 610)
+//   256 x 192   7.8 + 0.0217 K   (16384 x 768 x 1536: 2 rounds, 49.0; 16384 x 1536 x 768: 1 round, 41.2)
+//   256 x 256   6.4 + 0.0293 K   (16384 x 768 x 1536: 2 rounds, 57.8; 65536 x 2048 x 2048: 8 rounds, 531)
+// so that how evenly the tiles fill the rounds decides.  A contraction is
+// shared out where the tiles alone leave compute units idle, in shares of at
+// least 8 stages; the shares' sums then cost a launch and their bytes, written
+// and read.  float32 products are bound by the matrix instructions' rate (a
+// sixteenth of bf16's) with any tile and take the small one.
 ProductPlan plan_product(int64_t M, int64_t N, int64_t K, bool bf16) {
-  ProductPlan pl;
+  static const struct { int bm, bn, slots; double fix, per; } kTiles[3] = {
+      {128, 128, 512, 5.8, 0.0158}, {256, 192, 256, 7.8, 0.0217}, {256, 256, 256, 6.4, 0.0293}};
   const int bk = bf16 ? 64 : 32;
-  pl.bm = kTile[0], pl.bn = kTile[1];
-  pl.tiles_m = ceil_div(M, pl.bm);
-  pl.tiles_n = ceil_div(N, pl.bn);
-  const int64_t tiles = (int64_t)pl.tiles_m * pl.tiles_n;
-  const int kts = ceil_div(K, bk);
-  // A contraction is shared out where the tiles alone leave compute units
-  // idle; a share has at least 8 stages.
-  int64_t splits = 1;
-  if (tiles < MSCAN_LINEAR_WGS / 2) {
-    splits = MSCAN_LINEAR_WGS / tiles;
-    if (splits > kts / 8) splits = kts / 8;
-    if (splits < 1) splits = 1;
+  const int64_t kts = (K + bk - 1) / bk;
+  ProductPlan best{};
+  double best_us = 1e300;
+  for (int t = 0; t < (bf16 ? 3 : 1); ++t) {
+    if (MSCAN_LINEAR_FORCE >= 0 && bf16 && t != MSCAN_LINEAR_FORCE) continue;
+    const int64_t tm = (M + kTiles[t].bm - 1) / kTiles[t].bm, tn = (N + kTiles[t].bn - 1) / kTiles[t].bn, tiles = tm * tn;
+    int64_t most = tiles < kTiles[t].slots ? kTiles[t].slots / tiles : 1;
+    if (most > kts / 8) most = kts / 8 > 0 ? kts / 8 : 1;
+    for (int64_t s : {(int64_t)1, most}) {
+      const int64_t per = (kts + s - 1) / s, splits = (kts + per - 1) / per;
+      const int64_t rounds = (tiles * splits + kTiles[t].slots - 1) / kTiles[t].slots;
+      double us = (double)rounds * (kTiles[t].fix + kTiles[t].per * (double)(per * bk) * (bf16 ? 1 : 16));
+      if (splits > 1) us += 4.0 + (double)splits * (double)M * (double)N * 8.0 / 5.0e6;
+      if (us < best_us) {
+        best_us = us;
+        best = ProductPlan{t, (int)tm, (int)tn, (int)splits, (int)per, splits > 1 ? up256((size_t)splits * M * N * sizeof(float)) : 0};
+      }
+    }
   }
-  pl.kt_per_split = ceil_div(kts, splits);
-  pl.splits = ceil_div(kts, pl.kt_per_split);
-  pl.part = pl.splits > 1 ? up256((size_t)pl.splits * M * N * sizeof(float)) : 0;
-  return pl;
+  return best;
 }
 
 int check(const mamba_linear_dims* g) {
@@ -90,7 +102,13 @@ hipError_t product(LinearParams p, const ProductPlan& pl, hipStream_t stream) {
   p.tiles_m = pl.tiles_m, p.tiles_n = pl.tiles_n, p.splits = pl.splits, p.kt_per_split = pl.kt_per_split;
   if (pl.splits == 1) p.part = nullptr;
   const dim3 grid((unsigned)((int64_t)pl.tiles_m * pl.tiles_n), (unsigned)pl.splits);
-  linear_tile_kernel<T, TA, TB, MSCAN_LINEAR_TILE><<<grid, 64 * kTile[2] * kTile[3], 0, stream>>>(p);
+  if constexpr (sizeof(T) == 2) {
+    if (pl.tile == TILE_256x256) linear_large_kernel<T, TA, TB, 256, 2, 4><<<grid, 512, 0, stream>>>(p);
+    else if (pl.tile == TILE_256x192) linear_large_kernel<T, TA, TB, 192, 4, 2><<<grid, 512, 0, stream>>>(p);
+    else linear_tile_kernel<T, TA, TB><<<grid, 256, 0, stream>>>(p);
+  } else {
+    linear_tile_kernel<T, TA, TB><<<grid, 256, 0, stream>>>(p);
+  }
   if (pl.splits > 1) {
     const int64_t quads = (int64_t)p.M * p.N / 4;
     linear_join_kernel<T><<<(unsigned)((quads + 255) / 256), 256, 0, stream>>>(p);

@@ -7,9 +7,8 @@
 // One tile kernel does the three products.  Each operand lies in memory with
 // its contraction axis contiguous (x, W and dP of the forward and of dx) or
 // with the rows of the contraction one after the other (W of dx; dP and x of
-// dW); it is staged in LDS as it lies, 128 bytes of contraction deep, and the
-// second kind is turned on the way to the registers by the transposing LDS
-// read (bf16: 16 lanes read 4 contraction rows of 16 columns, lane i receives
+// dW); it is staged in LDS as it lies and the second kind is turned on the way
+// to the registers by the transposing LDS read (bf16: 16 lanes read 4 contraction rows of 16 columns, lane i receives
 // column i).  Products are 32 x 32 x 16 (bf16) or 32 x 32 x 2 (float32) matrix
 // instructions with float32 sums; the output's column axis N takes the
 // instruction's row side, which leaves each lane with four neighbouring
@@ -40,26 +39,74 @@ struct LinearParams {
   int act, splits, kt_per_split, tiles_m, tiles_n;
 };
 
-// One output quadruple: columns n..n+3 of row m.
-template <typename T>
-__device__ __forceinline__ void linear_finish(const LinearParams& p, int m, int n, float (&v)[4]) {
-  const int64_t at = (int64_t)m * p.N + n;
-  if (p.bias) {
+// V neighbouring outputs of one row, whose bias and residual are at hand.
+template <typename T, int V>
+__device__ __forceinline__ void linear_finish(const LinearParams& p, int64_t at, const float (&bias)[V], const Vec<T, V>& res,
+                                              float (&v)[V]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] += p.bias[n + j];
-  }
-  if (p.pre) storeV<4>(p.pre + at, v);
+  for (int j = 0; j < V; ++j) v[j] += bias[j];
+  if (p.pre) storeV_nt<V>(p.pre + at, v);
   if (p.act != ACT_NONE) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = act_any(v[j], p.act);
+    for (int j = 0; j < V; ++j) v[j] = act_any(v[j], p.act);
   }
   if (p.residual) {
-    Vec<T, 4> r;
-    r.load(static_cast<const T*>(p.residual) + at);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] += r.get(j);
+    for (int j = 0; j < V; ++j) v[j] += res.get(j);
   }
-  storeV<4>(static_cast<T*>(p.out) + at, v);
+  storeV<V>(static_cast<T*>(p.out) + at, v);
+}
+template <int V>
+__device__ __forceinline__ void linear_bias(const LinearParams& p, int n, float (&bias)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) bias[j] = p.bias && n < p.N ? p.bias[n + j] : 0.f;
+}
+
+// A wave's outputs, FM x FN blocks of 32 x 32 (element e of a lane: output row
+// lane%32, column 8·(e/4) + 4·(lane/32) + e%4 of the block), from row m0 and
+// column n0.  Each band of 32 rows goes through the wave's own LDS, so that a
+// lane then holds 8 neighbouring columns and a few lanes a whole row segment:
+// stores and residual loads of 16 bytes a lane and whole cache lines.
+template <typename T, int FM, int FN>
+__device__ __forceinline__ void linear_out(const LinearParams& p, f32x16 (&acc)[FN][FM], float* lds, int m0, int n0, int lane) {
+  constexpr int W = FN * 32, kRow = W + 4;  // (rows 16 bytes apart in the banks)
+  constexpr int LPR = W / 8, RPI = 64 / LPR, IT = (32 + RPI - 1) / RPI;
+  const int r0 = lane / LPR, n = n0 + (lane % LPR) * 8;
+  const bool on = lane < LPR * RPI && n < p.N;
+  float bias[8];
+  linear_bias(p, n, bias);
+#pragma unroll
+  for (int j = 0; j < FM; ++j) {
+    const int mb = m0 + j * 32;
+    Vec<T, 8> res[IT];
+    if (p.residual && !p.part) {
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+        const int r = it * RPI + r0;
+        if (on && r < 32 && mb + r < p.M) res[it].load(static_cast<const T*>(p.residual) + (int64_t)(mb + r) * p.N + n);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; e += 4)
+        *reinterpret_cast<float4*>(lds + (lane & 31) * kRow + i * 32 + 2 * e + (lane >> 5) * 4) =
+            make_float4(acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]);
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const int r = it * RPI + r0;
+      if (on && r < 32 && mb + r < p.M) {
+        Vec<float, 8> f;
+        f.load(lds + r * kRow + (lane % LPR) * 8);
+        float v[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = f.get(c);
+        const int64_t at = (int64_t)(mb + r) * p.N + n;
+        if (p.part) storeV<8>(p.part + (int64_t)blockIdx.y * p.M * p.N + at, v);
+        else linear_finish(p, at, bias, res[it], v);
+      }
+    }
+  }
 }
 
 // ---- operands ----
@@ -68,7 +115,7 @@ template <typename T>
 struct Elem;
 template <>
 struct Elem<uint16_t> {
-  static constexpr int BK = 64;     // contraction elements of a stage (128 bytes)
+  static constexpr int BK = 64;     // contraction elements of a 128-byte row
   static constexpr int KS = 16;     // of a fragment
   static constexpr int CH = 8;      // of a 16-byte chunk
   typedef bf16x8 Frag;
@@ -91,56 +138,101 @@ struct Elem<float> {
   }
 };
 
-// A stage of R rows (or columns) of one operand.  TR = false: R rows of 128
-// bytes, padded to 144 so that 16 rows read at one chunk fall on 16 different
-// 16-byte banks.  TR = true: BK contraction rows of R elements, padded so that
-// the 4 rows of a transposing read fall on different quarters of the banks.
-template <typename T, int R, bool TR, int NT>
+// A stage of one operand in LDS, 128 bytes of contraction deep, filled by loads
+// that go from memory straight to LDS: a wave's instruction fills 1 KB in lane
+// order, and which 16 bytes a lane fetches is free, so the bank swizzle is made
+// on that side.
+// TR = false: R rows of 128 bytes; row r keeps its 16-byte chunk c at slot
+// c ^ (r/2 % 8), so that the 16 rows that a pass of a 16-byte read takes at one
+// chunk lie on 16 different banks' widths.
+// TR = true: BK contraction rows of R elements; row k keeps its 64-byte blocks
+// at block ^ swz(k), for the 4 rows of a transposing read.
+// Chunks past the operand's edge are fetched from beyond the buffer's range,
+// which gives zeros.
+template <typename T, int R, bool TR, int NW>
 struct Stage {
   typedef Elem<T> E;
-  static constexpr int kStride = TR ? R + 64 / (int)sizeof(T) : E::BK + 16 / (int)sizeof(T);  // elements
-  static constexpr int kElems = (TR ? E::BK : R) * kStride;
-  static constexpr int kLoads = R * 8 / NT;  // 16-byte loads of a thread
-  static_assert(R * 8 % NT == 0, "whole loads");
-  u32x4 reg[kLoads];
+  static constexpr int kRow = TR ? R : E::BK;  // elements of a row in LDS
+  static constexpr int kCpr = kRow / E::CH;    // its chunks
+  static constexpr int kElems = R * E::BK;
+  static constexpr int kLoads = kElems * (int)sizeof(T) / (1024 * NW);  // of a wave
+  static_assert(kElems * (int)sizeof(T) % (1024 * NW) == 0, "whole loads");
+  uint32_t off[kLoads];  // the lane's bytes from the stage's first element
+  int kk[kLoads];        // and its contraction element, for a stage that ends early
 
-  // base: first element of the stage (row r0, contraction k0); rows, ks: how many are left there
-  __device__ __forceinline__ void load(const T* base, int64_t ld, int rows, int ks) {
+  // Rows a multiple of 256 bytes apart would share banks, rows 128 bytes more every second one.
+  __device__ static __forceinline__ int swz(int k) {
+    if constexpr (sizeof(T) == 4) return 0;
+    return kRow * (int)sizeof(T) % 256 == 0 ? k & 3 : (k >> 1) & 1;
+  }
+  __device__ __forceinline__ void init(int wave, int lane, int64_t ld, int rows) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int at = (i * NW + wave) * 64 + lane, r = at / kCpr, slot = at % kCpr;
+      const int c = TR ? slot ^ (swz(r) << 2) : slot ^ ((r >> 1) & 7);
+      const bool in = (TR ? c * E::CH : r) < rows;
+      kk[i] = TR ? r : c * E::CH;
+      off[i] = in ? (uint32_t)(r * (int)ld + c * E::CH) * (uint32_t)sizeof(T) : kDrop;
+    }
+  }
+  // base: the stage's first element in memory; ks: contraction elements left there
+  __device__ __forceinline__ void fetch(const T* base, T* lds, int wave, int ks) const {
+#ifdef __HIP_DEVICE_COMPILE__  // (the host pass, which only needs the kernels' names, does not take the builtin)
     const auto rsrc = make_rsrc(base, 0x7fffffffu);
+    typedef __attribute__((address_space(3))) uint32_t* P;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int id = threadIdx.x + i * NT;
-      constexpr int cpr = TR ? R / E::CH : 8;  // chunks of a stored row
-      const int r = id / cpr, c = (id % cpr) * E::CH;
-      const bool in = TR ? (r < ks && c < rows) : (r < rows && c < ks);
-      const uint32_t off = in ? (uint32_t)(r * (int)ld + c) * (uint32_t)sizeof(T) : kDrop;
-      reg[i] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, (int)off, 0, 0);
+      const P to = (P)(lds + (i * NW + wave) * (1024 / (int)sizeof(T)));
+      if (ks >= E::BK) __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, to, 16, (int)off[i], 0, 0, 0);
+      else __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, to, 16, (int)(kk[i] < ks ? off[i] : kDrop), 0, 0, 0);
     }
+#endif
   }
-  __device__ __forceinline__ void store(T* lds) const {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int id = threadIdx.x + i * NT;
-      constexpr int cpr = TR ? R / E::CH : 8;
-      *reinterpret_cast<u32x4*>(lds + (id / cpr) * kStride + (id % cpr) * E::CH) = reg[i];
-    }
-  }
-  // Fragment of rows r0..r0+31 and contraction elements k0..k0+KS-1: lane l
-  // holds row l%32, elements (l/32)·KS/2 onwards.
-  __device__ static __forceinline__ typename E::Frag frag(const T* lds, int r0, int k0) {
-    const int lane = threadIdx.x & 63;
+  // Fragments of rows r0 + 32 j (j < NF) of half h of the stage, two ksteps:
+  // lane l holds row l%32, elements (l/32)·KS/2 onwards of the kstep.
+  template <int NF>
+  __device__ static __forceinline__ void frags(const T* lds, int r0, int h, int lane, typename E::Frag (&f)[2][NF]) {
     if constexpr (!TR) {
-      return *reinterpret_cast<const typename E::Frag*>(lds + (r0 + (lane & 31)) * kStride + k0 + (lane >> 5) * E::CH);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const int c = (h * 4 + ks * 2 + (lane >> 5)) ^ ((lane >> 1) & 7);
+        const T* const at = lds + (r0 + (lane & 31)) * kRow + c * E::CH;
+#pragma unroll
+        for (int j = 0; j < NF; ++j) f[ks][j] = *reinterpret_cast<const typename E::Frag*>(at + j * 32 * kRow);
+      }
     } else if constexpr (sizeof(T) == 2) {
-      const int g = lane >> 4, i = lane & 15;
-      const T* const at = lds + (k0 + (g >> 1) * 8 + (i >> 2)) * kStride + r0 + (g & 1) * 16 + (i & 3) * 4;
-      typedef __attribute__((address_space(3))) s16x4* P;
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(at));
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(at + 4 * kStride));
-      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+      const int g = lane >> 4, i = lane & 15, k = i >> 2;
+      typedef __attribute__((address_space(3))) const T* P;
+#pragma unroll
+      for (int j = 0; j < NF; ++j) {
+        const uint32_t at = (uint32_t)(uintptr_t)(P)(lds + (h * 2 * E::KS + (g >> 1) * 8 + k) * kRow + ((r0 + j * 32) ^ (swz(k) << 5)) +
+                                                     (g & 1) * 16 + (i & 3) * 4);
+        u32x2 v[4];
+        // (Loads and their wait in one block: before the builtin the compiler,
+        // which cannot tell that the stage being filled is another one, would
+        // wait for all of that stage's loads.)
+#ifdef __HIP_DEVICE_COMPILE__
+        constexpr int o1 = 4 * kRow * 2, o2 = 16 * kRow * 2, o3 = 20 * kRow * 2;
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %4\n\tds_read_b64_tr_b16 %1, %4 offset:%c5\n\t"
+            "ds_read_b64_tr_b16 %2, %4 offset:%c6\n\tds_read_b64_tr_b16 %3, %4 offset:%c7\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+            : "v"(at), "n"(o1), "n"(o2), "n"(o3)
+            : "memory");
+#endif
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+          f[ks][j] = __builtin_bit_cast(bf16x8, u32x4{v[2 * ks][0], v[2 * ks][1], v[2 * ks + 1][0], v[2 * ks + 1][1]});
+      }
     } else {
-      const T* const at = lds + (k0 + (lane >> 5) * 4) * kStride + r0 + (lane & 31);
-      return f32x4v{at[0], at[kStride], at[2 * kStride], at[3 * kStride]};
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int j = 0; j < NF; ++j) {
+          const T* const at = lds + (h * 2 * E::KS + ks * E::KS + (lane >> 5) * 4) * kRow + r0 + j * 32 + (lane & 31);
+          f[ks][j] = f32x4v{at[0], at[kRow], at[2 * kRow], at[3 * kRow]};
+        }
     }
   }
 };
@@ -156,86 +248,165 @@ __device__ __forceinline__ void tile_of(const LinearParams& p, int bid, int& tm,
   tn = in / rows;
 }
 
-// ---- the tile kernel ----
-// BM x BN outputs by WM x WN waves, two stages of LDS: the next stage's loads
-// are in flight to registers while this one is multiplied.
-template <typename T, bool TA, bool TB, int BM, int BN, int WM, int WN>
-__global__ void __launch_bounds__(64 * WM * WN) linear_tile_kernel(const LinearParams p) {
+// What both tile kernels start from: the workgroup's tile, its operands and its share of the contraction.
+template <typename T, bool TA, bool TB, int BM, int BN, int NW>
+struct Tile {
   typedef Elem<T> E;
-  constexpr int NT = 64 * WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
-  typedef Stage<T, BM, TA, NT> SA;
-  typedef Stage<T, BN, TB, NT> SB;
-  __shared__ __align__(16) T lds[2 * (SA::kElems + SB::kElems)];
-  auto la = [&](int i) { return lds + i * SA::kElems; };
-  auto lb = [&](int i) { return lds + 2 * SA::kElems + i * SB::kElems; };
-  int tm, tn;
-  tile_of(p, blockIdx.x, tm, tn);
-  const int m0 = tm * BM, n0 = tn * BN;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int wm = (wave / WN) * TM, wn = (wave % WN) * TN;
-  const int kt0 = blockIdx.y * p.kt_per_split, kts = (p.K + E::BK - 1) / E::BK, kt1 = min(kts, kt0 + p.kt_per_split);
-
-  const T* const a = static_cast<const T*>(p.a);
-  const T* const b = static_cast<const T*>(p.b);
+  typedef Stage<T, BM, TA, NW> SA;
+  typedef Stage<T, BN, TB, NW> SB;
+  static constexpr int kStage = SA::kElems + SB::kElems;  // elements of a stage
+  static constexpr int kLoads = SA::kLoads + SB::kLoads;  // loads of a wave
+  int m0, n0, kt0, kt1;
+  const T *a, *b;
   SA sa;
   SB sb;
-  auto fetch = [&](int kt) __attribute__((always_inline)) {
+  __device__ __forceinline__ Tile(const LinearParams& p, int wave, int lane) {
+    int tm, tn;
+    tile_of(p, blockIdx.x, tm, tn);
+    m0 = tm * BM;
+    n0 = tn * BN;
+    kt0 = blockIdx.y * p.kt_per_split;
+    kt1 = min((p.K + E::BK - 1) / E::BK, kt0 + p.kt_per_split);
+    a = static_cast<const T*>(p.a) + (TA ? (int64_t)m0 : m0 * p.lda);
+    b = static_cast<const T*>(p.b) + (TB ? (int64_t)n0 : n0 * p.ldb);
+    sa.init(wave, lane, p.lda, p.M - m0);
+    sb.init(wave, lane, p.ldb, p.N - n0);
+  }
+  __device__ __forceinline__ T* stage(T* lds, int kt) const { return lds + ((kt - kt0) & 1) * kStage; }
+  __device__ __forceinline__ void fetch(const LinearParams& p, T* lds, int kt, int wave) const {
     const int k0 = kt * E::BK;
-    sa.load(TA ? a + k0 * p.lda + m0 : a + m0 * p.lda + k0, p.lda, p.M - m0, p.K - k0);
-    sb.load(TB ? b + k0 * p.ldb + n0 : b + n0 * p.ldb + k0, p.ldb, p.N - n0, p.K - k0);
-  };
-  f32x16 acc[FN][FM];
+    T* const l = stage(lds, kt);
+    sa.fetch(a + (TA ? k0 * p.lda : (int64_t)k0), l, wave, p.K - k0);
+    sb.fetch(b + (TB ? k0 * p.ldb : (int64_t)k0), l + SA::kElems, wave, p.K - k0);
+  }
+};
+
+template <typename E, int FM, int FN>
+__device__ __forceinline__ void mma_half(const typename E::Frag (&fa)[2][FM], const typename E::Frag (&fb)[2][FN], f32x16 (&acc)[FN][FM]) {
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j) acc[i][j] = E::mma(fb[ks][i], fa[ks][j], acc[i][j]);
+}
+template <int FM, int FN>
+__device__ __forceinline__ void acc_zero(f32x16 (&acc)[FN][FM]) {
 #pragma unroll
   for (int i = 0; i < FN; ++i)
 #pragma unroll
     for (int j = 0; j < FM; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+}
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-  if (kt0 < kt1) {
-    fetch(kt0);
-    sa.store(la(0));
-    sb.store(lb(0));
+// ---- the small tile: 128 x 128, four waves, two workgroups a compute unit ----
+// Two stages of LDS; while one is multiplied, the other is filled.  One
+// workgroup's waits are the other's time.
+template <typename T, bool TA, bool TB>
+__global__ void __launch_bounds__(256, 2) linear_tile_kernel(const LinearParams p) {
+  typedef Tile<T, TA, TB, 128, 128, 4> Tl;
+  typedef Elem<T> E;
+  __shared__ __align__(1024) T lds[2 * Tl::kStage];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+  const Tl t(p, wave, lane);
+  f32x16 acc[2][2];
+  acc_zero(acc);
+  if (t.kt0 < t.kt1) t.fetch(p, lds, t.kt0, wave);
+  for (int kt = t.kt0; kt < t.kt1; ++kt) {
+    wait_loads();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (kt + 1 < t.kt1) t.fetch(p, lds, kt + 1, wave);
+    const T* const la = t.stage(lds, kt);
+    const T* const lb = la + Tl::SA::kElems;
+    typename E::Frag fa[2][2][2], fb[2][2][2];
+    Tl::SA::template frags<2>(la, wm, 0, lane, fa[0]);
+    Tl::SB::template frags<2>(lb, wn, 0, lane, fb[0]);
+    if constexpr (!TA && !TB) {
+      Tl::SA::template frags<2>(la, wm, 1, lane, fa[1]);
+      Tl::SB::template frags<2>(lb, wn, 1, lane, fb[1]);
+      mma_half<E>(fa[0], fb[0], acc);
+    } else {
+      mma_half<E>(fa[0], fb[0], acc);
+      Tl::SA::template frags<2>(la, wm, 1, lane, fa[1]);
+      Tl::SB::template frags<2>(lb, wn, 1, lane, fb[1]);
+    }
+    mma_half<E>(fa[1], fb[1], acc);
+    asm volatile("" ::: "memory");
   }
   __syncthreads();
-  for (int kt = kt0; kt < kt1; ++kt) {
-    const int cur = (kt - kt0) & 1;
-    if (kt + 1 < kt1) fetch(kt + 1);
-#pragma unroll
-    for (int ks = 0; ks < E::BK; ks += E::KS) {
-      typename E::Frag fa[FM], fb[FN];
-#pragma unroll
-      for (int j = 0; j < FM; ++j) fa[j] = SA::frag(la(cur), wm + j * 32, ks);
-#pragma unroll
-      for (int i = 0; i < FN; ++i) fb[i] = SB::frag(lb(cur), wn + i * 32, ks);
-#pragma unroll
-      for (int i = 0; i < FN; ++i)
-#pragma unroll
-        for (int j = 0; j < FM; ++j) acc[i][j] = E::mma(fb[i], fa[j], acc[i][j]);
-    }
-    if (kt + 1 < kt1) {
-      sa.store(la(cur ^ 1));
-      sb.store(lb(cur ^ 1));
-    }
-    __syncthreads();
+  static_assert(4 * 32 * 68 * 4 <= (int)sizeof(lds), "the bands fit the stages");
+  linear_out<T>(p, acc, reinterpret_cast<float*>(lds) + wave * 32 * 68, t.m0 + wm, t.n0 + wn, lane);
+}
+
+// ---- the large tile: 256 x BN, eight waves, one workgroup a compute unit ----
+// A larger tile takes less from the L2 (128 x 128 tiles need 64 bytes a cycle
+// and compute unit at full rate, 256 x 256 tiles half of it), but leaves one
+// workgroup a compute unit.  So its waves work in two groups, one on each half
+// of every SIMD's pair of waves, half a step apart: while one group multiplies
+// (two ksteps), the other reads its fragments and starts loads.  A barrier ends
+// every half step; the late group waits at one more before the first and the
+// early group at one more after the last, so both meet the same number.
+//   - A stage's last reads are the late group's, one half step after the early
+//     group's; the early group refills that buffer in its next reading half
+//     step, the late one at the start of the multiplying half step beside it.
+//   - Each wave has waited for its own loads of a stage before the barrier that
+//     lets the early group read it: the late group at the end of its last
+//     reading half step before, the early one at the end of its last
+//     multiplying one.
+template <typename T, bool TA, bool TB, int BN, int WM, int WN>
+__global__ void __launch_bounds__(512) linear_large_kernel(const LinearParams p) {
+  static_assert(WM * WN == 8, "eight waves");
+  typedef Tile<T, TA, TB, 256, BN, 8> Tl;
+  typedef Elem<T> E;
+  constexpr int TM = 256 / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
+  __shared__ __align__(1024) T lds[2 * Tl::kStage];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wm = (wave / WN) * TM, wn = (wave % WN) * TN;
+  const Tl t(p, wave, lane);
+  f32x16 acc[FN][FM];
+  acc_zero(acc);
+  const bool late = wave >= 4;
+  if (t.kt0 < t.kt1) t.fetch(p, lds, t.kt0, wave);
+  if (late && t.kt0 + 1 < t.kt1) {
+    t.fetch(p, lds, t.kt0 + 1, wave);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(Tl::kLoads) : "memory");
+  } else {
+    wait_loads();
   }
-  // element e of a 32 x 32 block: output row lane%32, column 8·(e/4) + 4·(lane/32) + e%4
+  __builtin_amdgcn_s_barrier();
+  if (late) __builtin_amdgcn_s_barrier();
+  for (int kt = t.kt0; kt < t.kt1; ++kt) {
+    const T* const la = t.stage(lds, kt);
 #pragma unroll
-  for (int j = 0; j < FM; ++j) {
-    const int m = m0 + wm + j * 32 + (lane & 31);
-#pragma unroll
-    for (int i = 0; i < FN; ++i) {
-#pragma unroll
-      for (int e = 0; e < 16; e += 4) {
-        const int n = n0 + wn + i * 32 + 2 * e + (lane >> 5) * 4;
-        float v[4] = {acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]};
-        if (m < p.M && n < p.N) {
-          if (p.part) storeV<4>(p.part + ((int64_t)blockIdx.y * p.M + m) * p.N + n, v);
-          else linear_finish<T>(p, m, n, v);
-        }
-      }
+    for (int h = 0; h < 2; ++h) {
+      typename E::Frag fa[2][FM], fb[2][FN];
+      __builtin_amdgcn_sched_barrier(0);
+      if (h == 0 && !late && kt + 1 < t.kt1) t.fetch(p, lds, kt + 1, wave);
+      Tl::SA::template frags<FM>(la, wm, h, lane, fa);
+      Tl::SB::template frags<FN>(la + Tl::SA::kElems, wn, h, lane, fb);
+      if (h == 1 && late) wait_loads();
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      if (h == 1 && late && kt + 2 < t.kt1) t.fetch(p, lds, kt + 2, wave);
+      __builtin_amdgcn_s_setprio(1);
+      mma_half<E>(fa, fb, acc);
+      __builtin_amdgcn_s_setprio(0);
+      if (h == 1 && !late) wait_loads();
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
+  if (!late) __builtin_amdgcn_s_barrier();
+  constexpr int kWave = 32 * (TN + 4);  // floats of a wave's band
+  static_assert(8 * kWave * 4 <= (int)sizeof(lds), "the bands fit the stages");
+  linear_out<T>(p, acc, reinterpret_cast<float*>(lds) + wave * kWave, t.m0 + wm, t.n0 + wn, lane);
 }
 
 // Joins the shares of a split contraction, in order, and finishes the output.
@@ -243,15 +414,18 @@ template <typename T>
 __global__ void __launch_bounds__(256) linear_join_kernel(const LinearParams p) {
   const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, n = (int64_t)p.M * p.N;
   if (e >= n) return;
-  Vec<float, 4> s;
-  s.load(p.part + e);
-  float v[4] = {s.get(0), s.get(1), s.get(2), s.get(3)};
-  for (int k = 1; k < p.splits; ++k) {
+  float bias[4], v[4] = {0.f, 0.f, 0.f, 0.f};
+  linear_bias(p, (int)(e % p.N), bias);
+  Vec<T, 4> res;
+  if (p.residual) res.load(static_cast<const T*>(p.residual) + e);
+#pragma unroll 8
+  for (int k = 0; k < p.splits; ++k) {
+    Vec<float, 4> s;
     s.load(p.part + k * n + e);
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] += s.get(j);
   }
-  linear_finish<T>(p, (int)(e / p.N), (int)(e % p.N), v);
+  linear_finish(p, e, bias, res, v);
 }
 
 // ---- few rows ----
@@ -293,14 +467,23 @@ __global__ void __launch_bounds__(512) linear_rows_kernel(const LinearParams p) 
 #pragma unroll
   for (int t = 0; t < MT; ++t) *reinterpret_cast<f32x4v*>(&red[wave][t][lane * 4]) = acc[t];
   __syncthreads();
-  for (int e = threadIdx.x; e < MT * 64; e += 512) {
-    const int t = e >> 6, l = e & 63, m = t * 16 + (l & 15), n = n0 + (l >> 4) * 4;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
+  if (threadIdx.x < MT * 32) {
+    const int t = threadIdx.x >> 5, l = threadIdx.x & 15, half = (threadIdx.x >> 4) & 1, m = t * 16 + l, n = n0 + half * 8;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += red[k][t][l * 4 + j];
-    if (m < p.M && n < p.N) linear_finish<T>(p, m, n, v);
+      for (int j = 0; j < 8; ++j) v[j] += red[k][t][(half * 32 + (j >> 2) * 16 + l) * 4 + (j & 3)];
+    if (m < p.M && n < p.N) {
+      const int64_t at = (int64_t)m * p.N + n;
+      float bias[8];
+      linear_bias(p, n, bias);
+      Vec<T, 8> res;
+      if (p.residual) res.load(static_cast<const T*>(p.residual) + at);
+      linear_finish(p, at, bias, res, v);
+    }
   }
 }
 

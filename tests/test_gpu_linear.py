@@ -67,6 +67,10 @@ CASES = [
     (1500, 768, 1544, "bf16", "silu", True, False),
     (5003, 520, 256, "bf16", "gelu", True, True),
     (2100, 264, 1048, "bf16", "relu", False, True),
+    # enough tiles for the large ones, the last of them partly empty, in each of the three products
+    (16300, 328, 1528, "bf16", "silu", True, True),
+    (8200, 1000, 2056, "bf16", "none", True, True),
+    (2050, 2056, 2056, "bf16", "gelu", True, False),
 ]
 
 
