@@ -10,8 +10,10 @@ or None, the state [B][D] float32.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from . import _binding as _b
+from ._call import check_f32, check_like, done, launch_stream, nbytes, ptr, query, use_workspace
 
 GLR_SQRT, GLR_LERP, GLR_UNIT = 0, 1, 2
 
@@ -44,54 +46,40 @@ def make_glr_dims(batch, seqlen, dim, dtype, *, input_rule=GLR_SQRT, reverse=Fal
                    _b._ptr(initial_state), _b._ptr(reset), _b._ptr(workspace), int(workspace_bytes))
 
 
-def _query(name, dims) -> int:
-    n = getattr(_b.load_library(), name)(ctypes.byref(dims))
-    if n == ctypes.c_size_t(-1).value:
-        raise _b.MambaError(_b.MAMBA_ERR_UNSUPPORTED, name)
-    return n
-
-
 def glr_fwd_workspace_bytes(dims: GlrDims) -> int:
-    return _query("mamba_glr_fwd_workspace_bytes", dims)
+    return query("mamba_glr_fwd_workspace_bytes", dims)
 
 
 def glr_bwd_workspace_bytes(dims: GlrDims) -> int:
-    return _query("mamba_glr_bwd_workspace_bytes", dims)
+    return query("mamba_glr_bwd_workspace_bytes", dims)
 
 
 def glr_saved_bytes(dims: GlrDims) -> int:
-    return _query("mamba_glr_saved_bytes", dims)
+    return query("mamba_glr_saved_bytes", dims)
 
 
-def _bytes(t) -> int:
-    return 0 if t is None else t.numel() * t.element_size()
-
-
-def _workspace(dims, need, workspace, dev):
-    """Puts a workspace of need bytes (the caller's, if it is large enough) into dims and returns it, to be kept
-    until the launch."""
-    import torch
-    _b._check_buffer(workspace, "workspace", dev)
-    if need > 0 and _bytes(workspace) < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    if need > 0:
-        dims.workspace, dims.workspace_bytes = workspace.data_ptr(), _bytes(workspace)
-    return workspace
+@functools.lru_cache(maxsize=512)
+def _sizes(Bsz, L, Dm, dt):
+    """(forward workspace, backward workspace, saved states): pure functions of the sizes."""
+    d = make_glr_dims(Bsz, L, Dm, dt)
+    return glr_fwd_workspace_bytes(d), glr_bwd_workspace_bytes(d), glr_saved_bytes(d)
 
 
 def _check_inputs(x, r, i, z, lam, initial_state, reset):
     import torch
     if x.dim() != 3:
         raise ValueError("x must be [B][L][D], got %s" % (tuple(x.shape),))
-    Bsz, L, Dm = x.shape
-    dev, tdt = x.device, x.dtype
-    for name, t in (("x", x), ("r", r), ("i", i), ("z", z)):
-        _b._check(t, name, (Bsz, L, Dm), tdt, dev)
-    _b._check(lam, "lam", (Dm,), torch.float32, dev)
-    _b._check(initial_state, "initial_state", (Bsz, Dm), torch.float32, dev)
+    dt = _b._dtype_code(x)
+    shape = x.shape
+    Bsz, L, Dm = shape
+    check_like(x, shape, ("x", x), ("r", r), ("i", i), ("z", z))
+    if lam is not None:
+        check_f32(x, (Dm,), ("lam", lam))
+    if initial_state is not None:
+        check_f32(x, (Bsz, Dm), ("initial_state", initial_state))
     if reset is not None:
-        _b._check(reset, "reset", (Bsz, L), torch.bool if reset.dtype == torch.bool else torch.uint8, dev)
-    return Bsz, L, Dm, _b._dtype_code(x), dev
+        _b._check(reset, "reset", (Bsz, L), torch.bool if reset.dtype == torch.bool else torch.uint8, x.device)
+    return Bsz, L, Dm, dt
 
 
 def glr_fwd(x, r, i=None, z=None, lam=None, *, scale=8.0, input_rule=GLR_SQRT, reverse=False, initial_state=None,
@@ -121,24 +109,27 @@ def _fwd(x, r, i, z, lam, scale, input_rule, reverse, initial_state, reset, out,
         with torch.cuda.stream(ts):
             return _fwd(x, r, i, z, lam, scale, input_rule, reverse, initial_state, reset, out, last_state,
                         want_last_state, workspace, ts, save, saved)
-    lib = _b.load_library()
-    Bsz, L, Dm, dt, dev = _check_inputs(x, r, i, z, lam, initial_state, reset)
+    Bsz, L, Dm, dt = _check_inputs(x, r, i, z, lam, initial_state, reset)
+    raw = launch_stream(x, stream)
+    need, _, need_saved = _sizes(Bsz, L, Dm, dt)
     if out is None:
         out = torch.empty_like(x)
-    _b._check(out, "out", (Bsz, L, Dm), x.dtype, dev)
-    if last_state is None and want_last_state:
-        last_state = torch.empty((Bsz, Dm), dtype=torch.float32, device=dev)
-    _b._check(last_state, "last_state", (Bsz, Dm), torch.float32, dev)
+    else:
+        check_like(x, x.shape, ("out", out))
+    if last_state is not None:
+        check_f32(x, (Bsz, Dm), ("last_state", last_state))
+    elif want_last_state:
+        last_state = torch.empty((Bsz, Dm), dtype=torch.float32, device=x.device)
     dims = make_glr_dims(Bsz, L, Dm, dt, input_rule=input_rule, reverse=reverse, scale=scale,
                          initial_state=initial_state, reset=reset)
-    workspace = _workspace(dims, glr_fwd_workspace_bytes(dims), workspace, dev)
-    _b._check_buffer(saved, "saved", dev)
-    if save and saved is None:
-        saved = torch.empty(glr_saved_bytes(dims), dtype=torch.uint8, device=dev)
-    rc = lib.mamba_glr_fwd(_b._ptr(x), _b._ptr(r), _b._ptr(i), _b._ptr(z), _b._ptr(lam), ctypes.byref(dims),
-                           _b._ptr(out), _b._ptr(last_state), _b._ptr(saved), _bytes(saved), _b._stream(stream))
-    if rc != _b.MAMBA_OK:
-        raise _b.MambaError(rc, "mamba_glr_fwd")
+    workspace = use_workspace(dims, need, workspace, x)
+    if saved is not None:
+        _b._check_buffer(saved, "saved", x.device)
+    elif save:
+        saved = torch.empty(need_saved, dtype=torch.uint8, device=x.device)
+    done(_b.load_library().mamba_glr_fwd(x.data_ptr(), r.data_ptr(), ptr(i), ptr(z), ptr(lam), ctypes.byref(dims),
+                                         out.data_ptr(), ptr(last_state), ptr(saved), nbytes(saved), raw),
+         "mamba_glr_fwd")
     return out, last_state, saved
 
 
@@ -155,24 +146,33 @@ def glr_bwd(x, r, i=None, z=None, lam=None, *, dout, dlast=None, scale=8.0, inpu
             return glr_bwd(x, r, i, z, lam, dout=dout, dlast=dlast, scale=scale, input_rule=input_rule,
                            reverse=reverse, initial_state=initial_state, reset=reset, workspace=workspace,
                            saved=saved, stream=ts)
-    lib = _b.load_library()
-    Bsz, L, Dm, dt, dev = _check_inputs(x, r, i, z, lam, initial_state, reset)
-    _b._check(dout, "dout", (Bsz, L, Dm), x.dtype, dev)
-    _b._check(dlast, "dlast", (Bsz, Dm), torch.float32, dev)
-    g = dict(dx=torch.empty_like(x), dr=torch.empty_like(x), di=None if i is None else torch.empty_like(x),
-             dz=None if z is None else torch.empty_like(x), dlam=None if lam is None else torch.empty_like(lam),
-             dinit=torch.empty((Bsz, Dm), dtype=torch.float32, device=dev))
+    Bsz, L, Dm, dt = _check_inputs(x, r, i, z, lam, initial_state, reset)
+    raw = launch_stream(x, stream)
+    check_like(x, x.shape, ("dout", dout))
+    if dlast is not None:
+        check_f32(x, (Bsz, Dm), ("dlast", dlast))
+    _, need, _ = _sizes(Bsz, L, Dm, dt)
+    dx, dr = torch.empty_like(x), torch.empty_like(x)
+    di = None if i is None else torch.empty_like(x)
+    dz = None if z is None else torch.empty_like(x)
+    dlam = None if lam is None else torch.empty_like(lam)
+    dinit = torch.empty((Bsz, Dm), dtype=torch.float32, device=x.device)
     dims = make_glr_dims(Bsz, L, Dm, dt, input_rule=input_rule, reverse=reverse, scale=scale,
                          initial_state=initial_state, reset=reset)
-    workspace = _workspace(dims, glr_bwd_workspace_bytes(dims), workspace, dev)
-    _b._check_buffer(saved, "saved", dev)
-    rc = lib.mamba_glr_bwd(_b._ptr(x), _b._ptr(r), _b._ptr(i), _b._ptr(z), _b._ptr(lam), _b._ptr(dout),
-                           _b._ptr(dlast), ctypes.byref(dims), _b._ptr(g["dx"]), _b._ptr(g["dr"]), _b._ptr(g["di"]),
-                           _b._ptr(g["dz"]), _b._ptr(g["dlam"]), _b._ptr(g["dinit"]), _b._ptr(saved), _bytes(saved),
-                           _b._stream(stream))
-    if rc != _b.MAMBA_OK:
-        raise _b.MambaError(rc, "mamba_glr_bwd")
-    return g
+    workspace = use_workspace(dims, need, workspace, x)
+    _b._check_buffer(saved, "saved", x.device)
+    done(_b.load_library().mamba_glr_bwd(x.data_ptr(), r.data_ptr(), ptr(i), ptr(z), ptr(lam), dout.data_ptr(),
+                                         ptr(dlast), ctypes.byref(dims), dx.data_ptr(), dr.data_ptr(), ptr(di),
+                                         ptr(dz), ptr(dlam), dinit.data_ptr(), ptr(saved), nbytes(saved), raw),
+         "mamba_glr_bwd")
+    return dict(dx=dx, dr=dr, di=di, dz=dz, dlam=dlam, dinit=dinit)
+
+
+@functools.lru_cache(maxsize=512)
+def _step_dims(Bsz, Dm, dt, input_rule, scale):
+    """The dims of a step hold no pointers and are only read: one for all calls of these sizes."""
+    d = make_glr_dims(Bsz, 1, Dm, dt, input_rule=input_rule, scale=scale)
+    return d, ctypes.byref(d)
 
 
 def glr_step(state, x_t, r_t, i_t=None, z_t=None, lam=None, *, scale=8.0, input_rule=GLR_SQRT, out=None, stream=None):
@@ -183,21 +183,18 @@ def glr_step(state, x_t, r_t, i_t=None, z_t=None, lam=None, *, scale=8.0, input_
     if ts is not None:
         with torch.cuda.stream(ts):
             return glr_step(state, x_t, r_t, i_t, z_t, lam, scale=scale, input_rule=input_rule, out=out, stream=ts)
-    lib = _b.load_library()
     if x_t.dim() != 2:
         raise ValueError("x_t must be [B][D], got %s" % (tuple(x_t.shape),))
-    Bsz, Dm = shape = x_t.shape
-    dev, tdt = x_t.device, x_t.dtype
-    _b._check(state, "state", shape, torch.float32, dev)
-    for name, t in (("x_t", x_t), ("r_t", r_t), ("i_t", i_t), ("z_t", z_t)):
-        _b._check(t, name, shape, tdt, dev)
-    _b._check(lam, "lam", (Dm,), torch.float32, dev)
+    dt = _b._dtype_code(x_t)
+    shape = x_t.shape
+    check_like(x_t, shape, ("x_t", x_t), ("r_t", r_t), ("i_t", i_t), ("z_t", z_t), ("out", out))
+    check_f32(x_t, shape, ("state", state))
+    if lam is not None:
+        check_f32(x_t, shape[1:], ("lam", lam))
+    raw = launch_stream(x_t, stream)
     if out is None:
         out = torch.empty_like(x_t)
-    _b._check(out, "out", shape, tdt, dev)
-    dims = make_glr_dims(Bsz, 1, Dm, _b._dtype_code(x_t), input_rule=input_rule, scale=scale)
-    rc = lib.mamba_glr_step(_b._ptr(state), _b._ptr(x_t), _b._ptr(r_t), _b._ptr(i_t), _b._ptr(z_t), _b._ptr(lam),
-                            ctypes.byref(dims), _b._ptr(out), _b._stream(stream))
-    if rc != _b.MAMBA_OK:
-        raise _b.MambaError(rc, "mamba_glr_step")
+    done(_b.load_library().mamba_glr_step(state.data_ptr(), x_t.data_ptr(), r_t.data_ptr(), ptr(i_t), ptr(z_t),
+                                          ptr(lam), _step_dims(shape[0], shape[1], dt, input_rule, scale)[1],
+                                          out.data_ptr(), raw), "mamba_glr_step")
     return out

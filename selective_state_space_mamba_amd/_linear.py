@@ -4,9 +4,10 @@ out = act(x·weightᵀ + bias) + residual for x [..., K] and weight [N][K]."""
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from . import _binding as _b
-from ._glr import _query, _workspace
+from ._call import check_f32, check_like, done, launch_stream, ptr, query, use_workspace
 from ._norm import ACT_NONE
 
 
@@ -35,20 +36,29 @@ def make_linear_dims(rows, in_dim, out_dim, dtype, *, act=ACT_NONE, workspace=No
 
 
 def linear_fwd_workspace_bytes(dims: LinearDims) -> int:
-    return _query("mamba_linear_fwd_workspace_bytes", dims)
+    return query("mamba_linear_fwd_workspace_bytes", dims)
 
 
 def linear_bwd_workspace_bytes(dims: LinearDims) -> int:
-    return _query("mamba_linear_bwd_workspace_bytes", dims)
+    return query("mamba_linear_bwd_workspace_bytes", dims)
+
+
+@functools.lru_cache(maxsize=512)
+def _sizes(M, K, N, dt, act):
+    """(forward, backward) workspace: pure functions of the sizes."""
+    d = make_linear_dims(M, K, N, dt, act=act)
+    return linear_fwd_workspace_bytes(d), linear_bwd_workspace_bytes(d)
 
 
 def _check_inputs(x, weight):
-    if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
-        raise ValueError("x must be [..., K] and weight [N][K], got %s and %s" % (tuple(x.shape), tuple(weight.shape)))
-    N, K = weight.shape
-    _b._check(x, "x", tuple(x.shape), x.dtype, x.device)
-    _b._check(weight, "weight", (N, K), x.dtype, x.device)
-    return x.numel() // K if K else 0, K, N, tuple(x.shape[:-1]) + (N,), _b._dtype_code(x), x.device
+    xs, ws = x.shape, weight.shape
+    if len(ws) != 2 or len(xs) < 1 or xs[-1] != ws[1]:
+        raise ValueError("x must be [..., K] and weight [N][K], got %s and %s" % (tuple(xs), tuple(ws)))
+    dt = _b._dtype_code(x)
+    check_like(x, xs, ("x", x))
+    check_like(x, ws, ("weight", weight))
+    N, K = ws
+    return x.numel() // K if K else 0, K, N, xs[:-1] + ws[:1], dt
 
 
 def linear_fwd(x, weight, bias=None, residual=None, *, act=ACT_NONE, out=None, pre=None, want_pre=False,
@@ -63,21 +73,22 @@ def linear_fwd(x, weight, bias=None, residual=None, *, act=ACT_NONE, out=None, p
         with torch.cuda.stream(ts):
             return linear_fwd(x, weight, bias, residual, act=act, out=out, pre=pre, want_pre=want_pre,
                               workspace=workspace, stream=ts)
-    lib = _b.load_library()
-    M, K, N, shape, dt, dev = _check_inputs(x, weight)
-    _b._check(bias, "bias", (N,), torch.float32, dev)
-    _b._check(residual, "residual", shape, x.dtype, dev)
+    M, K, N, shape, dt = _check_inputs(x, weight)
+    raw = launch_stream(x, stream)
+    if bias is not None:
+        check_f32(x, (N,), ("bias", bias))
+    check_like(x, shape, ("residual", residual), ("out", out))
+    need, _ = _sizes(M, K, N, dt, act)
     dims = make_linear_dims(M, K, N, dt, act=act)
-    workspace = _workspace(dims, linear_fwd_workspace_bytes(dims), workspace, dev)
-    out = torch.empty(shape, dtype=x.dtype, device=dev) if out is None else out
-    if pre is None and want_pre:
-        pre = torch.empty(shape, dtype=torch.float32, device=dev)
-    _b._check(out, "out", shape, x.dtype, dev)
-    _b._check(pre, "pre", shape, torch.float32, dev)
-    rc = lib.mamba_linear_fwd(_b._ptr(x), _b._ptr(weight), _b._ptr(bias), _b._ptr(residual), ctypes.byref(dims),
-                              _b._ptr(out), _b._ptr(pre), _b._stream(stream))
-    if rc != _b.MAMBA_OK:
-        raise _b.MambaError(rc, "mamba_linear_fwd")
+    workspace = use_workspace(dims, need, workspace, x)
+    if out is None:
+        out = x.new_empty(shape)
+    if pre is not None:
+        check_f32(x, shape, ("pre", pre))
+    elif want_pre:
+        pre = torch.empty(shape, dtype=torch.float32, device=x.device)
+    done(_b.load_library().mamba_linear_fwd(x.data_ptr(), weight.data_ptr(), ptr(bias), ptr(residual),
+                                            ctypes.byref(dims), out.data_ptr(), ptr(pre), raw), "mamba_linear_fwd")
     return out, pre
 
 
@@ -92,16 +103,18 @@ def linear_bwd(x, weight, *, dout, pre=None, act=ACT_NONE, want_dx=True, want_dw
         with torch.cuda.stream(ts):
             return linear_bwd(x, weight, dout=dout, pre=pre, act=act, want_dx=want_dx, want_dweight=want_dweight,
                               want_dbias=want_dbias, workspace=workspace, stream=ts)
-    lib = _b.load_library()
-    M, K, N, shape, dt, dev = _check_inputs(x, weight)
-    _b._check(dout, "dout", shape, x.dtype, dev)
-    _b._check(pre, "pre", shape, torch.float32, dev)
+    M, K, N, shape, dt = _check_inputs(x, weight)
+    raw = launch_stream(x, stream)
+    check_like(x, shape, ("dout", dout))
+    if pre is not None:
+        check_f32(x, shape, ("pre", pre))
+    _, need = _sizes(M, K, N, dt, act)
     dims = make_linear_dims(M, K, N, dt, act=act)
-    workspace = _workspace(dims, linear_bwd_workspace_bytes(dims), workspace, dev)
-    g = dict(dx=torch.empty_like(x) if want_dx else None, dweight=torch.empty_like(weight) if want_dweight else None,
-             dbias=torch.empty(N, dtype=torch.float32, device=dev) if want_dbias else None)
-    rc = lib.mamba_linear_bwd(_b._ptr(x), _b._ptr(weight), _b._ptr(pre), _b._ptr(dout), ctypes.byref(dims),
-                              _b._ptr(g["dx"]), _b._ptr(g["dweight"]), _b._ptr(g["dbias"]), _b._stream(stream))
-    if rc != _b.MAMBA_OK:
-        raise _b.MambaError(rc, "mamba_linear_bwd")
-    return g
+    workspace = use_workspace(dims, need, workspace, x)
+    dx = torch.empty_like(x) if want_dx else None
+    dweight = torch.empty_like(weight) if want_dweight else None
+    dbias = torch.empty(N, dtype=torch.float32, device=x.device) if want_dbias else None
+    done(_b.load_library().mamba_linear_bwd(x.data_ptr(), weight.data_ptr(), ptr(pre), dout.data_ptr(),
+                                            ctypes.byref(dims), ptr(dx), ptr(dweight), ptr(dbias), raw),
+         "mamba_linear_bwd")
+    return dict(dx=dx, dweight=dweight, dbias=dbias)

@@ -4,9 +4,10 @@ out = act((x - mean)·rstd·weight + bias) over G groups of channels."""
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from . import _binding as _b
-from ._glr import _query, _workspace
+from ._call import check_f32, check_like, done, launch_stream, ptr, query, use_workspace
 
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = 0, 1, 2, 3
 
@@ -37,21 +38,28 @@ def make_norm_dims(batch, seqlen, dim, groups, dtype, *, act=ACT_NONE, eps=1e-5,
 
 
 def group_norm_fwd_workspace_bytes(dims: NormDims) -> int:
-    return _query("mamba_group_norm_fwd_workspace_bytes", dims)
+    return query("mamba_group_norm_fwd_workspace_bytes", dims)
 
 
 def group_norm_bwd_workspace_bytes(dims: NormDims) -> int:
-    return _query("mamba_group_norm_bwd_workspace_bytes", dims)
+    return query("mamba_group_norm_bwd_workspace_bytes", dims)
+
+
+@functools.lru_cache(maxsize=512)
+def _sizes(Bsz, L, Dm, groups, dt):
+    """(forward, backward) workspace: pure functions of the sizes."""
+    d = make_norm_dims(Bsz, L, Dm, groups, dt)
+    return group_norm_fwd_workspace_bytes(d), group_norm_bwd_workspace_bytes(d)
 
 
 def _check_inputs(x, weight, bias):
-    import torch
     if x.dim() != 3:
         raise ValueError("x must be [B][L][D], got %s" % (tuple(x.shape),))
-    _b._check(x, "x", tuple(x.shape), x.dtype, x.device)
-    _b._check(weight, "weight", (x.shape[2],), torch.float32, x.device)
-    _b._check(bias, "bias", (x.shape[2],), torch.float32, x.device)
-    return tuple(x.shape) + (_b._dtype_code(x), x.device)
+    dt = _b._dtype_code(x)
+    shape = x.shape
+    check_like(x, shape, ("x", x))
+    check_f32(x, shape[2:], ("weight", weight), ("bias", bias))
+    return tuple(shape) + (dt,)
 
 
 def group_norm_fwd(x, groups, weight=None, bias=None, *, eps=1e-5, act=ACT_NONE, out=None, mean=None, rstd=None,
@@ -64,20 +72,22 @@ def group_norm_fwd(x, groups, weight=None, bias=None, *, eps=1e-5, act=ACT_NONE,
         with torch.cuda.stream(ts):
             return group_norm_fwd(x, groups, weight, bias, eps=eps, act=act, out=out, mean=mean, rstd=rstd,
                                   workspace=workspace, stream=ts)
-    lib = _b.load_library()
-    Bsz, L, Dm, dt, dev = _check_inputs(x, weight, bias)
+    Bsz, L, Dm, dt = _check_inputs(x, weight, bias)
+    raw = launch_stream(x, stream)
+    groups = int(groups)
+    need, _ = _sizes(Bsz, L, Dm, groups, dt)
     dims = make_norm_dims(Bsz, L, Dm, groups, dt, act=act, eps=eps)
-    workspace = _workspace(dims, group_norm_fwd_workspace_bytes(dims), workspace, dev)
-    out = torch.empty_like(x) if out is None else out
-    _b._check(out, "out", (Bsz, L, Dm), x.dtype, dev)
-    mean = torch.empty((Bsz, groups), dtype=torch.float32, device=dev) if mean is None else mean
-    rstd = torch.empty((Bsz, groups), dtype=torch.float32, device=dev) if rstd is None else rstd
-    _b._check(mean, "mean", (Bsz, groups), torch.float32, dev)
-    _b._check(rstd, "rstd", (Bsz, groups), torch.float32, dev)
-    rc = lib.mamba_group_norm_fwd(_b._ptr(x), _b._ptr(weight), _b._ptr(bias), ctypes.byref(dims), _b._ptr(out),
-                                  _b._ptr(mean), _b._ptr(rstd), _b._stream(stream))
-    if rc != _b.MAMBA_OK:
-        raise _b.MambaError(rc, "mamba_group_norm_fwd")
+    workspace = use_workspace(dims, need, workspace, x)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        check_like(x, x.shape, ("out", out))
+    check_f32(x, (Bsz, groups), ("mean", mean), ("rstd", rstd))
+    mean = torch.empty((Bsz, groups), dtype=torch.float32, device=x.device) if mean is None else mean
+    rstd = torch.empty_like(mean) if rstd is None else rstd
+    done(_b.load_library().mamba_group_norm_fwd(x.data_ptr(), ptr(weight), ptr(bias), ctypes.byref(dims),
+                                                out.data_ptr(), mean.data_ptr(), rstd.data_ptr(), raw),
+         "mamba_group_norm_fwd")
     return out, mean, rstd
 
 
@@ -91,18 +101,18 @@ def group_norm_bwd(x, groups, weight=None, bias=None, *, dout, mean, rstd, act=A
         with torch.cuda.stream(ts):
             return group_norm_bwd(x, groups, weight, bias, dout=dout, mean=mean, rstd=rstd, act=act,
                                   workspace=workspace, stream=ts)
-    lib = _b.load_library()
-    Bsz, L, Dm, dt, dev = _check_inputs(x, weight, bias)
+    Bsz, L, Dm, dt = _check_inputs(x, weight, bias)
+    raw = launch_stream(x, stream)
+    groups = int(groups)
+    _, need = _sizes(Bsz, L, Dm, groups, dt)
     dims = make_norm_dims(Bsz, L, Dm, groups, dt, act=act)
-    workspace = _workspace(dims, group_norm_bwd_workspace_bytes(dims), workspace, dev)
-    _b._check(dout, "dout", (Bsz, L, Dm), x.dtype, dev)
-    _b._check(mean, "mean", (Bsz, groups), torch.float32, dev)
-    _b._check(rstd, "rstd", (Bsz, groups), torch.float32, dev)
-    g = dict(dx=torch.empty_like(x), dweight=None if weight is None else torch.empty_like(weight),
-             dbias=None if bias is None else torch.empty_like(bias))
-    rc = lib.mamba_group_norm_bwd(_b._ptr(x), _b._ptr(weight), _b._ptr(bias), _b._ptr(dout), _b._ptr(mean),
-                                  _b._ptr(rstd), ctypes.byref(dims), _b._ptr(g["dx"]), _b._ptr(g["dweight"]),
-                                  _b._ptr(g["dbias"]), _b._stream(stream))
-    if rc != _b.MAMBA_OK:
-        raise _b.MambaError(rc, "mamba_group_norm_bwd")
-    return g
+    workspace = use_workspace(dims, need, workspace, x)
+    check_like(x, x.shape, ("dout", dout))
+    check_f32(x, (Bsz, groups), ("mean", mean), ("rstd", rstd))
+    dx = torch.empty_like(x)
+    dweight = None if weight is None else torch.empty_like(weight)
+    dbias = None if bias is None else torch.empty_like(bias)
+    done(_b.load_library().mamba_group_norm_bwd(x.data_ptr(), ptr(weight), ptr(bias), dout.data_ptr(),
+                                                mean.data_ptr(), rstd.data_ptr(), ctypes.byref(dims), dx.data_ptr(),
+                                                ptr(dweight), ptr(dbias), raw), "mamba_group_norm_bwd")
+    return dict(dx=dx, dweight=dweight, dbias=dbias)

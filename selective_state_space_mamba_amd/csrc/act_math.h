@@ -8,12 +8,31 @@ namespace mscan {
 
 enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3 };
 
-// relu u if u > 0 else 0 (NaN stays NaN); silu u·sigmoid(u); gelu u·Φ(u), Φ the normal distribution's cdf
+// The standard normal cdf at u and e^{-u²/2}.  With x = |u|/sqrt 2,
+// erfc(x) = (a1 t + a2 t² + a3 t³ + a4 t⁴ + a5 t⁵)·e^{-x²}, t = 1/(1 + 0.3275911 x)
+// to 1.5e-7 absolute (Abramowitz and Stegun, Handbook of Mathematical
+// Functions, 7.1.26), so the cdf to 7.5e-8, the rounding of a float32 near 1;
+// the exponential serves the derivative too.  (The library's erf is three times
+// as many instructions: 16384 x 768 x 1536 with gelu took 92 us with it.)
+__device__ __forceinline__ float normal_cdf(float u, float& e) {
+  e = ex2(-0.5f * kLog2e * u * u);
+  const float t = rcp(__builtin_fmaf(__builtin_fabsf(u), 0.23164189f, 1.0f));
+  const float poly =
+      t * __builtin_fmaf(t, __builtin_fmaf(t, __builtin_fmaf(t, __builtin_fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                         0.254829592f);
+  const float tail = 0.5f * poly * e;  // the cdf at -|u|
+  return u < 0.f ? tail : 1.0f - tail;
+}
+
+// relu u if u > 0 else 0 (NaN stays NaN); silu u·sigmoid(u); gelu u·Φ(u), Φ the normal cdf
 template <int ACT>
 __device__ __forceinline__ float act_f(float u) {
   if constexpr (ACT == ACT_RELU) return u <= 0.f ? 0.f : u;
   if constexpr (ACT == ACT_SILU) return u * rcp(1.0f + ex2(-u * kLog2e));
-  if constexpr (ACT == ACT_GELU) return 0.5f * u * (1.0f + erff(u * 0.70710678118654752440f));
+  if constexpr (ACT == ACT_GELU) {
+    float e;
+    return u * normal_cdf(u, e);
+  }
   return u;
 }
 
@@ -26,8 +45,9 @@ __device__ __forceinline__ float act_d(float u) {
     return q * __builtin_fmaf(u, 1.0f - q, 1.0f);
   }
   if constexpr (ACT == ACT_GELU) {
-    const float cdf = 0.5f * (1.0f + erff(u * 0.70710678118654752440f));
-    return __builtin_fmaf(u * 0.39894228040143267794f, ex2(-0.5f * kLog2e * u * u), cdf);
+    float e;
+    const float cdf = normal_cdf(u, e);
+    return __builtin_fmaf(u * 0.39894228040143267794f, e, cdf);
   }
   return 1.f;
 }

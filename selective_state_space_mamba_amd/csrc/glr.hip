@@ -63,6 +63,7 @@ void glr_params(const mamba_glr_dims* g, const GlrPlan& pl, GlrParams* p) {
   p->nblk = pl.nblk;
   p->reverse = g->reverse ? 1 : 0;
   p->scale = g->scale;
+  p->block = p->B * pl.nblk < 8 ? 16 : 4;
 }
 
 // Points p at the chain's words in the workspace and clears them.

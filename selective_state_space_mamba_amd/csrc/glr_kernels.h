@@ -68,6 +68,7 @@ struct GlrParams {
   // the chain (null: one workgroup walks the tiles of its rows)
   uint64_t* words;            // 3 x [rows][tiles][64]
   uint32_t* ticket;
+  int block;  // tiles of a block
   int B, L, D, nblk, ntiles, reverse;
   float scale;
 };
@@ -161,17 +162,26 @@ __device__ __forceinline__ float run_mul(float A, float B) {
 // knows the state that enters it, the state that leaves it.  Each value is one
 // 64-bit word {1 : value}, stored and loaded atomically at agent scope, so a
 // word that is there is whole and no fence (which would write back the L2) is
-// needed; the words start at zero.  A tile takes the nearest state that is
-// there within a window of tiles behind it and applies the runs in between, in
-// order; since a state is made by exactly that operation, the result does not
-// depend on how far the others have come: every call gives the same bits.
+// needed; the words start at zero.
+//
+// Waiting only for the tile before would make a sequence of as many waits as
+// tiles.  So the tiles form blocks: a block's last tile joins the
+// block's runs, which need no one's state, and publishes the state that leaves
+// the block as that joint run's image of the state that entered it; the waits in
+// sequence are one a block.  Every other tile takes the state that enters its
+// block, or that leaves the tile before if it is there already, and applies the
+// runs in between in order; since the tile before made its state by exactly
+// those operations, both give the same bits, and no result depends on how far
+// the others have come.
 // Tickets hand the tiles out in the order of the chain, so a workgroup only
 // ever waits for one that has already started, and every wait ends.
-// (The window costs registers in a kernel that has none to spare, and saves
-// waits where few rows make many tiles wait at once: forward, 3 x 4133 x 392 in
-// float32 took 37, 31, 28.7 and 28.4 us with 1, 2, 3 and 4 tiles; backward, 8 x
-// 2048 x 1536 in bf16 took 124 us with 3 and 113 with 2.)
-constexpr int kGlrFwdWindow = 3, kGlrBwdWindow = 2;
+// Longer blocks cost their last tile more and the others a longer way to their
+// state: they pay where few rows leave the waits as all there is.  us forward /
+// backward in bf16 with blocks of 4, 8 and 16: 1 x 26155 x 16 (one row) 37 / 67,
+// 23 / 42, 19 / 32 (waiting for the tile before alone: 56 / 138); 12 x 28897 x
+// 16 67 / 117, 66 / 120, 70 / 122; 1 x 262144 x 2048 (32 rows) 1261 / 2302,
+// 1307 / 2318, 1361 / 2348.
+constexpr int kGlrBatch = 3;  // runs fetched at a time: what the registers leave
 
 __device__ __forceinline__ void word_put(uint64_t* p, float v) {
   __hip_atomic_store(p, ((uint64_t)1 << 32) | __float_as_uint(v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -182,48 +192,82 @@ __device__ __forceinline__ uint64_t word_get(const uint64_t* p) {
 __device__ __forceinline__ bool word_there(uint64_t w) { return (uint32_t)(w >> 32) != 0; }
 __device__ __forceinline__ float word_val(uint64_t w) { return __uint_as_float((uint32_t)w); }
 
-// One wave, one channel a lane.  step: the tile's place in the chain; first:
-// the state that enters place 0.  Returns the state that enters this tile and
-// publishes the one that leaves it.
-template <bool RESET, int WINDOW>
+// Runs 0..n-1 of a block, kGlrBatch at a time once they are there: f(A, H) in order.
+template <typename F>
+__device__ __forceinline__ void chain_runs(const uint64_t* wa, const uint64_t* wh, int n, F f) {
+#pragma unroll 1  // (unrolled it takes the registers of a wave)
+  for (int k0 = 0; k0 < n; k0 += kGlrBatch) {
+    uint64_t a[kGlrBatch], h[kGlrBatch];
+    for (;;) {
+      bool ok = true;
+#pragma unroll
+      for (int k = 0; k < kGlrBatch; ++k) {
+        const int at = min(k0 + k, n - 1) * kGlrCB;
+        a[k] = word_get(wa + at);
+        h[k] = word_get(wh + at);
+      }
+#pragma unroll
+      for (int k = 0; k < kGlrBatch; ++k) ok = ok && word_there(a[k]) && word_there(h[k]);
+      if (__all(ok)) break;
+      __builtin_amdgcn_s_sleep(1);
+    }
+#pragma unroll
+    for (int k = 0; k < kGlrBatch; ++k)
+      if (k0 + k < n) f(word_val(a[k]), word_val(h[k]));
+  }
+}
+
+// One wave, one channel a lane.  step: the tile's place in the chain; (A, H)
+// its run; first: the state that enters place 0.  Returns the state that enters
+// this tile and publishes the one that leaves it.
+template <bool RESET>
 __device__ __forceinline__ float chain_carry(const GlrParams& p, int row, int step, int lane, float A, float H, float first) {
   const int64_t stride = (int64_t)p.B * p.nblk * p.ntiles * kGlrCB;
+  const int in = step % p.block;  // place in the block
   uint64_t* const inc = p.words + ((int64_t)row * p.ntiles + step) * kGlrCB + lane;
   uint64_t* const wa = inc + stride;
   uint64_t* const wh = wa + stride;
-  float v = first;
-  if (step > 0) {
-    uint64_t w = word_get(inc - kGlrCB);
-    if (!__all(word_there(w))) {
-      word_put(wa, A);
-      word_put(wh, H);
-      for (;;) {
-        uint64_t si[WINDOW], sa[WINDOW], sh[WINDOW];
-#pragma unroll
-        for (int k = 0; k < WINDOW; ++k) {
-          const int back = min(k + 1, step) * kGlrCB;
-          si[k] = word_get(inc - back);
-          sa[k] = word_get(wa - back);
-          sh[k] = word_get(wh - back);
-        }
-        bool ok = false;
-#pragma unroll
-        for (int k = WINDOW - 1; k >= 0; --k) {
-          if (k + 1 <= step) {
-            const float next = run_apply<RESET>(word_val(sa[k]), word_val(sh[k]), v);
-            const bool run = word_there(sa[k]) && word_there(sh[k]), have = word_there(si[k]);
-            v = have ? word_val(si[k]) : next;
-            ok = have || (ok && run);
-          }
-        }
-        if (__all(ok)) break;
-        __builtin_amdgcn_s_sleep(2);
-      }
-    } else {
+  const uint64_t *const ba = wa - in * kGlrCB, *const bh = wh - in * kGlrCB;  // the block's runs
+  const uint64_t* const bi = inc - (in + 1) * kGlrCB;                         // the state that enters the block
+  const bool ends = in == p.block - 1, from_start = step == in;
+  if (step + 1 == p.ntiles) {
+    // no one follows
+  } else if (!ends) {
+    word_put(wa, A);
+    word_put(wh, H);
+  } else {  // the block's run, then its image
+    float JA = 1.f, JH = 0.f;
+    chain_runs(ba, bh, in, [&](float a, float h) {
+      JH = run_apply<RESET>(a, h, JH);
+      JA = run_mul<RESET>(JA, a);
+    });
+    JH = run_apply<RESET>(A, H, JH);
+    JA = run_mul<RESET>(JA, A);
+    float v = first;
+    if (!from_start) {
+      uint64_t w;
+      while (!__all(word_there(w = word_get(bi)))) __builtin_amdgcn_s_sleep(1);
       v = word_val(w);
     }
+    word_put(inc, run_apply<RESET>(JA, JH, v));
   }
-  word_put(inc, run_apply<RESET>(A, H, v));
+  float v = first;
+  if (step > 0) {
+    for (;;) {
+      const uint64_t w = word_get(inc - kGlrCB), e = from_start ? ~(uint64_t)0 : word_get(bi);
+      if (__all(word_there(w))) {
+        v = word_val(w);
+        break;
+      }
+      if (__all(word_there(e))) {
+        if (!from_start) v = word_val(e);
+        chain_runs(ba, bh, in, [&](float a, float h) { v = run_apply<RESET>(a, h, v); });
+        break;
+      }
+      __builtin_amdgcn_s_sleep(1);
+    }
+  }
+  if (!ends && step + 1 < p.ntiles) word_put(inc, run_apply<RESET>(A, H, v));
   return v;
 }
 
@@ -388,7 +432,7 @@ __global__ void __launch_bounds__(64 * GlrGeom<T>::FW) glr_fwd_kernel(const GlrP
           Ht = run_apply<RESET>(sA[w][lane], sH[w][lane], Ht);
           At = run_mul<RESET>(At, sA[w][lane]);
         }
-        carry = chain_carry<RESET, kGlrFwdWindow>(p, row, tile, lane, At, Ht, carry);
+        carry = chain_carry<RESET>(p, row, tile, lane, At, Ht, carry);
       }
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
@@ -614,7 +658,7 @@ __global__ void __launch_bounds__(64 * GlrGeom<T>::BW, 3) glr_bwd_kernel(const G
           Gt = run_apply<RESET>(sA[u][lane], sG[u][lane], Gt);
           At = run_mul<RESET>(At, sA[u][lane]);
         }
-        carry = chain_carry<RESET, kGlrBwdWindow>(p, row, step, lane, At, Gt, carry);
+        carry = chain_carry<RESET>(p, row, step, lane, At, Gt, carry);
       }
 #pragma unroll
       for (int u = NW - 1; u >= 0; --u) {

@@ -37,25 +37,26 @@ struct ProductPlan {
 //   256 x 256   6.4 + 0.0293 K   (16384 x 768 x 1536: 2 rounds, 57.8; 65536 x 2048 x 2048: 8 rounds, 531)
 // so that how evenly the tiles fill the rounds decides.  A contraction is
 // shared out where the tiles alone leave compute units idle, in shares of at
-// least 8 stages; the shares' sums then cost a launch and their bytes, written
+// least 8 stages (float32: 2, each as long as 16); the shares' sums then cost a launch and their bytes, written
 // and read.  float32 products are bound by the matrix instructions' rate (a
-// sixteenth of bf16's) with any tile and take the small one.
+// sixteenth of bf16's) with any tile and take the small one, at 8 times its
+// time for a contraction element (16384 x 768 x 1536: 3 rounds, 291).
 ProductPlan plan_product(int64_t M, int64_t N, int64_t K, bool bf16) {
   static const struct { int bm, bn, slots; double fix, per; } kTiles[3] = {
       {128, 128, 512, 5.8, 0.0158}, {256, 192, 256, 7.8, 0.0217}, {256, 256, 256, 6.4, 0.0293}};
   const int bk = bf16 ? 64 : 32;
-  const int64_t kts = (K + bk - 1) / bk;
+  const int64_t kts = (K + bk - 1) / bk, least = bf16 ? 8 : 2;
   ProductPlan best{};
   double best_us = 1e300;
   for (int t = 0; t < (bf16 ? 3 : 1); ++t) {
     if (MSCAN_LINEAR_FORCE >= 0 && bf16 && t != MSCAN_LINEAR_FORCE) continue;
     const int64_t tm = (M + kTiles[t].bm - 1) / kTiles[t].bm, tn = (N + kTiles[t].bn - 1) / kTiles[t].bn, tiles = tm * tn;
     int64_t most = tiles < kTiles[t].slots ? kTiles[t].slots / tiles : 1;
-    if (most > kts / 8) most = kts / 8 > 0 ? kts / 8 : 1;
+    if (most > kts / least) most = kts / least > 0 ? kts / least : 1;
     for (int64_t s : {(int64_t)1, most}) {
       const int64_t per = (kts + s - 1) / s, splits = (kts + per - 1) / per;
       const int64_t rounds = (tiles * splits + kTiles[t].slots - 1) / kTiles[t].slots;
-      double us = (double)rounds * (kTiles[t].fix + kTiles[t].per * (double)(per * bk) * (bf16 ? 1 : 16));
+      double us = (double)rounds * (kTiles[t].fix + kTiles[t].per * (double)(per * bk) * (bf16 ? 1 : 8));
       if (splits > 1) us += 4.0 + (double)splits * (double)M * (double)N * 8.0 / 5.0e6;
       if (us < best_us) {
         best_us = us;

@@ -68,13 +68,12 @@ __device__ __forceinline__ void linear_bias(const LinearParams& p, int n, float 
 // lane then holds 8 neighbouring columns and a few lanes a whole row segment:
 // stores and residual loads of 16 bytes a lane and whole cache lines.
 template <typename T, int FM, int FN>
-__device__ __forceinline__ void linear_out(const LinearParams& p, f32x16 (&acc)[FN][FM], float* lds, int m0, int n0, int lane) {
+__device__ __forceinline__ void linear_out(const LinearParams& p, f32x16 (&acc)[FN][FM], const float (&bias)[8], float* lds, int m0,
+                                           int n0, int lane) {
   constexpr int W = FN * 32, kRow = W + 4;  // (rows 16 bytes apart in the banks)
   constexpr int LPR = W / 8, RPI = 64 / LPR, IT = (32 + RPI - 1) / RPI;
   const int r0 = lane / LPR, n = n0 + (lane % LPR) * 8;
   const bool on = lane < LPR * RPI && n < p.N;
-  float bias[8];
-  linear_bias(p, n, bias);
 #pragma unroll
   for (int j = 0; j < FM; ++j) {
     const int mb = m0 + j * 32;
@@ -290,6 +289,25 @@ __device__ __forceinline__ void mma_half(const typename E::Frag (&fa)[2][FM], co
 #pragma unroll
       for (int j = 0; j < FM; ++j) acc[i][j] = E::mma(fb[ks][i], fa[ks][j], acc[i][j]);
 }
+// float32's instructions are slow enough (16 to a bf16 one's work) that blocks
+// without outputs are worth a branch: dw of 641 x 24 x 16 28 -> 9 us, with the
+// contraction in more shares.
+template <typename E, int FM, int FN>
+__device__ __forceinline__ void mma_live(const typename E::Frag (&fa)[2][FM], const typename E::Frag (&fb)[2][FN], f32x16 (&acc)[FN][FM],
+                                         int live_m, int live_n) {
+  if (E::CH == 8 || (live_m >= FM && live_n >= FN)) {
+    mma_half<E>(fa, fb, acc);
+  } else {
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j)
+        if (i < live_n && j < live_m) {
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) acc[i][j] = E::mma(fb[ks][i], fa[ks][j], acc[i][j]);
+        }
+  }
+}
 template <int FM, int FN>
 __device__ __forceinline__ void acc_zero(f32x16 (&acc)[FN][FM]) {
 #pragma unroll
@@ -312,8 +330,11 @@ __global__ void __launch_bounds__(256, 2) linear_tile_kernel(const LinearParams 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
   const Tl t(p, wave, lane);
+  float bias[8];  // of the lane's columns in linear_out, here so that it has arrived by then
+  linear_bias(p, t.n0 + wn + (lane & 7) * 8, bias);
   f32x16 acc[2][2];
   acc_zero(acc);
+  const int live_m = (p.M - t.m0 - wm + 31) / 32, live_n = (p.N - t.n0 - wn + 31) / 32;  // blocks with outputs
   if (t.kt0 < t.kt1) t.fetch(p, lds, t.kt0, wave);
   for (int kt = t.kt0; kt < t.kt1; ++kt) {
     wait_loads();
@@ -328,18 +349,18 @@ __global__ void __launch_bounds__(256, 2) linear_tile_kernel(const LinearParams 
     if constexpr (!TA && !TB) {
       Tl::SA::template frags<2>(la, wm, 1, lane, fa[1]);
       Tl::SB::template frags<2>(lb, wn, 1, lane, fb[1]);
-      mma_half<E>(fa[0], fb[0], acc);
+      mma_live<E>(fa[0], fb[0], acc, live_m, live_n);
     } else {
-      mma_half<E>(fa[0], fb[0], acc);
+      mma_live<E>(fa[0], fb[0], acc, live_m, live_n);
       Tl::SA::template frags<2>(la, wm, 1, lane, fa[1]);
       Tl::SB::template frags<2>(lb, wn, 1, lane, fb[1]);
     }
-    mma_half<E>(fa[1], fb[1], acc);
+    mma_live<E>(fa[1], fb[1], acc, live_m, live_n);
     asm volatile("" ::: "memory");
   }
   __syncthreads();
   static_assert(4 * 32 * 68 * 4 <= (int)sizeof(lds), "the bands fit the stages");
-  linear_out<T>(p, acc, reinterpret_cast<float*>(lds) + wave * 32 * 68, t.m0 + wm, t.n0 + wn, lane);
+  linear_out<T>(p, acc, bias, reinterpret_cast<float*>(lds) + wave * 32 * 68, t.m0 + wm, t.n0 + wn, lane);
 }
 
 // ---- the large tile: 256 x BN, eight waves, one workgroup a compute unit ----
@@ -367,6 +388,8 @@ __global__ void __launch_bounds__(512) linear_large_kernel(const LinearParams p)
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = (wave / WN) * TM, wn = (wave % WN) * TN;
   const Tl t(p, wave, lane);
+  float bias[8];
+  linear_bias(p, t.n0 + wn + (lane % (TN / 8)) * 8, bias);
   f32x16 acc[FN][FM];
   acc_zero(acc);
   const bool late = wave >= 4;
@@ -406,7 +429,7 @@ __global__ void __launch_bounds__(512) linear_large_kernel(const LinearParams p)
   if (!late) __builtin_amdgcn_s_barrier();
   constexpr int kWave = 32 * (TN + 4);  // floats of a wave's band
   static_assert(8 * kWave * 4 <= (int)sizeof(lds), "the bands fit the stages");
-  linear_out<T>(p, acc, reinterpret_cast<float*>(lds) + wave * kWave, t.m0 + wm, t.n0 + wn, lane);
+  linear_out<T>(p, acc, bias, reinterpret_cast<float*>(lds) + wave * kWave, t.m0 + wm, t.n0 + wn, lane);
 }
 
 // Joins the shares of a split contraction, in order, and finishes the output.
