@@ -53,15 +53,18 @@ ProductPlan plan_product(int64_t M, int64_t N, int64_t K, bool bf16) {
     const int64_t tm = (M + kTiles[t].bm - 1) / kTiles[t].bm, tn = (N + kTiles[t].bn - 1) / kTiles[t].bn, tiles = tm * tn;
     int64_t most = tiles < kTiles[t].slots ? kTiles[t].slots / tiles : 1;
     if (most > kts / least) most = kts / least > 0 ? kts / least : 1;
-    for (int64_t s : {(int64_t)1, most}) {
-      const int64_t per = (kts + s - 1) / s, splits = (kts + per - 1) / per;
-      const int64_t rounds = (tiles * splits + kTiles[t].slots - 1) / kTiles[t].slots;
-      double us = (double)rounds * (kTiles[t].fix + kTiles[t].per * (double)(per * bk) * (bf16 ? 1 : 8));
+    for (int64_t s = 1;; s = 2 * s < most ? 2 * s : most) {
+      const int64_t per = (kts + s - 1) / s, splits = (kts + per - 1) / per, wgs = tiles * splits, slots = kTiles[t].slots;
+      const int64_t rounds = (wgs + slots - 1) / slots;
+      // (a last round that leaves the small tile's workgroups a compute unit each takes 0.6 of one)
+      const double last = t == TILE_128 && (wgs - 1) % slots < 256 ? 0.6 : 1.0;
+      double us = (double)rounds * kTiles[t].fix + ((double)rounds - 1 + last) * kTiles[t].per * (double)(per * bk) * (bf16 ? 1 : 8);
       if (splits > 1) us += 4.0 + (double)splits * (double)M * (double)N * 8.0 / 5.0e6;
       if (us < best_us) {
         best_us = us;
         best = ProductPlan{t, (int)tm, (int)tn, (int)splits, (int)per, splits > 1 ? up256((size_t)splits * M * N * sizeof(float)) : 0};
       }
+      if (s >= most) break;
     }
   }
   return best;
