@@ -74,17 +74,19 @@ __device__ __forceinline__ void linear_out(const LinearParams& p, f32x16 (&acc)[
   constexpr int LPR = W / 8, RPI = 64 / LPR, IT = (32 + RPI - 1) / RPI;
   const int r0 = lane / LPR, n = n0 + (lane % LPR) * 8;
   const bool on = lane < LPR * RPI && n < p.N;
+  Vec<T, 8> res[FM][IT];  // all at once: they wait for memory one time, in the registers that the fragments have left
+  if (p.residual && !p.part) {
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+        const int r = it * RPI + r0, m = m0 + j * 32 + r;
+        if (on && r < 32 && m < p.M) res[j][it].load(static_cast<const T*>(p.residual) + (int64_t)m * p.N + n);
+      }
+  }
 #pragma unroll
   for (int j = 0; j < FM; ++j) {
     const int mb = m0 + j * 32;
-    Vec<T, 8> res[IT];
-    if (p.residual && !p.part) {
-#pragma unroll
-      for (int it = 0; it < IT; ++it) {
-        const int r = it * RPI + r0;
-        if (on && r < 32 && mb + r < p.M) res[it].load(static_cast<const T*>(p.residual) + (int64_t)(mb + r) * p.N + n);
-      }
-    }
 #pragma unroll
     for (int i = 0; i < FN; ++i)
 #pragma unroll
@@ -102,7 +104,7 @@ __device__ __forceinline__ void linear_out(const LinearParams& p, f32x16 (&acc)[
         for (int c = 0; c < 8; ++c) v[c] = f.get(c);
         const int64_t at = (int64_t)(mb + r) * p.N + n;
         if (p.part) storeV<8>(p.part + (int64_t)blockIdx.y * p.M * p.N + at, v);
-        else linear_finish(p, at, bias, res[it], v);
+        else linear_finish(p, at, bias, res[j][it], v);
       }
     }
   }
@@ -272,11 +274,17 @@ struct Tile {
     sb.init(wave, lane, p.ldb, p.N - n0);
   }
   __device__ __forceinline__ T* stage(T* lds, int kt) const { return lds + ((kt - kt0) & 1) * kStage; }
-  __device__ __forceinline__ void fetch(const LinearParams& p, T* lds, int kt, int wave) const {
+  __device__ __forceinline__ void fetch_a(const LinearParams& p, T* lds, int kt, int wave) const {
     const int k0 = kt * E::BK;
-    T* const l = stage(lds, kt);
-    sa.fetch(a + (TA ? k0 * p.lda : (int64_t)k0), l, wave, p.K - k0);
-    sb.fetch(b + (TB ? k0 * p.ldb : (int64_t)k0), l + SA::kElems, wave, p.K - k0);
+    sa.fetch(a + (TA ? k0 * p.lda : (int64_t)k0), stage(lds, kt), wave, p.K - k0);
+  }
+  __device__ __forceinline__ void fetch_b(const LinearParams& p, T* lds, int kt, int wave) const {
+    const int k0 = kt * E::BK;
+    sb.fetch(b + (TB ? k0 * p.ldb : (int64_t)k0), stage(lds, kt) + SA::kElems, wave, p.K - k0);
+  }
+  __device__ __forceinline__ void fetch(const LinearParams& p, T* lds, int kt, int wave) const {
+    fetch_a(p, lds, kt, wave);
+    fetch_b(p, lds, kt, wave);
   }
 };
 
@@ -318,6 +326,15 @@ __device__ __forceinline__ void acc_zero(f32x16 (&acc)[FN][FM]) {
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 }
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+// A barrier that no access to memory, and no other instruction, is moved over by the compiler (the builtin alone orders neither).
+__device__ __forceinline__ void meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+}
 
 // ---- the small tile: 128 x 128, four waves, two workgroups a compute unit ----
 // Two stages of LDS; while one is multiplied, the other is filled.  One
@@ -337,9 +354,9 @@ __global__ void __launch_bounds__(256, 2) linear_tile_kernel(const LinearParams 
   const int live_m = (p.M - t.m0 - wm + 31) / 32, live_n = (p.N - t.n0 - wn + 31) / 32;  // blocks with outputs
   if (t.kt0 < t.kt1) t.fetch(p, lds, t.kt0, wave);
   for (int kt = t.kt0; kt < t.kt1; ++kt) {
-    wait_loads();
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    wait_loads();  // of this stage, and the last one's fragments, before anyone refills its buffer
+    wait_lds();
+    meet();
     if (kt + 1 < t.kt1) t.fetch(p, lds, kt + 1, wave);
     const T* const la = t.stage(lds, kt);
     const T* const lb = la + Tl::SA::kElems;
@@ -356,7 +373,6 @@ __global__ void __launch_bounds__(256, 2) linear_tile_kernel(const LinearParams 
       Tl::SB::template frags<2>(lb, wn, 1, lane, fb[1]);
     }
     mma_live<E>(fa[1], fb[1], acc, live_m, live_n);
-    asm volatile("" ::: "memory");
   }
   __syncthreads();
   static_assert(4 * 32 * 68 * 4 <= (int)sizeof(lds), "the bands fit the stages");
@@ -372,8 +388,10 @@ __global__ void __launch_bounds__(256, 2) linear_tile_kernel(const LinearParams 
 // every half step; the late group waits at one more before the first and the
 // early group at one more after the last, so both meet the same number.
 //   - A stage's last reads are the late group's, one half step after the early
-//     group's; the early group refills that buffer in its next reading half
-//     step, the late one at the start of the multiplying half step beside it.
+//     group's; the early group refills that buffer in its next two reading half
+//     steps (an operand in each: together the loads' addresses would take longer
+//     than the other group's products; 65536 x 2048 x 2048: 522 us against 570),
+//     the late one at the start of the multiplying half step beside the first.
 //   - Each wave has waited for its own loads of a stage before the barrier that
 //     lets the early group read it: the late group at the end of its last
 //     reading half step before, the early one at the end of its last
@@ -400,33 +418,29 @@ __global__ void __launch_bounds__(512) linear_large_kernel(const LinearParams p)
   } else {
     wait_loads();
   }
-  __builtin_amdgcn_s_barrier();
-  if (late) __builtin_amdgcn_s_barrier();
+  meet();
+  if (late) meet();
   for (int kt = t.kt0; kt < t.kt1; ++kt) {
     const T* const la = t.stage(lds, kt);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       typename E::Frag fa[2][FM], fb[2][FN];
-      __builtin_amdgcn_sched_barrier(0);
-      if (h == 0 && !late && kt + 1 < t.kt1) t.fetch(p, lds, kt + 1, wave);
+      if (!late && kt + 1 < t.kt1) {
+        if (h == 0) t.fetch_a(p, lds, kt + 1, wave);
+        else t.fetch_b(p, lds, kt + 1, wave);
+      }
       Tl::SA::template frags<FM>(la, wm, h, lane, fa);
       Tl::SB::template frags<FN>(la + Tl::SA::kElems, wn, h, lane, fb);
       if (h == 1 && late) wait_loads();
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_sched_barrier(0);
+      wait_lds();
+      meet();
       if (h == 1 && late && kt + 2 < t.kt1) t.fetch(p, lds, kt + 2, wave);
-      __builtin_amdgcn_s_setprio(1);
       mma_half<E>(fa, fb, acc);
-      __builtin_amdgcn_s_setprio(0);
       if (h == 1 && !late) wait_loads();
-      __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_sched_barrier(0);
+      meet();
     }
   }
-  if (!late) __builtin_amdgcn_s_barrier();
+  if (!late) meet();
   constexpr int kWave = 32 * (TN + 4);  // floats of a wave's band
   static_assert(8 * kWave * 4 <= (int)sizeof(lds), "the bands fit the stages");
   linear_out<T>(p, acc, bias, reinterpret_cast<float*>(lds) + wave * kWave, t.m0 + wm, t.n0 + wn, lane);
