@@ -8,17 +8,31 @@ import ctypes
 from . import _binding as _b
 
 
+def _raw_current():
+    """device -> torch's current stream there as a raw handle.  torch.cuda's own
+    way makes a Stream object (1.1 us of a 10 us call); torch._C has the handle alone."""
+    import torch
+    return getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+_current = None
+
+
 def launch_stream(x, stream) -> int:
     """The raw stream to launch on (torch's current one where stream is None).
     x has to be on the current GPU: that is the device the library launches on."""
+    global _current
     import torch
-    dev = x.get_device() if x.is_cuda else -1
-    if dev < 0:
+    dev = x.get_device()
+    if dev < 0 or not x.is_cuda:
         raise ValueError("x is on %s, a GPU is needed" % x.device)
     if dev != torch.cuda.current_device():
         raise ValueError("x is on cuda:%d, the current device is cuda:%d" % (dev, torch.cuda.current_device()))
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        if _current is None:
+            _current = _raw_current()
+        return _current(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 

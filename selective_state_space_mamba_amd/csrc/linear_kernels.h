@@ -8,8 +8,8 @@
 // its contraction axis contiguous (x, W and dP of the forward and of dx) or
 // with the rows of the contraction one after the other (W of dx; dP and x of
 // dW); it is staged in LDS as it lies and the second kind is turned on the way
-// to the registers by the transposing LDS read (bf16: 16 lanes read 4 contraction rows of 16 columns, lane i receives
-// column i).  Products are 32 x 32 x 16 (bf16) or 32 x 32 x 2 (float32) matrix
+// to the registers by the transposing LDS read (bf16: 16 lanes read 4
+// contraction rows of 16 columns, lane i receives column i).  Products are 32 x 32 x 16 (bf16) or 32 x 32 x 2 (float32) matrix
 // instructions with float32 sums; the output's column axis N takes the
 // instruction's row side, which leaves each lane with four neighbouring
 // columns of one output row.
@@ -24,7 +24,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 struct LinearParams {
   const void* a;         // rows of the output (M side)
@@ -40,16 +39,17 @@ struct LinearParams {
 };
 
 // V neighbouring outputs of one row, whose bias and residual are at hand.
+// Plain stores: the last-level cache takes a round's outputs at once, where
+// stores past it hold up the end of every tile (16384 x 768 x 1536 with pre
+// 79 -> 64 us, 4096 x 1024 x 4096 60 -> 47; 32768 x 2048 x 2048, whose outputs
+// the cache does not hold, 304 with either).
 template <typename T, int V>
 __device__ __forceinline__ void linear_finish(const LinearParams& p, int64_t at, const float (&bias)[V], const Vec<T, V>& res,
                                               float (&v)[V]) {
 #pragma unroll
   for (int j = 0; j < V; ++j) v[j] += bias[j];
-  if (p.pre) storeV_nt<V>(p.pre + at, v);
-  if (p.act != ACT_NONE) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = act_any(v[j], p.act);
-  }
+  if (p.pre) storeV<V>(p.pre + at, v);
+  act_all(v, p.act);
   if (p.residual) {
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] += res.get(j);
@@ -62,17 +62,23 @@ __device__ __forceinline__ void linear_bias(const LinearParams& p, int n, float 
   for (int j = 0; j < V; ++j) bias[j] = p.bias && n < p.N ? p.bias[n + j] : 0.f;
 }
 
+// Where a lane's 8 columns begin among the wave's, of which it holds the c-th eight.
+template <int STEP>
+__device__ __forceinline__ int linear_col(int c) {
+  return (c >> 2) * STEP + (c & 3) * 8;
+}
+
 // A wave's outputs, FM x FN blocks of 32 x 32 (element e of a lane: output row
-// lane%32, column 8·(e/4) + 4·(lane/32) + e%4 of the block), from row m0 and
-// column n0.  Each band of 32 rows goes through the wave's own LDS, so that a
+// lane%32, column 8·(e/4) + 4·(lane/32) + e%4 of the block), STEP rows and
+// columns apart from row m0 and column n0 on.  Each band of 32 rows goes through the wave's own LDS, so that a
 // lane then holds 8 neighbouring columns and a few lanes a whole row segment:
 // stores and residual loads of 16 bytes a lane and whole cache lines.
-template <typename T, int FM, int FN>
+template <typename T, int STEP, int FM, int FN>
 __device__ __forceinline__ void linear_out(const LinearParams& p, f32x16 (&acc)[FN][FM], const float (&bias)[8], float* lds, int m0,
                                            int n0, int lane) {
   constexpr int W = FN * 32, kRow = W + 4;  // (rows 16 bytes apart in the banks)
   constexpr int LPR = W / 8, RPI = 64 / LPR, IT = (32 + RPI - 1) / RPI;
-  const int r0 = lane / LPR, n = n0 + (lane % LPR) * 8;
+  const int r0 = lane / LPR, n = n0 + linear_col<STEP>(lane % LPR);
   const bool on = lane < LPR * RPI && n < p.N;
   Vec<T, 8> res[FM][IT];  // all at once: they wait for memory one time, in the registers that the fragments have left
   if (p.residual && !p.part) {
@@ -80,13 +86,13 @@ __device__ __forceinline__ void linear_out(const LinearParams& p, f32x16 (&acc)[
     for (int j = 0; j < FM; ++j)
 #pragma unroll
       for (int it = 0; it < IT; ++it) {
-        const int r = it * RPI + r0, m = m0 + j * 32 + r;
+        const int r = it * RPI + r0, m = m0 + j * STEP + r;
         if (on && r < 32 && m < p.M) res[j][it].load(static_cast<const T*>(p.residual) + (int64_t)m * p.N + n);
       }
   }
 #pragma unroll
   for (int j = 0; j < FM; ++j) {
-    const int mb = m0 + j * 32;
+    const int mb = m0 + j * STEP;
 #pragma unroll
     for (int i = 0; i < FN; ++i)
 #pragma unroll
@@ -189,9 +195,9 @@ struct Stage {
     }
 #endif
   }
-  // Fragments of rows r0 + 32 j (j < NF) of half h of the stage, two ksteps:
+  // Fragments of rows r0 + STEP j (j < NF) and the 31 after each, of half h of the stage, two ksteps:
   // lane l holds row l%32, elements (l/32)·KS/2 onwards of the kstep.
-  template <int NF>
+  template <int NF, int STEP = 32>
   __device__ static __forceinline__ void frags(const T* lds, int r0, int h, int lane, typename E::Frag (&f)[2][NF]) {
     if constexpr (!TR) {
 #pragma unroll
@@ -199,14 +205,14 @@ struct Stage {
         const int c = (h * 4 + ks * 2 + (lane >> 5)) ^ ((lane >> 1) & 7);
         const T* const at = lds + (r0 + (lane & 31)) * kRow + c * E::CH;
 #pragma unroll
-        for (int j = 0; j < NF; ++j) f[ks][j] = *reinterpret_cast<const typename E::Frag*>(at + j * 32 * kRow);
+        for (int j = 0; j < NF; ++j) f[ks][j] = *reinterpret_cast<const typename E::Frag*>(at + j * STEP * kRow);
       }
     } else if constexpr (sizeof(T) == 2) {
       const int g = lane >> 4, i = lane & 15, k = i >> 2;
       typedef __attribute__((address_space(3))) const T* P;
 #pragma unroll
       for (int j = 0; j < NF; ++j) {
-        const uint32_t at = (uint32_t)(uintptr_t)(P)(lds + (h * 2 * E::KS + (g >> 1) * 8 + k) * kRow + ((r0 + j * 32) ^ (swz(k) << 5)) +
+        const uint32_t at = (uint32_t)(uintptr_t)(P)(lds + (h * 2 * E::KS + (g >> 1) * 8 + k) * kRow + ((r0 + j * STEP) ^ (swz(k) << 5)) +
                                                      (g & 1) * 16 + (i & 3) * 4);
         u32x2 v[4];
         // (Loads and their wait in one block: before the builtin the compiler,
@@ -231,7 +237,7 @@ struct Stage {
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
         for (int j = 0; j < NF; ++j) {
-          const T* const at = lds + (h * 2 * E::KS + ks * E::KS + (lane >> 5) * 4) * kRow + r0 + j * 32 + (lane & 31);
+          const T* const at = lds + (h * 2 * E::KS + ks * E::KS + (lane >> 5) * 4) * kRow + r0 + j * STEP + (lane & 31);
           f[ks][j] = f32x4v{at[0], at[kRow], at[2 * kRow], at[3 * kRow]};
         }
     }
@@ -338,20 +344,25 @@ __device__ __forceinline__ void meet() {
 
 // ---- the small tile: 128 x 128, four waves, two workgroups a compute unit ----
 // Two stages of LDS; while one is multiplied, the other is filled.  One
-// workgroup's waits are the other's time.
+// workgroup's waits are the other's time.  A wave's four blocks of 32 x 32 are
+// neighbours in bf16, whose rows of 64 columns are whole cache lines; in
+// float32, where 32 columns are one and the matrix instructions are what costs,
+// every second one, so that an edge with half its columns or fewer keeps all
+// four waves at work (14352 x 2664 x 56: forward 78 -> 67 us, dw 96 -> 60).
 template <typename T, bool TA, bool TB>
 __global__ void __launch_bounds__(256, 2) linear_tile_kernel(const LinearParams p) {
   typedef Tile<T, TA, TB, 128, 128, 4> Tl;
   typedef Elem<T> E;
   __shared__ __align__(1024) T lds[2 * Tl::kStage];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+  constexpr int kStep = sizeof(T) == 2 ? 32 : 64;
+  const int wm = (wave >> 1) * (96 - kStep), wn = (wave & 1) * (96 - kStep);
   const Tl t(p, wave, lane);
   float bias[8];  // of the lane's columns in linear_out, here so that it has arrived by then
-  linear_bias(p, t.n0 + wn + (lane & 7) * 8, bias);
+  linear_bias(p, t.n0 + wn + linear_col<kStep>(lane & 7), bias);
   f32x16 acc[2][2];
   acc_zero(acc);
-  const int live_m = (p.M - t.m0 - wm + 31) / 32, live_n = (p.N - t.n0 - wn + 31) / 32;  // blocks with outputs
+  const int live_m = (p.M - t.m0 - wm + kStep - 1) / kStep, live_n = (p.N - t.n0 - wn + kStep - 1) / kStep;  // blocks with outputs
   if (t.kt0 < t.kt1) t.fetch(p, lds, t.kt0, wave);
   for (int kt = t.kt0; kt < t.kt1; ++kt) {
     wait_loads();  // of this stage, and the last one's fragments, before anyone refills its buffer
@@ -361,22 +372,22 @@ __global__ void __launch_bounds__(256, 2) linear_tile_kernel(const LinearParams 
     const T* const la = t.stage(lds, kt);
     const T* const lb = la + Tl::SA::kElems;
     typename E::Frag fa[2][2][2], fb[2][2][2];
-    Tl::SA::template frags<2>(la, wm, 0, lane, fa[0]);
-    Tl::SB::template frags<2>(lb, wn, 0, lane, fb[0]);
+    Tl::SA::template frags<2, kStep>(la, wm, 0, lane, fa[0]);
+    Tl::SB::template frags<2, kStep>(lb, wn, 0, lane, fb[0]);
     if constexpr (!TA && !TB) {
-      Tl::SA::template frags<2>(la, wm, 1, lane, fa[1]);
-      Tl::SB::template frags<2>(lb, wn, 1, lane, fb[1]);
+      Tl::SA::template frags<2, kStep>(la, wm, 1, lane, fa[1]);
+      Tl::SB::template frags<2, kStep>(lb, wn, 1, lane, fb[1]);
       mma_live<E>(fa[0], fb[0], acc, live_m, live_n);
     } else {
       mma_live<E>(fa[0], fb[0], acc, live_m, live_n);
-      Tl::SA::template frags<2>(la, wm, 1, lane, fa[1]);
-      Tl::SB::template frags<2>(lb, wn, 1, lane, fb[1]);
+      Tl::SA::template frags<2, kStep>(la, wm, 1, lane, fa[1]);
+      Tl::SB::template frags<2, kStep>(lb, wn, 1, lane, fb[1]);
     }
     mma_live<E>(fa[1], fb[1], acc, live_m, live_n);
   }
   __syncthreads();
   static_assert(4 * 32 * 68 * 4 <= (int)sizeof(lds), "the bands fit the stages");
-  linear_out<T>(p, acc, bias, reinterpret_cast<float*>(lds) + wave * 32 * 68, t.m0 + wm, t.n0 + wn, lane);
+  linear_out<T, kStep>(p, acc, bias, reinterpret_cast<float*>(lds) + wave * 32 * 68, t.m0 + wm, t.n0 + wn, lane);
 }
 
 // ---- the large tile: 256 x BN, eight waves, one workgroup a compute unit ----
@@ -407,7 +418,7 @@ __global__ void __launch_bounds__(512) linear_large_kernel(const LinearParams p)
   const int wm = (wave / WN) * TM, wn = (wave % WN) * TN;
   const Tl t(p, wave, lane);
   float bias[8];
-  linear_bias(p, t.n0 + wn + (lane % (TN / 8)) * 8, bias);
+  linear_bias(p, t.n0 + wn + linear_col<32>(lane % (TN / 8)), bias);
   f32x16 acc[FN][FM];
   acc_zero(acc);
   const bool late = wave >= 4;
@@ -443,7 +454,7 @@ __global__ void __launch_bounds__(512) linear_large_kernel(const LinearParams p)
   if (!late) meet();
   constexpr int kWave = 32 * (TN + 4);  // floats of a wave's band
   static_assert(8 * kWave * 4 <= (int)sizeof(lds), "the bands fit the stages");
-  linear_out<T>(p, acc, bias, reinterpret_cast<float*>(lds) + wave * kWave, t.m0 + wm, t.n0 + wn, lane);
+  linear_out<T, 32>(p, acc, bias, reinterpret_cast<float*>(lds) + wave * kWave, t.m0 + wm, t.n0 + wn, lane);
 }
 
 // Joins the shares of a split contraction, in order, and finishes the output.
@@ -468,37 +479,50 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinearParams p) 
 // ---- few rows ----
 // Up to 16·MT rows: bound by reading W once (and, at a decode step's sizes, by
 // the launch).  A workgroup takes 16 columns; its 8 waves share the contraction
-// in turn, each lane reading its fragment of W straight into registers, and
-// join their sums through LDS in order.
+// in turn, each lane reading its fragments of W and x straight into registers,
+// U turns at once so that they wait for memory together (past the contraction's
+// end a load gives zeros; with pointers and a branch around the load, as a first
+// form had it, 64 x 4096 x 4096 took 26.3 us against 20.2, in float32 49.4
+// against 37.7), and join their sums through LDS in order.
 template <typename T, int MT>
 __global__ void __launch_bounds__(512) linear_rows_kernel(const LinearParams p) {
-  constexpr int CH = Elem<T>::CH, KS = 4 * CH;  // contraction elements of a step (a chunk a lane)
+  constexpr int CH = Elem<T>::CH, KS = 4 * CH;  // contraction elements of a turn (a chunk a lane)
+  constexpr int U = 4;  // (8 turns: 64 x 4096 x 4096 20.2 us either way, 1 x 768 x 1536 2.95 -> 3.4)
   __shared__ float red[8][MT][256];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, kq = (lane >> 4) * CH;
   const int n0 = blockIdx.x * 16;
-  const T* const w = static_cast<const T*>(p.b) + (int64_t)min(n0 + i, p.N - 1) * p.ldb + kq;
-  const T* x[MT];
+  // (16 rows of W, or 64 of x, are at most 2^28 bytes)
+  const auto wr = make_rsrc(static_cast<const T*>(p.b) + (int64_t)n0 * p.ldb, 0x7fffffffu), xr = make_rsrc(p.a, 0x7fffffffu);
+  const uint32_t w = (uint32_t)((min(n0 + i, p.N - 1) - n0) * (int)p.ldb + kq) * (uint32_t)sizeof(T);
+  uint32_t x[MT];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) x[t] = static_cast<const T*>(p.a) + (int64_t)min(t * 16 + i, p.M - 1) * p.lda + kq;
+  for (int t = 0; t < MT; ++t) x[t] = (uint32_t)(min(t * 16 + i, p.M - 1) * (int)p.lda + kq) * (uint32_t)sizeof(T);
   f32x4v acc[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) acc[t] = f32x4v{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int k = wave * KS; k < p.K; k += 8 * KS) {
-    const bool in = k + kq < p.K;
-    const u32x4 zero = {0, 0, 0, 0};
-    const u32x4 wv = in ? *reinterpret_cast<const u32x4*>(w + k) : zero;
+  for (int k0 = wave * KS; k0 < p.K; k0 += U * 8 * KS) {
+    u32x4 wv[U], xv[U][MT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const u32x4 xv = in ? *reinterpret_cast<const u32x4*>(x[t] + k) : zero;
-      if constexpr (sizeof(T) == 2) {
-        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wv), __builtin_bit_cast(bf16x8, xv), acc[t], 0, 0, 0);
-      } else {
-        const f32x4v wf = __builtin_bit_cast(f32x4v, wv), xf = __builtin_bit_cast(f32x4v, xv);
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * 8 * KS;
+      const uint32_t at = k + kq < p.K ? (uint32_t)k * (uint32_t)sizeof(T) : kDrop;
+      wv[u] = __builtin_amdgcn_raw_buffer_load_b128(wr, (int)(w + at), 0, 0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[j], xf[j], acc[t], 0, 0, 0);
-      }
+      for (int t = 0; t < MT; ++t) xv[u][t] = __builtin_amdgcn_raw_buffer_load_b128(xr, (int)(x[t] + at), 0, 0);
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        if constexpr (sizeof(T) == 2) {
+          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wv[u]), __builtin_bit_cast(bf16x8, xv[u][t]), acc[t],
+                                                           0, 0, 0);
+        } else {
+          const f32x4v wf = __builtin_bit_cast(f32x4v, wv[u]), xf = __builtin_bit_cast(f32x4v, xv[u][t]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[j], xf[j], acc[t], 0, 0, 0);
+        }
+      }
   }
   // lane: output row lane%16, columns 4·(lane/16) onwards
 #pragma unroll

@@ -519,7 +519,8 @@ __global__ void __launch_bounds__(256) norm_rows_kernel(const NormRowParams p) {
       row_param<V>(p.w, c0 + c, 1.f, w);
       row_param<V>(p.bias, c0 + c, 0.f, b);
 #pragma unroll
-      for (int j = 0; j < V; ++j) f[i][j] = act_any(__builtin_fmaf(f[i][j] * rs, w[j], b[j]), p.act);
+      for (int j = 0; j < V; ++j) f[i][j] = __builtin_fmaf(f[i][j] * rs, w[j], b[j]);
+      act_all(f[i], p.act);
       row_store<T, V>(static_cast<T*>(p.out) + u * p.C + c, f[i]);
     }
   }
@@ -561,10 +562,16 @@ __global__ void __launch_bounds__(256) norm_rows_bwd_kernel(const NormRowParams 
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if ((i * p.lanes + li) * V < p.C) {
+        float d[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           xh[i][j] = (xh[i][j] - mu) * rs;
-          const float du = t[i][j] * act_d_any(__builtin_fmaf(xh[i][j], w[i][j], b[i][j]), p.act);
+          d[j] = __builtin_fmaf(xh[i][j], w[i][j], b[i][j]);
+        }
+        act_d_all(d, p.act);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float du = t[i][j] * d[j];
           ts[i][j] += du;
           tq[i][j] = __builtin_fmaf(du, xh[i][j], tq[i][j]);
           t[i][j] = du * w[i][j];
