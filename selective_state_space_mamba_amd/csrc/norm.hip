@@ -29,8 +29,9 @@ constexpr int64_t kNormBlocks = 1024;
 struct NormPlan {
   int nv, threads, slots, chunks, chunk_len, bwd_rows;
   size_t lds, pg, pc;  // bytes
-  int v, nvec, lanes;  // single tokens: vector width, vectors a lane, lanes a group (v = 0: not this way)
-  int64_t stride;      // and the backward's lane groups
+  int v, nvec, lanes;       // single tokens: vector width, vectors a lane, lanes a group (v = 0: not this way)
+  int bwd_nvec, bwd_lanes;  // the backward's (bwd_nvec = 0: not this way)
+  int64_t stride;           // and its lane groups
 };
 
 // Waves of the single-token backward, each with partial sums of its own that a
@@ -38,29 +39,52 @@ struct NormPlan {
 // 2048 / 4096 / 8192, with gelu 48.2 / 39.5 / 41.7.
 constexpr int64_t kNormRowWaves = 4096;
 
-// Single tokens: groups as rows in registers, up to 16 vectors of 8 values or
-// 4 of fewer (a group that is no multiple of 8 values starts at any of them).
+int64_t gcd(int64_t a, int64_t b) { return b ? gcd(b, a % b) : a; }
+
+// Single tokens: groups as rows in registers.  Forward: up to 16 vectors of 8
+// values a lane straight from memory, or 8 (of 4 values: 4) smaller ones through
+// LDS.  Backward, which keeps its weights and sums too: up to 4 vectors, or 8
+// single values through LDS.  A workgroup's rows in LDS, at least 8 of single
+// values, 4 of pairs or fours, are whole 16 bytes.
 void row_plan(const mamba_norm_dims* g, NormPlan* pl) {
-  pl->v = 0;
+  pl->v = pl->bwd_nvec = 0;
   if (g->seqlen != 1) return;
   const int C = (int)(g->dim / g->groups);
   const int v = C % 8 == 0 ? 8 : C % 4 == 0 ? 4 : C % 2 == 0 ? 2 : 1;
   const int vecs = C / v;
-  pl->lanes = pow2_at_least(vecs < 64 ? vecs : 64);
-  int nvec = pow2_at_least((vecs + pl->lanes - 1) / pl->lanes);
-  if (v < 8 && nvec > 1) nvec = 4;
-  if ((v == 8 && nvec > 16) || (v < 8 && vecs > 4 * pl->lanes)) return;
+  // the lanes of a row with `most` vectors each, and the vectors then
+  auto lanes_of = [&](int most) { return pow2_at_least(vecs > 64 * most ? 64 : (vecs + most - 1) / most); };
+  auto nvec_of = [&](int lanes, int least) {
+    const int n = pow2_at_least((vecs + lanes - 1) / lanes);
+    return n < least ? least : n;
+  };
+  const int most = v == 8 ? 1 : v == 4 ? 4 : 8;
+  pl->lanes = lanes_of(most);
+  pl->nvec = nvec_of(pl->lanes, v == 8 ? 1 : 4);
+  if (pl->nvec > (v == 8 ? 16 : most) || (v == 1 && pl->lanes > 32)) return;
   pl->v = v;
-  pl->nvec = nvec;
-  const int64_t rows = g->batch * g->groups;
-  int64_t s = kNormRowWaves * 64 / pl->lanes;
-  if (s > rows) s = rows;
-  s = (s + g->groups - 1) / g->groups * g->groups;
-  pl->stride = s;
-  if (nvec <= 4) {
-    pl->bwd_rows = (int)(s / g->groups);
-    pl->pc = up256((size_t)pl->bwd_rows * g->dim * sizeof(float2));
+  pl->bwd_lanes = v == 1 ? pl->lanes : lanes_of(1);
+  int nvec = v == 1 ? pl->nvec : nvec_of(pl->bwd_lanes, 1);
+  if (v > 1 && v < 8 && nvec > 1) nvec = nvec > 4 ? 0 : 4;
+  if (v == 8 && nvec > 4) nvec = 0;
+  pl->bwd_nvec = nvec;
+  if (nvec == 0) return;
+  // The backward's lane groups: a multiple of G, in LDS of whole workgroups
+  // too.  Single values: 4 rows each where that leaves a wave a SIMD, as the
+  // sums, 8 bytes a value, outweigh the rows otherwise (20000 tokens of 8 groups
+  // of 3: 48 us, 25 so).
+  const int64_t rows = g->batch * g->groups, per = 256 / pl->bwd_lanes;
+  int64_t s = kNormRowWaves * 64 / pl->bwd_lanes, unit = g->groups;
+  if (v == 1) {
+    const int64_t simds = 1024 * 64 / pl->bwd_lanes, few = rows / 4 > simds ? rows / 4 : simds;
+    if (s > few) s = few;
+    unit *= per / gcd(g->groups, per);
   }
+  if (s > rows) s = rows;
+  s = (s + unit - 1) / unit * unit;
+  pl->stride = s;
+  pl->bwd_rows = (int)(s / g->groups);
+  pl->pc = up256((size_t)pl->bwd_rows * g->dim * sizeof(float2));
 }
 
 // Validates the sizes and derives the launch plan; a pure function of dims.
@@ -118,32 +142,39 @@ void by_type_act(const mamba_norm_dims* g, F f) {
   else by_act((float*)nullptr);
 }
 
+// f(type, vector width, vectors a lane)
 template <typename F>
-void by_row_shape(const mamba_norm_dims* g, const NormPlan& pl, F f) {
+void by_row_shape(const mamba_norm_dims* g, int v, int nvec, F f) {
   auto by_v = [&](auto* t) {
-    auto c = [](auto i) { return i; };
-    using std::integral_constant;
-    auto small = [&](auto v) {
-      if (pl.nvec == 1) f(t, v, c(integral_constant<int, 1>{}));
-      else f(t, v, c(integral_constant<int, 4>{}));
+    auto by_nvec = [&](auto vc) {
+      switch (nvec) {
+        case 1: f(t, vc, std::integral_constant<int, 1>{}); break;
+        case 2: f(t, vc, std::integral_constant<int, 2>{}); break;
+        case 4: f(t, vc, std::integral_constant<int, 4>{}); break;
+        case 8: f(t, vc, std::integral_constant<int, 8>{}); break;
+        default: f(t, vc, std::integral_constant<int, 16>{});
+      }
     };
-    if (pl.v == 1) small(integral_constant<int, 1>{});
-    else if (pl.v == 2) small(integral_constant<int, 2>{});
-    else if (pl.v == 4) small(integral_constant<int, 4>{});
-    else if (pl.nvec == 1) f(t, integral_constant<int, 8>{}, integral_constant<int, 1>{});
-    else if (pl.nvec == 2) f(t, integral_constant<int, 8>{}, integral_constant<int, 2>{});
-    else if (pl.nvec == 4) f(t, integral_constant<int, 8>{}, integral_constant<int, 4>{});
-    else if (pl.nvec == 8) f(t, integral_constant<int, 8>{}, integral_constant<int, 8>{});
-    else f(t, integral_constant<int, 8>{}, integral_constant<int, 16>{});
+    switch (v) {
+      case 1: by_nvec(std::integral_constant<int, 1>{}); break;
+      case 2: by_nvec(std::integral_constant<int, 2>{}); break;
+      case 4: by_nvec(std::integral_constant<int, 4>{}); break;
+      default: by_nvec(std::integral_constant<int, 8>{});
+    }
   };
   if (g->dtype == MAMBA_DTYPE_BF16) by_v((uint16_t*)nullptr);
   else by_v((float*)nullptr);
+}
+// The shapes that row_plan gives.
+constexpr bool row_fwd(int v, int nvec) { return v == 8 || nvec == 4 || (v < 4 && nvec == 8); }
+constexpr bool row_bwd(int v, int nvec) {
+  return v == 8 ? nvec <= 4 : v == 1 ? nvec == 4 || nvec == 8 : nvec == 1 || nvec == 4;
 }
 
 NormRowParams row_params(const mamba_norm_dims* g, const NormPlan& pl) {
   NormRowParams r{};
   r.rows = g->batch * g->groups, r.stride = pl.stride;
-  r.C = (int)(g->dim / g->groups), r.G = (int)g->groups, r.lanes = pl.lanes, r.act = g->act, r.eps = g->eps;
+  r.C = (int)(g->dim / g->groups), r.G = (int)g->groups, r.act = g->act, r.eps = g->eps;
   return r;
 }
 
@@ -188,10 +219,13 @@ int mamba_group_norm_fwd(const void* x, const float* weight, const float* bias, 
   if (pl.v > 0) {
     NormRowParams r = row_params(dims, pl);
     r.x = x, r.w = weight, r.bias = bias, r.out = out, r.mean = mean, r.rstd = rstd;
-    by_row_shape(dims, pl, [&](auto* t, auto v, auto nv) {
+    r.lanes = pl.lanes;
+    by_row_shape(dims, pl.v, pl.nvec, [&](auto* t, auto v, auto nv) {
       using T = std::remove_pointer_t<decltype(t)>;
-      const int64_t per = 256 / pl.lanes;
-      norm_rows_kernel<T, decltype(v)::value, decltype(nv)::value><<<(unsigned)((r.rows + per - 1) / per), 256, 0, stream>>>(r);
+      constexpr int V = decltype(v)::value, NV = decltype(nv)::value;
+      const int64_t per = 256 / r.lanes;
+      const size_t lds = V == 8 ? 0 : per * r.C * sizeof(T);
+      if constexpr (row_fwd(V, NV)) norm_rows_kernel<T, V, NV><<<(unsigned)((r.rows + per - 1) / per), 256, lds, stream>>>(r);
     });
     return hipGetLastError() == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
   }
@@ -233,16 +267,17 @@ int mamba_group_norm_bwd(const void* x, const float* weight, const float* bias, 
   p.pc = reinterpret_cast<float2*>(static_cast<char*>(dims->workspace) + pl.pg);
   p.want_dw = dweight || dbias;
   bool ok = true;
-  if (pl.v > 0 && pl.nvec <= 4) {
+  if (pl.bwd_nvec > 0) {
     NormRowParams r = row_params(dims, pl);
     r.x = x, r.dout = dout, r.w = weight, r.bias = bias, r.out = dx, r.mean = p.mean, r.rstd = p.rstd;
     r.pc = p.pc, r.want_dw = p.want_dw;
-    by_row_shape(dims, pl, [&](auto* t, auto v, auto nv) {
+    r.lanes = pl.bwd_lanes;
+    by_row_shape(dims, pl.v, pl.bwd_nvec, [&](auto* t, auto v, auto nv) {
       using T = std::remove_pointer_t<decltype(t)>;
-      constexpr int NV = decltype(nv)::value;
-      const int64_t per = 256 / pl.lanes;
-      if constexpr (NV <= 4)
-        norm_rows_bwd_kernel<T, decltype(v)::value, NV><<<(unsigned)((pl.stride + per - 1) / per), 256, 0, stream>>>(r);
+      constexpr int V = decltype(v)::value, NV = decltype(nv)::value;
+      const int64_t per = 256 / r.lanes;
+      const size_t lds = V > 1 ? 0 : 2 * per * r.C * sizeof(T);
+      if constexpr (row_bwd(V, NV)) norm_rows_bwd_kernel<T, V, NV><<<(unsigned)((pl.stride + per - 1) / per), 256, lds, stream>>>(r);
     });
   } else by_type_act(dims, [&](auto* t, auto act) {
     using T = std::remove_pointer_t<decltype(t)>;

@@ -78,6 +78,16 @@ CASES = [
     (3, 1, 3000, 8, "f32", "silu"),
     (3, 1, 1000, 8, "bf16", "silu"),
     (9000, 1, 256, 4, "bf16", "none"),
+    # single tokens through LDS: odd groups and pairs and fours, short last workgroups, lane groups that
+    # begin anywhere among a token's groups and take many rows, one workgroup's lane group a wave
+    (3001, 1, 24, 8, "bf16", "relu"),
+    (2000, 1, 408, 8, "bf16", "gelu"),
+    (601, 1, 2040, 8, "f32", "silu"),
+    (999, 1, 240, 40, "bf16", "silu"),
+    (33, 1, 4008, 4, "bf16", "none"),
+    (33, 1, 1800, 2, "f32", "gelu"),
+    (20000, 1, 1224, 24, "bf16", "silu"),
+    (1, 1, 1096, 8, "f32", "none"),
 ]
 
 
