@@ -4,8 +4,9 @@ The compute path is libmamba_scan.so: hand-written HIP kernels behind the C
 ABI declared in include/mamba_scan.h.  This package holds its sources
 (csrc/), the in-tree build step (build.py), a ctypes binding that only
 marshals arguments (_binding.py for the scan, _glr.py for the gated recurrence,
-_norm.py for the group normalisation, _linear.py for the matrix product), and
-the seeded input generator used by the tests and the benchmark (inputs.py).
+_norm.py for the group normalisation, _linear.py for the matrix product, _call.py
+for what those three share), and the seeded input generator used by the tests and
+the benchmark (inputs.py).
 """
 from ._binding import (DIR_BIDIR, DIR_BWD, DIR_CROSS2D, DIR_FWD, DTYPE_BF16, DTYPE_F32, EXPORTED, LIB_PATH,
                        MambaDims, MambaError, ScanStepper, bwd_workspace_bytes, conv1d_silu, load_library, make_dims, num_dirs,
