@@ -399,10 +399,14 @@ __global__ void __launch_bounds__(256, 2) linear_tile_kernel(const LinearParams 
 // every half step; the late group waits at one more before the first and the
 // early group at one more after the last, so both meet the same number.
 //   - A stage's last reads are the late group's, one half step after the early
-//     group's; the early group refills that buffer in its next two reading half
-//     steps (an operand in each: together the loads' addresses would take longer
-//     than the other group's products; 65536 x 2048 x 2048: 522 us against 570),
-//     the late one at the start of the multiplying half step beside the first.
+//     group's.  From then on each group refills its part of that buffer: the
+//     early group one operand beside its next reads and one beside the products
+//     that follow, the late group one beside its last products of the stage and
+//     one beside its first of the next, so that no half step has the addresses
+//     of more loads than the other group's work covers (both operands in one:
+//     65536 x 2048 x 2048 570 us against 522; the early group's second and the
+//     late group's both a half step later: 8192 x 8192 x 8192 894 against 881,
+//     dx of 16384 x 768 x 1536 44.9 against 41.5).
 //   - Each wave has waited for its own loads of a stage before the barrier that
 //     lets the early group read it: the late group at the end of its last
 //     reading half step before, the early one at the end of its last
@@ -436,16 +440,14 @@ __global__ void __launch_bounds__(512) linear_large_kernel(const LinearParams p)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       typename E::Frag fa[2][FM], fb[2][FN];
-      if (!late && kt + 1 < t.kt1) {
-        if (h == 0) t.fetch_a(p, lds, kt + 1, wave);
-        else t.fetch_b(p, lds, kt + 1, wave);
-      }
+      if (h == 0 && !late && kt + 1 < t.kt1) t.fetch_a(p, lds, kt + 1, wave);
       Tl::SA::template frags<FM>(la, wm, h, lane, fa);
       Tl::SB::template frags<FN>(la + Tl::SA::kElems, wn, h, lane, fb);
       if (h == 1 && late) wait_loads();
       wait_lds();
       meet();
-      if (h == 1 && late && kt + 2 < t.kt1) t.fetch(p, lds, kt + 2, wave);
+      if (h == 0 && (!late || kt > t.kt0) && kt + 1 < t.kt1) t.fetch_b(p, lds, kt + 1, wave);
+      if (h == 1 && late && kt + 2 < t.kt1) t.fetch_a(p, lds, kt + 2, wave);
       mma_half<E>(fa, fb, acc);
       if (h == 1 && !late) wait_loads();
       meet();
