@@ -38,19 +38,19 @@ def launch_stream(x, stream) -> int:
 
 def check_like(x, shape, *named):
     """Each (name, tensor or None) has this shape, and x's type and device, and is contiguous."""
-    dtype, dev = x.dtype, x.device
+    dtype, dev = x.dtype, x.get_device()
     for name, t in named:
-        if t is not None and not (t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.device == dev):
-            _b._check(t, name, shape, dtype, dev)  # raises with the reason
+        if t is not None and not (t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == dev):
+            _b._check(t, name, shape, dtype, x.device)  # raises with the reason
 
 
 def check_f32(x, shape, *named):
     """The same for float32 tensors beside x."""
     import torch
-    f32, dev = torch.float32, x.device
+    f32, dev = torch.float32, x.get_device()
     for name, t in named:
-        if t is not None and not (t.shape == shape and t.dtype is f32 and t.is_contiguous() and t.device == dev):
-            _b._check(t, name, shape, f32, dev)
+        if t is not None and not (t.shape == shape and t.dtype is f32 and t.is_contiguous() and t.get_device() == dev):
+            _b._check(t, name, shape, f32, x.device)
 
 
 def ptr(t):

@@ -189,8 +189,7 @@ def glr_step(state, x_t, r_t, i_t=None, z_t=None, lam=None, *, scale=8.0, input_
     shape = x_t.shape
     check_like(x_t, shape, ("x_t", x_t), ("r_t", r_t), ("i_t", i_t), ("z_t", z_t), ("out", out))
     check_f32(x_t, shape, ("state", state))
-    if lam is not None:
-        check_f32(x_t, shape[1:], ("lam", lam))
+    check_f32(x_t, shape[1:], ("lam", lam))
     raw = launch_stream(x_t, stream)
     if out is None:
         out = torch.empty_like(x_t)

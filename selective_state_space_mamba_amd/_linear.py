@@ -82,7 +82,7 @@ def linear_fwd(x, weight, bias=None, residual=None, *, act=ACT_NONE, out=None, p
     dims = make_linear_dims(M, K, N, dt, act=act)
     workspace = use_workspace(dims, need, workspace, x)
     if out is None:
-        out = x.new_empty(shape)
+        out = x.new_empty(shape) if residual is None else torch.empty_like(residual)
     if pre is not None:
         check_f32(x, shape, ("pre", pre))
     elif want_pre:
