@@ -46,7 +46,7 @@ int glr_plan(const mamba_glr_dims* g, GlrPlan* pl) {
   pl->bwd_tiles = (int)bt;
   pl->fwd_chain = ft > 1 && rows < kFwdWalkRows;
   pl->bwd_chain = bt > 1 && rows < kBwdWalkRows;
-  auto words = [&](bool chain, int64_t tiles) { return chain ? 256 + up256((size_t)rows * tiles * kGlrCB * 24) : 0; };
+  auto words = [&](bool chain, int64_t tiles) { return chain ? 256 + up256((size_t)rows * tiles * kGlrCB * 16) : 0; };
   pl->fwd_words = words(pl->fwd_chain, ft);
   pl->bwd_words = words(pl->bwd_chain, bt);
   pl->part = up256((size_t)g->batch * (pl->bwd_chain ? bt : 1) * g->dim * 4);
@@ -63,7 +63,8 @@ void glr_params(const mamba_glr_dims* g, const GlrPlan& pl, GlrParams* p) {
   p->nblk = pl.nblk;
   p->reverse = g->reverse ? 1 : 0;
   p->scale = g->scale;
-  p->block = p->B * pl.nblk < 8 ? 16 : 4;
+  const int64_t rows = (int64_t)p->B * pl.nblk;
+  p->block = rows < 8 ? 16 : rows < 12 ? 8 : 4;
 }
 
 // Points p at the chain's words in the workspace and clears them.

@@ -39,10 +39,10 @@ constexpr int kGlrFwdTile = 128;           // positions of a workgroup, forward
 constexpr int kGlrBwdTile = 64;            // and backward: also the spacing of the saved states
 
 // Positions of a thread: what its inputs and their gates take in registers sets
-// the waves that fit.  Forward, 4 positions leave 4 waves a SIMD (8 x 2048 x
-// 1536 in bf16: 61 us, with 8 positions and 2 waves 64); backward, 4 in bf16
-// and 2 in float32, 3 waves (2 in bf16: 168 us against 133, the joins then
-// weigh twice as much).
+// the waves that fit.  Forward, 4 positions leave 4 or 5 waves a SIMD (8 x 2048
+// x 1536 in bf16: 61 us, with 8 positions and 2 waves 64); backward, 4 in bf16
+// leave 3 waves and 2 in float32 4 (2 in bf16: 168 us against 133, the joins
+// then weigh twice as much).
 template <typename T>
 struct GlrGeom {
   static constexpr int FP = 4, BP = sizeof(T) == 2 ? 4 : 2;
@@ -66,7 +66,7 @@ struct GlrParams {
   float* dlam_part;           // [B][tiles or 1][D] or null
   float* dinit;               // [B][D] or null
   // the chain (null: one workgroup walks the tiles of its rows)
-  uint64_t* words;            // 3 x [rows][tiles][64]
+  uint64_t* words;            // 2 x [rows][tiles][64]
   uint32_t* ticket;
   int block;  // tiles of a block
   int B, L, D, nblk, ntiles, reverse;
@@ -159,10 +159,10 @@ __device__ __forceinline__ float run_mul(float A, float B) {
 // ---- the chain ----
 // Tiles of one row (64 channels of one batch item) run in different
 // workgroups, at the same time.  A tile publishes its run (A, H) and, once it
-// knows the state that enters it, the state that leaves it.  Each value is one
-// 64-bit word {1 : value}, stored and loaded atomically at agent scope, so a
-// word that is there is whole and no fence (which would write back the L2) is
-// needed; the words start at zero.
+// knows the state that enters it, the state that leaves it: two 64-bit words,
+// {A with its sign bit set (A >= 0) : H} and {1 : state}, stored and loaded
+// atomically at agent scope, so a word that is there is whole and no fence
+// (which would write back the L2) is needed; the words start at zero.
 //
 // Waiting only for the tile before would make a sequence of as many waits as
 // tiles.  So the tiles form blocks: a block's last tile joins the
@@ -177,43 +177,42 @@ __device__ __forceinline__ float run_mul(float A, float B) {
 // ever waits for one that has already started, and every wait ends.
 // Longer blocks cost their last tile more and the others a longer way to their
 // state: they pay where few rows leave the waits as all there is.  us forward /
-// backward in bf16 with blocks of 4, 8 and 16: 1 x 26155 x 16 (one row) 37 / 67,
-// 23 / 42, 19 / 32 (waiting for the tile before alone: 56 / 138); 12 x 28897 x
-// 16 67 / 117, 66 / 120, 70 / 122; 1 x 262144 x 2048 (32 rows) 1261 / 2302,
-// 1307 / 2318, 1361 / 2348.
-constexpr int kGlrBatch = 3;  // runs fetched at a time: what the registers leave
+// backward in bf16 with blocks of 4, 8 and 16: 1 x 26155 x 16 (one row) 35 / 66,
+// 24 / 42, 19 / 32 (waiting for the tile before alone: 56 / 138); 1 x 200000 x
+// 640 (10 rows) 348 / 723, 342 / 637, 358 / 645; 12 x 28897 x 16 65 / 117, 66 /
+// 119, 68 / 122; 1 x 262144 x 2048 (32 rows) 1225 / 2234, 1296 / 2254, 1347 /
+// 2278 (of 2: 1248 / 2342).  So 16 below 8 rows, 8 below 12, else 4.
+constexpr int kGlrBatch = 3;  // runs fetched at a time (4 and 5: the longest sequence 1 % slower)
 
-__device__ __forceinline__ void word_put(uint64_t* p, float v) {
-  __hip_atomic_store(p, ((uint64_t)1 << 32) | __float_as_uint(v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ __forceinline__ void word_put(uint64_t* p, uint32_t tag, float v) {
+  __hip_atomic_store(p, ((uint64_t)tag << 32) | __float_as_uint(v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+__device__ __forceinline__ void run_put(uint64_t* p, float A, float H) { word_put(p, __float_as_uint(A) | 0x80000000u, H); }
 __device__ __forceinline__ uint64_t word_get(const uint64_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ bool word_there(uint64_t w) { return (uint32_t)(w >> 32) != 0; }
 __device__ __forceinline__ float word_val(uint64_t w) { return __uint_as_float((uint32_t)w); }
+__device__ __forceinline__ float word_decay(uint64_t w) { return __uint_as_float((uint32_t)(w >> 32) & 0x7fffffffu); }
 
 // Runs 0..n-1 of a block, kGlrBatch at a time once they are there: f(A, H) in order.
 template <typename F>
-__device__ __forceinline__ void chain_runs(const uint64_t* wa, const uint64_t* wh, int n, F f) {
+__device__ __forceinline__ void chain_runs(const uint64_t* runs, int n, F f) {
 #pragma unroll 1  // (unrolled it takes the registers of a wave)
   for (int k0 = 0; k0 < n; k0 += kGlrBatch) {
-    uint64_t a[kGlrBatch], h[kGlrBatch];
+    uint64_t w[kGlrBatch];
     for (;;) {
       bool ok = true;
 #pragma unroll
-      for (int k = 0; k < kGlrBatch; ++k) {
-        const int at = min(k0 + k, n - 1) * kGlrCB;
-        a[k] = word_get(wa + at);
-        h[k] = word_get(wh + at);
-      }
+      for (int k = 0; k < kGlrBatch; ++k) w[k] = word_get(runs + min(k0 + k, n - 1) * kGlrCB);
 #pragma unroll
-      for (int k = 0; k < kGlrBatch; ++k) ok = ok && word_there(a[k]) && word_there(h[k]);
+      for (int k = 0; k < kGlrBatch; ++k) ok = ok && word_there(w[k]);
       if (__all(ok)) break;
       __builtin_amdgcn_s_sleep(1);
     }
 #pragma unroll
     for (int k = 0; k < kGlrBatch; ++k)
-      if (k0 + k < n) f(word_val(a[k]), word_val(h[k]));
+      if (k0 + k < n) f(word_decay(w[k]), word_val(w[k]));
   }
 }
 
@@ -225,19 +224,17 @@ __device__ __forceinline__ float chain_carry(const GlrParams& p, int row, int st
   const int64_t stride = (int64_t)p.B * p.nblk * p.ntiles * kGlrCB;
   const int in = step % p.block;  // place in the block
   uint64_t* const inc = p.words + ((int64_t)row * p.ntiles + step) * kGlrCB + lane;
-  uint64_t* const wa = inc + stride;
-  uint64_t* const wh = wa + stride;
-  const uint64_t *const ba = wa - in * kGlrCB, *const bh = wh - in * kGlrCB;  // the block's runs
-  const uint64_t* const bi = inc - (in + 1) * kGlrCB;                         // the state that enters the block
+  uint64_t* const run = inc + stride;
+  const uint64_t* const runs = run - in * kGlrCB;      // the block's
+  const uint64_t* const bi = inc - (in + 1) * kGlrCB;  // the state that enters the block
   const bool ends = in == p.block - 1, from_start = step == in;
   if (step + 1 == p.ntiles) {
     // no one follows
   } else if (!ends) {
-    word_put(wa, A);
-    word_put(wh, H);
+    run_put(run, A, H);
   } else {  // the block's run, then its image
     float JA = 1.f, JH = 0.f;
-    chain_runs(ba, bh, in, [&](float a, float h) {
+    chain_runs(runs, in, [&](float a, float h) {
       JH = run_apply<RESET>(a, h, JH);
       JA = run_mul<RESET>(JA, a);
     });
@@ -249,7 +246,7 @@ __device__ __forceinline__ float chain_carry(const GlrParams& p, int row, int st
       while (!__all(word_there(w = word_get(bi)))) __builtin_amdgcn_s_sleep(1);
       v = word_val(w);
     }
-    word_put(inc, run_apply<RESET>(JA, JH, v));
+    word_put(inc, 1, run_apply<RESET>(JA, JH, v));
   }
   float v = first;
   if (step > 0) {
@@ -261,13 +258,13 @@ __device__ __forceinline__ float chain_carry(const GlrParams& p, int row, int st
       }
       if (__all(word_there(e))) {
         if (!from_start) v = word_val(e);
-        chain_runs(ba, bh, in, [&](float a, float h) { v = run_apply<RESET>(a, h, v); });
+        chain_runs(runs, in, [&](float a, float h) { v = run_apply<RESET>(a, h, v); });
         break;
       }
       __builtin_amdgcn_s_sleep(1);
     }
   }
-  if (!ends && step + 1 < p.ntiles) word_put(inc, run_apply<RESET>(A, H, v));
+  if (!ends && step + 1 < p.ntiles) word_put(inc, 1, run_apply<RESET>(A, H, v));
   return v;
 }
 
