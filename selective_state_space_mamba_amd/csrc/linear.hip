@@ -103,7 +103,7 @@ template <typename T, bool TA, bool TB>
 hipError_t product(LinearParams p, const ProductPlan& pl, hipStream_t stream) {
   p.tiles_m = pl.tiles_m, p.tiles_n = pl.tiles_n, p.splits = pl.splits, p.kt_per_split = pl.kt_per_split;
   if (pl.splits == 1) p.part = nullptr;
-  const dim3 grid((unsigned)((int64_t)pl.tiles_m * pl.tiles_n), (unsigned)pl.splits);
+  const unsigned grid = (unsigned)((int64_t)pl.tiles_m * pl.tiles_n * pl.splits);
   if constexpr (sizeof(T) == 2) {
     if (pl.tile == TILE_256x256) linear_large_kernel<T, TA, TB, 256, 2, 4><<<grid, 512, 0, stream>>>(p);
     else if (pl.tile == TILE_256x192) linear_large_kernel<T, TA, TB, 192, 4, 2><<<grid, 512, 0, stream>>>(p);

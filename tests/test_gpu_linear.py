@@ -67,6 +67,12 @@ CASES = [
     (1500, 768, 1544, "bf16", "silu", True, False),
     (5003, 520, 256, "bf16", "gelu", True, True),
     (2100, 264, 1048, "bf16", "relu", False, True),
+    # few rows whose contraction ends inside a turn; float32 tiles with half their columns or rows, or a quarter
+    (40, 2008, 48, "bf16", "relu", True, True),
+    (64, 1048, 72, "f32", "relu", True, True),
+    (300, 96, 56, "f32", "silu", True, True),
+    (333, 264, 152, "f32", "none", True, False),
+    (3000, 40, 24, "f32", "gelu", True, True),
     # enough tiles for the large ones, the last of them partly empty, in each of the three products
     (16300, 328, 1528, "bf16", "silu", True, True),
     (8200, 1000, 2056, "bf16", "none", True, True),
