@@ -59,8 +59,12 @@ __device__ __forceinline__ float lane_sum(float v, int width) {
 // (of two tensors of the same layout where NS = 2), U rows at a time: the next
 // rows' loads are issued before the current ones are used, and the first ones
 // by start(), before whatever else a kernel has to fetch.  Rows past the end
-// repeat the last one and are not used.
-template <typename T, int NS, int U>
+// repeat the last one and are not used.  BACK walks from the last row to the
+// first: a second pass then begins with what the first one has left in the L2
+// (us forward / backward in bf16, second passes from the front and from the
+// back: 32 x 4096 x 192 33.6 / 57.6, 30.7 / 57; 8 x 2048 x 1536 40.2 / 63.5,
+// 37.3 / 62.9; 64 x 4096 x 384 99 / 212, 97 / 186).
+template <typename T, int NS, int U, bool BACK = false>
 struct RowWalk {
   const T* src[NS];
   int64_t at, step;  // first row's vector, distance between a thread's rows (elements)
@@ -82,6 +86,10 @@ struct RowWalk {
     at = (int64_t)(l0 + slot) * p.D + col * 8;
     step = (int64_t)p.slots * p.D;
     n = slot < p.slots && l0 + slot < l1 ? (l1 - l0 - slot + p.slots - 1) / p.slots : 0;
+    if constexpr (BACK) {
+      at += (n - 1) * step;
+      step = -step;
+    }
     if (n > 0) fetch(cur, 0);
   }
   // f(vectors of one row, its element offset)
@@ -171,7 +179,7 @@ template <typename T, int ACT, typename F>
 __device__ __forceinline__ void rows_apply(const NormParams& p, const T* xb, T* ob, int l0, int l1, F stats) {
   if ((int)threadIdx.x / p.nv >= p.slots) return;
   const int col = threadIdx.x % p.nv;
-  RowWalk<T, 1, 4> rows;
+  RowWalk<T, 1, 4, true> rows;
   rows.start(p, xb, nullptr, l0, l1);
   float mu[8], sc[8], bi[8];
 #pragma unroll
@@ -342,7 +350,7 @@ template <typename T, int ACT, typename F>
 __device__ __forceinline__ void rows_dx(const NormParams& p, int b, const T* xb, const T* yb, T* ob, int l0, int l1, F sums) {
   if ((int)threadIdx.x / p.nv >= p.slots) return;
   const int col = threadIdx.x % p.nv;
-  RowWalk<T, 2, 2> rows;
+  RowWalk<T, 2, 2, true> rows;
   rows.start(p, xb, yb, l0, l1);
   NormCol k;
   k.load(p, b, col);
