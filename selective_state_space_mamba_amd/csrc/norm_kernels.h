@@ -60,10 +60,10 @@ __device__ __forceinline__ float lane_sum(float v, int width) {
 // rows' loads are issued before the current ones are used, and the first ones
 // by start(), before whatever else a kernel has to fetch.  Rows past the end
 // repeat the last one and are not used.  BACK walks from the last row to the
-// first: a second pass then begins with what the first one has left in the L2
-// (us forward / backward in bf16, second passes from the front and from the
-// back: 32 x 4096 x 192 33.6 / 57.6, 30.7 / 57; 8 x 2048 x 1536 40.2 / 63.5,
-// 37.3 / 62.9; 64 x 4096 x 384 99 / 212, 97 / 186).
+// first: a second pass then begins with what the first one has left in the
+// caches (bf16, second passes from the front and from the back: 64 x 4096 x 384,
+// whose 600 MB pass the last-level cache, backward 212 and 186 us; 32 x 4096 x
+// 192, whose do not, forward 33.0 and 32.3).
 template <typename T, int NS, int U, bool BACK = false>
 struct RowWalk {
   const T* src[NS];
