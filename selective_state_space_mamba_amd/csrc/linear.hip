@@ -89,6 +89,8 @@ GradPlan plan_grad(const mamba_linear_dims* g) {
   GradPlan pl;
   const int64_t cols = ceil_div(g->out_dim, 512);
   int64_t chunks = 2048 / cols;
+  // runs of 16 rows at least: up to 16 rows one, whose sums are dbias as they are
+  // (8 x 1536 x 768 20.1 -> 18.1 us; one run of 64 rows took 2 us longer than four and their join)
   if (chunks > ceil_div(g->rows, 16)) chunks = ceil_div(g->rows, 16);
   if (chunks < 1) chunks = 1;
   pl.chunk = ceil_div(g->rows, chunks);
@@ -200,10 +202,10 @@ int mamba_linear_bwd(const void* x, const void* weight, const float* pre, const 
   if (dbias || (acts && (dx || dweight))) {
     LinearGradParams g{};
     g.dout = dout, g.pre = acts ? pre : nullptr, g.dp = acts ? ws : nullptr;
-    g.part = dbias ? reinterpret_cast<float*>(ws + gp.dp) : nullptr;
+    g.part = !dbias ? nullptr : gp.chunks == 1 ? dbias : reinterpret_cast<float*>(ws + gp.dp);
     g.M = (int)dims->rows, g.N = (int)dims->out_dim, g.chunk = gp.chunk;
     e = bf16 ? grad<uint16_t>(g, dims->act, (unsigned)gp.chunks, stream) : grad<float>(g, dims->act, (unsigned)gp.chunks, stream);
-    if (e == hipSuccess && dbias) {
+    if (e == hipSuccess && dbias && gp.chunks > 1) {
       colsum_kernel<float><<<(unsigned)((g.N + 15) / 16), 1024, 0, stream>>>(g.part, gp.chunks, g.N, ColStore{dbias, nullptr});
       e = hipGetLastError();
     }
