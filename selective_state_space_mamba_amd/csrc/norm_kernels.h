@@ -12,10 +12,15 @@
 // the rows are done and joined to groups through LDS.  A workgroup takes one
 // run of rows with all D channels.
 //
-// Statistics.  Sums of x and x² about the run's first row (a value of the
-// channel itself, so that an offset of the channel costs no bits), turned into
-// mean and sum of squared deviations M per channel; sets are joined by
-//   mean = Σ n_i·mean_i / n,  M = Σ (M_i + n_i·(mean_i - mean)²).
+// Statistics.  Mean and sum of squared deviations M, never a difference of
+// large sums: a thread takes four rows at a time about their own mean and joins
+// them to its rows before; the threads of a channel, the channels of a group and
+// the runs of an item are joined likewise.  Two sets a and b, and any number:
+//   mean = mean_a + δ·n_b/n,  M = M_a + M_b + δ²·n_a·n_b/n,  δ = mean_b - mean_a
+//   mean = Σ n_i·mean_i / n,  M = Σ (M_i + n_i·(mean_i - mean)²)
+// Within a run, values and means are taken from the run's first row, so that an
+// offset that all rows have in common costs no bits.  (Sums of x and x² about the run's first row, as
+// a first form had them, left rstd 1e-3 off where that row was far from the others.)
 //
 // What bounds it: bytes.  An item that one workgroup can take is read twice by
 // the same workgroup, the second time from the caches close by; a larger one
@@ -24,6 +29,8 @@
 
 #include "act_math.h"
 #include "colsum.h"
+
+#include <type_traits>
 
 namespace mscan {
 
@@ -92,6 +99,16 @@ struct RowWalk {
     }
     if (n > 0) fetch(cur, 0);
   }
+  // f(U vectors, how many of them are rows), one tensor
+  template <typename F>
+  __device__ __forceinline__ void walk_blocks(F f) {
+    for (int r = 0; r < n; r += U) {
+      if (r + U < n) fetch(nxt, r + U);
+      f(cur[0], min(U, n - r));
+#pragma unroll
+      for (int u = 0; u < U; ++u) cur[0][u] = nxt[0][u];
+    }
+  }
   // f(vectors of one row, its element offset)
   template <typename F>
   __device__ __forceinline__ void walk(F f) {
@@ -114,41 +131,96 @@ struct RowWalk {
 
 // ---- pieces of a workgroup's work; red: 2·slots·D floats of LDS ----
 
+// Joins set b of n_b values to set a of n_a: w = n_b/(n_a + n_b), naw = n_a·w.
+__device__ __forceinline__ void stats_join(float& ma, float& Ma, float mb, float Mb, float w, float naw) {
+  const float d = mb - ma;
+  ma = __builtin_fmaf(d, w, ma);
+  Ma += __builtin_fmaf(d * d, naw, Mb);
+}
+
 // Per-channel mean and M of rows [l0, l1) of item b, left in red[0..D) and red[slots·D..slots·D + D).
 template <typename T>
 __device__ __forceinline__ void rows_stats(const NormParams& p, const T* xb, int l0, int l1, float* red) {
+  constexpr int U = 4;
   const int tid = threadIdx.x, slot = tid / p.nv, col = tid % p.nv;
   const int D = p.D, n = p.slots * D;
-  const bool on = slot < p.slots;
-  float s[8], q[8], sh[8];
-  if (on) {
-    RowWalk<T, 1, 4> rows;
+  float* const at = red + slot * D + col * 8;
+  float mu[8], M[8];
+  if (slot < p.slots) {
+    RowWalk<T, 1, U> rows;
     rows.start(p, xb, nullptr, l0, l1);
-    Vec<T, 8> v;
-    v.load(xb + (int64_t)l0 * D + col * 8);
+    Vec<T, 8> ref;  // the run's first row: means are kept from it
+    ref.load(xb + (int64_t)l0 * D + col * 8);
+    float done = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sh[j] = v.get(j), s[j] = 0.f, q[j] = 0.f;
-    rows.walk([&](const Vec<T, 8>& r, int64_t) {
+    for (int j = 0; j < 8; ++j) mu[j] = M[j] = 0.f;
+    auto block = [&](const Vec<T, 8>(&r)[U], auto whole, int m) {
+      constexpr bool kWhole = decltype(whole)::value;
+      const float cnt = kWhole ? (float)U : (float)m, inv = kWhole ? 1.0f / U : 1.0f / cnt;
+      const float w = cnt * rcp(done + cnt), naw = done * w;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float d = r.get(j) - sh[j];
-        s[j] += d;
-        q[j] = __builtin_fmaf(d, d, q[j]);
+        float d[U], s = 0.f, q = 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          d[u] = r[u].get(j) - ref.get(j);
+          s += kWhole || u < m ? d[u] : 0.f;
+        }
+        s *= inv;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          d[u] = kWhole || u < m ? d[u] - s : 0.f;
+          q = __builtin_fmaf(d[u], d[u], q);
+        }
+        stats_join(mu[j], M[j], s, q, w, naw);
       }
+      done += cnt;
+    };
+    rows.walk_blocks([&](const Vec<T, 8>(&r)[U], int m) {
+      if (m == U) block(r, std::true_type{}, m);
+      else block(r, std::false_type{}, m);
     });
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      red[slot * D + col * 8 + j] = s[j];
-      red[n + slot * D + col * 8 + j] = q[j];
-    }
+    for (int j = 0; j < 8; ++j) at[j] = mu[j], at[n + j] = M[j];
   }
   __syncthreads();
-  const float cnt = (float)(l1 - l0), inv = 1.0f / cnt;
+  // The slots of a channel: with few channels `parts` threads join every parts-th slot each, into the first of
+  // them; then one joins what there is.  (In pairs, a barrier a level: 32 x 4096 x 192 35.6 us forward against 33.3.)
+  const int least = (l1 - l0) / p.slots, more = (l1 - l0) % p.slots;  // rows of every slot; slots with one more
+  auto join = [&](int c, int s0, int s1, int step, auto rows) {
+    float cnt = 0.f, m = 0.f, q = 0.f;
+#pragma unroll 8
+    for (int s = s0; s < s1; s += step) {
+      const float k = rows(s);
+      cnt += k;
+      m = __builtin_fmaf(k, red[s * D + c], m);
+    }
+    m *= rcp(__builtin_fmaxf(cnt, 1.f));
+#pragma unroll 8
+    for (int s = s0; s < s1; s += step) {
+      const float d = red[s * D + c] - m;
+      q += __builtin_fmaf(rows(s) * d, d, red[n + s * D + c]);
+    }
+    red[s0 * D + c] = m;
+    red[n + s0 * D + c] = q;
+  };
+  auto one = [&](int s) { return (float)(least + (s < more)); };
+  int lg = 0;
+  while ((D << (lg + 1)) <= (int)blockDim.x) ++lg;
+  const int parts = 1 << lg;
+  if (lg > 0) {
+    const int s = tid / D;
+    if (s < parts) join(tid % D, s, p.slots, parts, one);
+    __syncthreads();
+  }
   for (int c = tid; c < D; c += blockDim.x) {
-    float S = 0.f, Q = 0.f;
-    for (int k = 0; k < p.slots; ++k) S += red[k * D + c], Q += red[n + k * D + c];
-    red[c] = to_f32(xb[(int64_t)l0 * D + c]) + S * inv;
-    red[n + c] = __builtin_fmaxf(Q - S * S * inv, 0.f);
+    if (lg > 0)
+      join(c, 0, parts, 1, [&](int s) {
+        return (float)(least * ((p.slots - s + parts - 1) >> lg) + (s < more ? (more - s + parts - 1) >> lg : 0));
+      });
+    else if (p.slots > 1)
+      join(c, 0, p.slots, 1, one);
+    red[c] += to_f32(xb[(int64_t)l0 * D + c]);
   }
   __syncthreads();
 }
