@@ -143,17 +143,19 @@ __device__ __forceinline__ float glr_beta(float base) {
 
 // ---- runs ----
 
-// h -> A·h + H.  With resets, A = 0 marks a run that holds one: nothing that
-// came before it may reach through, not even an infinity or a NaN.
+// h -> A·h + H.  With resets, A = kCut marks a run that holds one: nothing that
+// came before it may reach through, not even an infinity or a NaN.  (A decay is
+// at most 1, and one that has vanished is no cut: 0 passes a NaN on.)
+constexpr float kCut = 2.0f;
 template <bool RESET>
 __device__ __forceinline__ float run_apply(float A, float H, float h) {
   const float v = __builtin_fmaf(A, h, H);
-  return RESET ? (A == 0.f ? H : v) : v;
+  return RESET ? (A == kCut ? H : v) : v;
 }
 template <bool RESET>
 __device__ __forceinline__ float run_mul(float A, float B) {
   const float v = A * B;
-  return RESET ? ((A == 0.f || B == 0.f) ? 0.f : v) : v;
+  return RESET ? ((A == kCut || B == kCut) ? kCut : v) : v;
 }
 
 // ---- the chain ----
@@ -389,12 +391,12 @@ __global__ void __launch_bounds__(64 * GlrGeom<T>::FW) glr_fwd_kernel(const GlrP
     }
 #pragma unroll
     for (int c = 0; c < V; ++c) {
-      if constexpr (RESET) a[0][c] = rst[0] ? 0.f : a[0][c];
+      if constexpr (RESET) a[0][c] = rst[0] ? kCut : a[0][c];
       A[c] = a[0][c];
       H[c] = h[0][c];
 #pragma unroll
       for (int k = 1; k < P; ++k) {
-        if constexpr (RESET) a[k][c] = rst[k] ? 0.f : a[k][c];
+        if constexpr (RESET) a[k][c] = rst[k] ? kCut : a[k][c];
         H[c] = run_apply<RESET>(a[k][c], h[k][c], H[c]);
         A[c] = run_mul<RESET>(A[c], a[k][c]);
       }
@@ -594,7 +596,7 @@ __global__ void __launch_bounds__(64 * GlrGeom<T>::BW, 3) glr_bwd_kernel(const G
 #pragma unroll
       for (int k = 0; k < P; ++k) {
         // (a stays what it is where a sequence starts: the input factor's derivative takes it)
-        const float v = w[k][c] * x[k].get(c), ak = RESET && rst[k] ? 0.f : a[k][c];
+        const float v = w[k][c] * x[k].get(c), ak = RESET && rst[k] ? kCut : a[k][c];
         H[c] = k == 0 ? v : run_apply<RESET>(ak, v, H[c]);
         A[c] = k == 0 ? ak : run_mul<RESET>(A[c], ak);
       }

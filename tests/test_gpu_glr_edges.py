@@ -1,0 +1,70 @@
+"""GPU: what the gated recurrence does where decays vanish, where a value is NaN
+and where a sequence spans several blocks of tiles, with the float64 form."""
+import numpy as np
+import pytest
+
+import selective_state_space_mamba_amd as ms
+
+from layerutil import from_dev, glr_grads, glr_ref, rounded, to_dev
+from scanutil import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch().cuda.is_available():
+        pytest.skip("no GPU")
+    ms.load_library()
+    yield
+
+
+def bits(t_):
+    """NaNs compare equal."""
+    t = torch()
+    return t.nan_to_num(t_.float(), nan=12345.0, posinf=1e38, neginf=-1e38)
+
+
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("with_lam", [False, True])
+@pytest.mark.parametrize("shape", [(1, 700, 64), (3, 1500, 40), (40, 200, 1664)], ids=lambda s: "%dx%dx%d" % s)
+def test_a_vanishing_decay_is_no_reset(shape, with_lam, reverse):
+    """Decays of 0, and products of decays that underflow, still pass a NaN on: 0·NaN.  Only a reset stops one, and
+    with a mask that holds none the results are those without a mask."""
+    B, L, D = shape
+    print("[gpu case] glr vanishing decays", shape, with_lam, reverse, flush=True)
+    r = np.random.Generator(np.random.PCG64([L, D]))
+    v = {k: r.standard_normal((B, L, D)).astype(np.float32) for k in "xiz"}
+    v["r"] = r.choice(np.float32([30.0, 2.0, -1.0] if with_lam else [-200.0, -20.0, -3.0]), (B, L, D))
+    lam = np.full(D, 30.0, np.float32) if with_lam else None
+    dout = r.standard_normal((B, L, D)).astype(np.float32)
+    bad = L // 7 if not reverse else L - 1 - L // 7  # a quarter into the scan, and near its end for the adjoint
+    far = L - 1 - bad
+    v["x"][:, bad, ::2] = np.nan
+    dout[:, far, ::3] = np.nan
+    a = [to_dev(v[k]) for k in "xriz"] + [to_dev(lam)]
+    kw = dict(reverse=reverse)
+    plain = ms.glr_fwd(*a, **kw)
+    grads = ms.glr_bwd(*a, dout=to_dev(dout), **kw)
+    none = to_dev(np.zeros((B, L), np.uint8))
+    masked = ms.glr_fwd(*a, reset=none, **kw)
+    mgrads = ms.glr_bwd(*a, dout=to_dev(dout), reset=none, **kw)
+    for x, y in zip(plain, masked):
+        assert torch().equal(bits(x), bits(y))
+    for k in grads:
+        assert grads[k] is None or torch().equal(bits(grads[k]), bits(mgrads[k])), k
+    for reset in (None, np.zeros((B, L), np.uint8)):
+        if reset is not None:
+            reset[:, L // 2] = 1
+        rd = None if reset is None else to_dev(reset)
+        out, last = ms.glr_fwd(*a, reset=rd, **kw)
+        g = ms.glr_bwd(*a, dout=to_dev(dout), reset=rd, **kw)
+        with np.errstate(all="ignore"):
+            ref = [v[k].astype(np.float64) for k in "xriz"] + [None if lam is None else lam.astype(np.float64)]
+            want, want_last, _, _ = glr_ref(*ref, reverse=reverse, reset=reset)
+            wg = glr_grads(*ref, dout.astype(np.float64), reverse=reverse, reset=reset)
+        assert np.array_equal(np.isnan(from_dev(out)), np.isnan(want))
+        assert np.array_equal(np.isnan(from_dev(last)), np.isnan(want_last))
+        for k, w in wg.items():
+            if w is not None:
+                assert np.array_equal(np.isnan(from_dev(g[k])), np.isnan(w)), k
