@@ -90,10 +90,10 @@ __device__ __forceinline__ void sigm2(float v, float& q, float& omq) {
 // decays close to 1 come from: ln(1 + e) by its series while e < 1/32
 // (remainder below e^5/6 = 5e-9 of it).
 __device__ __forceinline__ float softplus_rel(float v) {
-  const float e = ex2(__builtin_fminf(v, 60.f) * kLog2e);
+  const float e = ex2((v > 60.f ? 60.f : v) * kLog2e);  // (a select, as a minimum or maximum drops a NaN)
   const float series =
       e * __builtin_fmaf(e, __builtin_fmaf(e, __builtin_fmaf(e, __builtin_fmaf(e, 0.2f, -0.25f), 1.0f / 3.0f), -0.5f), 1.0f);
-  const float direct = __builtin_fmaxf(v, kLn2 * lg2(1.0f + e));
+  const float ln = kLn2 * lg2(1.0f + e), direct = v > ln ? v : ln;
   return e < 0.03125f ? series : direct;
 }
 

@@ -68,3 +68,34 @@ def test_a_vanishing_decay_is_no_reset(shape, with_lam, reverse):
         for k, w in wg.items():
             if w is not None:
                 assert np.array_equal(np.isnan(from_dev(g[k])), np.isnan(w)), k
+
+
+@pytest.mark.parametrize("rule", [ms.GLR_SQRT, ms.GLR_LERP, ms.GLR_UNIT])
+def test_nan_in_lam_shows_in_its_channel(rule):
+    """And in no other.  (The unit rule's first state does not depend on lam.)"""
+    t = torch()
+    B, L, D = 2, 300, 72
+    g = t.Generator(device="cuda:0")
+    g.manual_seed(3)
+    x, r, z, dout = (t.randn(B, L, D, generator=g, device="cuda:0") for _ in range(4))
+    lam = t.full((D,), -4.0, device="cuda:0")
+    bad = lam.clone()
+    bad[[5, 70]] = float("nan")
+    keep = [d for d in range(D) if d not in (5, 70)]
+    init = t.randn(B, D, generator=g, device="cuda:0")
+    print("[gpu case] glr NaN in lam", rule, flush=True)
+    want = ms.glr_fwd(x, r, None, z, lam, input_rule=rule, initial_state=init)
+    got = ms.glr_fwd(x, r, None, z, bad, input_rule=rule, initial_state=init)
+    wg = ms.glr_bwd(x, r, None, z, lam, dout=dout, input_rule=rule, initial_state=init)
+    gg = ms.glr_bwd(x, r, None, z, bad, dout=dout, input_rule=rule, initial_state=init)
+    ws, gs = init.clone(), init.clone()
+    wo = ms.glr_step(ws, x[:, 0].contiguous(), r[:, 0].contiguous(), None, z[:, 0].contiguous(), lam, input_rule=rule)
+    go = ms.glr_step(gs, x[:, 0].contiguous(), r[:, 0].contiguous(), None, z[:, 0].contiguous(), bad, input_rule=rule)
+    pairs = [(want[0], got[0]), (want[1], got[1]), (ws, gs), (wo, go)]
+    pairs += [(wg[k], gg[k]) for k in ("dr", "dz", "dlam", "dinit")]
+    for w, v in pairs:
+        assert t.equal(v[..., keep], w[..., keep])
+        assert bool(t.isnan(v[..., [5, 70]]).all())
+    # dx needs the later adjoints alone: NaN but at the last token
+    assert t.equal(gg["dx"][..., keep], wg["dx"][..., keep])
+    assert bool(t.isnan(gg["dx"][:, :-1][..., [5, 70]]).all())
