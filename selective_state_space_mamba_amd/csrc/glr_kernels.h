@@ -86,15 +86,26 @@ __device__ __forceinline__ void sigm2(float v, float& q, float& omq) {
   omq = v >= 0.f ? small : big;
 }
 
-// softplus to full relative accuracy for very negative arguments too, where
-// decays close to 1 come from: ln(1 + e) by its series while e < 1/32
-// (remainder below e^5/6 = 5e-9 of it).
+// softplus(v) = max(v, 0) + ln(1 + e), e = e^{-|v|}, to full relative accuracy
+// (3e-7) for very negative arguments too, where decays close to 1 come from:
+// ln(1 + e) = 2·atanh(s) = 2s·(1 + s²/3 + s⁴/5 + ...) with s = e/(2 + e) <= 1/3
+// never takes the sum 1 + e (terms up to s¹²/13: remainder below 4e-8), and the
+// exponent's rounding is made up for to first order.  (The bound on |v| is a
+// select, as a minimum would drop a NaN.)
 __device__ __forceinline__ float softplus_rel(float v) {
-  const float e = ex2((v > 60.f ? 60.f : v) * kLog2e);  // (a select, as a minimum or maximum drops a NaN)
-  const float series =
-      e * __builtin_fmaf(e, __builtin_fmaf(e, __builtin_fmaf(e, __builtin_fmaf(e, 0.2f, -0.25f), 1.0f / 3.0f), -0.5f), 1.0f);
-  const float ln = kLn2 * lg2(1.0f + e), direct = v > ln ? v : ln;
-  return e < 0.03125f ? series : direct;
+  constexpr float kLog2eLow = 1.92596303e-8f;  // log2 e less its float32
+  const float m = __builtin_fabsf(v) > 200.f ? -200.f : -__builtin_fabsf(v), t = m * kLog2e;
+  const float low = __builtin_fmaf(m, kLog2eLow, __builtin_fmaf(m, kLog2e, -t));
+  float e = ex2(t);
+  e = __builtin_fmaf(e, low * kLn2, e);
+  const float s = e * rcp(2.0f + e), z = s * s;
+  float p = __builtin_fmaf(z, 1.0f / 13.0f, 1.0f / 11.0f);
+  p = __builtin_fmaf(z, p, 1.0f / 9.0f);
+  p = __builtin_fmaf(z, p, 1.0f / 7.0f);
+  p = __builtin_fmaf(z, p, 1.0f / 5.0f);
+  p = __builtin_fmaf(z, p, 1.0f / 3.0f);
+  const float l = __builtin_fmaf(2.0f * s, p * z, 2.0f * s);
+  return (v > 0.f ? v : 0.f) + l;
 }
 
 // 1 - e^{-y} for y >= 0, given its direct value 1 - e^{-y}: below y = 1/4 the

@@ -99,3 +99,24 @@ def test_nan_in_lam_shows_in_its_channel(rule):
     # dx needs the later adjoints alone: NaN but at the last token
     assert t.equal(gg["dx"][..., keep], wg["dx"][..., keep])
     assert bool(t.isnan(gg["dx"][:, :-1][..., [5, 70]]).all())
+
+
+def test_softplus_keeps_its_relative_accuracy():
+    """One token behind a fully open gate (r = 30: sigmoid rounds to 1) with x = 1 and a small scale shows the rate:
+    out = 1 - exp(-scale·softplus(lam)) = scale·softplus(lam) to its second order.  An exponential and a reciprocal of
+    one ulp each, a quotient's series and the products around them are about ten roundings of 2^-24: 6e-7, from
+    lam = -80 (softplus = 2e-35) to 80, where a sum 1 + e or a rounded exponent would lose up to all of them."""
+    t = torch()
+    D, scale = 8192, 2.0 ** -10
+    lam = np.linspace(-80.0, 80.0, D).astype(np.float32)
+    lam[: D // 2] = np.linspace(-6.0, 2.0, D // 2).astype(np.float32)  # densely where the terms are of one size
+    x, r = t.ones(1, 1, D, device="cuda:0"), t.full((1, 1, D), 30.0, device="cuda:0")
+    print("[gpu case] glr softplus", flush=True)
+    want = -np.expm1(-scale * np.logaddexp(0.0, lam.astype(np.float64)))
+    big = want > 1e-30  # (below, float32 holds fewer bits)
+    step = ms.glr_step(t.zeros(1, D, device="cuda:0"), x[0], r[0], lam=to_dev(lam), scale=scale, input_rule=ms.GLR_LERP)
+    out, _ = ms.glr_fwd(x, r, lam=to_dev(lam), scale=scale, input_rule=ms.GLR_LERP)
+    for got in (from_dev(out)[0, 0], from_dev(step)[0]):
+        rel = np.abs(got - want)[big] / want[big]
+        print("worst %.2e at lam %.2f" % (rel.max(), lam[big][rel.argmax()]), flush=True)
+        assert rel.max() <= 6e-7
