@@ -170,7 +170,8 @@ def glr_bwd(x, r, i=None, z=None, lam=None, *, dout, dlast=None, scale=8.0, inpu
 
 @functools.lru_cache(maxsize=512)
 def _step_dims(Bsz, Dm, dt, input_rule, scale):
-    """The dims of a step hold no pointers and are only read: one for all calls of these sizes."""
+    """The dims of a step hold no pointers and are only read: one for all calls of these sizes.  (Plain numbers as
+    arguments: a tensor would be looked up by its identity, whatever it holds by then.)"""
     d = make_glr_dims(Bsz, 1, Dm, dt, input_rule=input_rule, scale=scale)
     return d, ctypes.byref(d)
 
@@ -194,6 +195,6 @@ def glr_step(state, x_t, r_t, i_t=None, z_t=None, lam=None, *, scale=8.0, input_
     if out is None:
         out = torch.empty_like(x_t)
     done(_b.load_library().mamba_glr_step(state.data_ptr(), x_t.data_ptr(), r_t.data_ptr(), ptr(i_t), ptr(z_t),
-                                          ptr(lam), _step_dims(shape[0], shape[1], dt, input_rule, scale)[1],
+                                          ptr(lam), _step_dims(shape[0], shape[1], dt, int(input_rule), float(scale))[1],
                                           out.data_ptr(), raw), "mamba_glr_step")
     return out

@@ -78,6 +78,7 @@ def linear_fwd(x, weight, bias=None, residual=None, *, act=ACT_NONE, out=None, p
     if bias is not None:
         check_f32(x, (N,), ("bias", bias))
     check_like(x, shape, ("residual", residual), ("out", out))
+    act = int(act)  # (a tensor would be looked up below by its identity)
     need, _ = _sizes(M, K, N, dt, act)
     dims = make_linear_dims(M, K, N, dt, act=act)
     workspace = use_workspace(dims, need, workspace, x)
@@ -108,6 +109,7 @@ def linear_bwd(x, weight, *, dout, pre=None, act=ACT_NONE, want_dx=True, want_dw
     check_like(x, shape, ("dout", dout))
     if pre is not None:
         check_f32(x, shape, ("pre", pre))
+    act = int(act)
     _, need = _sizes(M, K, N, dt, act)
     dims = make_linear_dims(M, K, N, dt, act=act)
     workspace = use_workspace(dims, need, workspace, x)

@@ -120,3 +120,26 @@ def test_softplus_keeps_its_relative_accuracy():
         rel = np.abs(got - want)[big] / want[big]
         print("worst %.2e at lam %.2f" % (rel.max(), lam[big][rel.argmax()]), flush=True)
         assert rel.max() <= 6e-7
+
+
+def test_scalars_are_read_on_every_call():
+    """A scale or a rule given as a tensor counts with the value it has at the call."""
+    t = torch()
+    g = t.Generator(device="cuda:0")
+    g.manual_seed(4)
+    x, r = (t.randn(2, 64, generator=g, device="cuda:0") for _ in range(2))
+    lam = t.zeros(64, device="cuda:0")
+    scale, rule, act = t.tensor(8.0), t.tensor(ms.GLR_SQRT), t.tensor(ms.ACT_NONE)
+    for s, k in ((8.0, ms.GLR_SQRT), (2.0, ms.GLR_SQRT), (2.0, ms.GLR_UNIT)):
+        scale.fill_(s), rule.fill_(k)
+        want = ms.glr_step(t.ones(2, 64, device="cuda:0"), x, r, lam=lam, scale=s, input_rule=k)
+        for sc in (scale, scale.numpy()):
+            got = ms.glr_step(t.ones(2, 64, device="cuda:0"), x, r, lam=lam, scale=sc, input_rule=rule)
+            assert t.equal(got, want), (s, k)
+    w = t.randn(64, 64, generator=g, device="cuda:0")
+    for a in (ms.ACT_NONE, ms.ACT_SILU):  # an activation's backward needs a larger workspace
+        act.fill_(a)
+        _, pre = ms.linear_fwd(x, w, act=act, want_pre=True)
+        got = ms.linear_bwd(x, w, dout=r, pre=pre, act=act)
+        want = ms.linear_bwd(x, w, dout=r, pre=pre, act=a)
+        assert all(t.equal(got[n], want[n]) for n in got)
