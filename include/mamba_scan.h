@@ -332,8 +332,9 @@ MAMBA_API size_t mamba_glr_saved_bytes(const mamba_glr_dims* dims);
  * the scan, [B][ceil(L/64)][D] float32, for mamba_glr_bwd.  out must not alias
  * an input.  Errors: MAMBA_ERR_INVALID (NULL x, r or out, a size <= 0, an
  * unknown dtype or rule, a negative or infinite scale), MAMBA_ERR_UNSUPPORTED
- * (D not a multiple of 4, a pointer other than reset not 16-byte aligned,
- * sizes beyond 32-bit tile counts), MAMBA_ERR_WORKSPACE (workspace or saved too
+ * (D not a multiple of 4, a pointer other than reset not 16-byte aligned (with
+ * bfloat16 and D = 8k + 4, where a slice of a batch begins on 8 bytes: 8 for x,
+ * r, i, z, out and their gradients), sizes beyond 32-bit tile counts), MAMBA_ERR_WORKSPACE (workspace or saved too
  * small), MAMBA_ERR_HIP.
  */
 MAMBA_API int mamba_glr_fwd(const void* x, const void* r, const void* i, const void* z, const float* lam,

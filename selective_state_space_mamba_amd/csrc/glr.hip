@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "../../include/mamba_scan.h"
 #include "glr_launch.h"
 
@@ -12,6 +14,15 @@ using namespace mscan;
 namespace {
 
 bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+bool aligned(std::initializer_list<const void*> ps, uintptr_t n) {
+  for (const void* p : ps)
+    if (!aligned(p, n)) return false;
+  return true;
+}
+// Of x, r, i, z, out and their gradients.  A thread's four channels are one
+// access of 8 (bf16) or 16 bytes, and a slice of a batch begins where a token
+// does: on 8 bytes only, in bf16 with D = 8k + 4.
+uintptr_t elem_align(const mamba_glr_dims* g) { return g->dtype == MAMBA_DTYPE_BF16 && g->dim % 8 != 0 ? 8 : 16; }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 // From this many rows of 64 channels on, one workgroup walks the tiles of a row
@@ -116,9 +127,9 @@ int mamba_glr_fwd(const void* x, const void* r, const void* i, const void* z, co
   GlrPlan pl;
   const int rc = glr_plan(dims, &pl);
   if (rc != MAMBA_OK) return rc;
-  for (const void* q : {x, r, i, z, (const void*)lam, (const void*)dims->initial_state, (const void*)out, (const void*)last_state,
-                        (const void*)saved, (const void*)dims->workspace})
-    if (!aligned(q, 16)) return MAMBA_ERR_UNSUPPORTED;
+  if (!aligned({x, r, i, z, out}, elem_align(dims)) ||
+      !aligned({lam, dims->initial_state, last_state, saved, dims->workspace}, 16))
+    return MAMBA_ERR_UNSUPPORTED;
   if (saved && saved_bytes < pl.saved) return MAMBA_ERR_WORKSPACE;
   if (pl.fwd_words > 0 && (!dims->workspace || dims->workspace_bytes < pl.fwd_words)) return MAMBA_ERR_WORKSPACE;
   GlrParams p{};
@@ -137,10 +148,9 @@ int mamba_glr_bwd(const void* x, const void* r, const void* i, const void* z, co
   GlrPlan pl;
   const int rc = glr_plan(dims, &pl);
   if (rc != MAMBA_OK) return rc;
-  for (const void* q : {x, r, i, z, (const void*)lam, dout, (const void*)dlast, (const void*)dims->initial_state, (const void*)dx,
-                        (const void*)dr, (const void*)di, (const void*)dz, (const void*)dlam, (const void*)dinit,
-                        (const void*)saved, (const void*)dims->workspace})
-    if (!aligned(q, 16)) return MAMBA_ERR_UNSUPPORTED;
+  if (!aligned({x, r, i, z, dout, dx, dr, di, dz}, elem_align(dims)) ||
+      !aligned({lam, dlast, dims->initial_state, dlam, dinit, saved, dims->workspace}, 16))
+    return MAMBA_ERR_UNSUPPORTED;
   if (saved && saved_bytes < pl.saved) return MAMBA_ERR_WORKSPACE;
   if (!dims->workspace || dims->workspace_bytes < mamba_glr_bwd_workspace_bytes(dims)) return MAMBA_ERR_WORKSPACE;
   char* const ws = static_cast<char*>(dims->workspace);
@@ -185,8 +195,7 @@ int mamba_glr_step(float* state, const void* x_t, const void* r_t, const void* i
   GlrPlan pl;
   const int rc = glr_plan(&one, &pl);
   if (rc != MAMBA_OK) return rc;
-  for (const void* q : {(const void*)state, x_t, r_t, i_t, z_t, (const void*)lam, (const void*)out})
-    if (!aligned(q, 16)) return MAMBA_ERR_UNSUPPORTED;
+  if (!aligned({x_t, r_t, i_t, z_t, out}, elem_align(&one)) || !aligned({state, lam}, 16)) return MAMBA_ERR_UNSUPPORTED;
   const int64_t n = one.batch * one.dim, blocks = (n / kGlrV + 255) / 256;
   if (blocks > INT32_MAX) return MAMBA_ERR_UNSUPPORTED;
   auto go = [&](auto* t, auto rule, auto with_lam) {

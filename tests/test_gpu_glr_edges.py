@@ -143,3 +143,30 @@ def test_scalars_are_read_on_every_call():
         got = ms.linear_bwd(x, w, dout=r, pre=pre, act=act)
         want = ms.linear_bwd(x, w, dout=r, pre=pre, act=a)
         assert all(t.equal(got[n], want[n]) for n in got)
+
+
+@pytest.mark.parametrize("reverse", [False, True])
+def test_slices_of_a_batch(reverse):
+    """bfloat16 items of an odd number of tokens and D = 8k + 4 channels begin 8 bytes apart from 16; every one of them
+    is a contiguous tensor and gives what the item by itself gives."""
+    t = torch()
+    B, L, D = 3, 333, 76
+    g = t.Generator(device="cuda:0")
+    g.manual_seed(6)
+    v = {k: t.randn(B, L, D, generator=g, device="cuda:0").bfloat16() for k in ("x", "r", "i", "z", "dout")}
+    lam = t.full((D,), -3.0, device="cuda:0")
+    init = t.randn(1, D, generator=g, device="cuda:0")
+    print("[gpu case] glr slices", flush=True)
+    for b in range(B):
+        got = []
+        for take in (lambda a: a, lambda a: a.clone()):
+            s = {k: take(a[b:b + 1]) for k, a in v.items()}
+            assert s["x"].is_contiguous()
+            args = (s["x"], s["r"], s["i"], s["z"], lam)
+            out = take(t.empty(B, L, D, dtype=t.bfloat16, device="cuda:0")[b:b + 1])
+            _, last, saved = ms.glr_fwd_save(*args, initial_state=init, reverse=reverse, out=out)
+            grads = ms.glr_bwd(*args, dout=s["dout"], saved=saved, initial_state=init, reverse=reverse)
+            state = init.clone()
+            step = ms.glr_step(state, *(take(v[k][b, 7:8]) for k in "xriz"), lam, out=take(v["dout"][b, 7:8].clone()))
+            got.append([out, last, step, state] + [grads[k] for k in sorted(grads)])
+        assert all(t.equal(p, q) for p, q in zip(*got))
