@@ -25,7 +25,7 @@ GLR = os.path.join(CSRC, "glr_inst.hip")
 HOSTS = [HOST, GLR_HOST, os.path.join(CSRC, "norm.hip"), os.path.join(CSRC, "linear.hip")]
 SOURCES = HOSTS + [INST, ROWS, GLR]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("scan_launch.h", "scan_kernels.h", "scan_row.h", "scan_bwd.h", "conv_kernels.h",
-                                                  "device_math.h", "glr_kernels.h", "glr_launch.h", "act_math.h", "colsum.h", "norm_kernels.h", "linear_kernels.h")] + [
+                                                  "device_math.h", "glr_kernels.h", "glr_launch.h", "act_math.h", "colsum.h", "wide_grid.h", "norm_kernels.h", "linear_kernels.h")] + [
     os.path.join(ROOT, "include", "mamba_scan.h")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # (bf16, exact) flags of the four instantiation units

@@ -196,12 +196,12 @@ int mamba_glr_step(float* state, const void* x_t, const void* r_t, const void* i
   const int rc = glr_plan(&one, &pl);
   if (rc != MAMBA_OK) return rc;
   if (!aligned({x_t, r_t, i_t, z_t, out}, elem_align(&one)) || !aligned({state, lam}, 16)) return MAMBA_ERR_UNSUPPORTED;
-  const int64_t n = one.batch * one.dim, blocks = (n / kGlrV + 255) / 256;
-  if (blocks > INT32_MAX) return MAMBA_ERR_UNSUPPORTED;
+  const int64_t n = one.batch * one.dim;
+  const dim3 blocks = wide_grid((n / kGlrV + 255) / 256);
   auto go = [&](auto* t, auto rule, auto with_lam) {
     using T = std::remove_pointer_t<decltype(t)>;
     glr_step_kernel<T, decltype(rule)::value, decltype(with_lam)::value>
-        <<<(unsigned)blocks, 256, 0, stream>>>(state, x_t, r_t, i_t, z_t, lam, out, one.scale, n, (int)one.dim);
+        <<<blocks, 256, 0, stream>>>(state, x_t, r_t, i_t, z_t, lam, out, one.scale, n, (int)one.dim);
   };
   auto by_lam = [&](auto* t, auto rule) { lam ? go(t, rule, std::true_type{}) : go(t, rule, std::false_type{}); };
   auto by_rule = [&](auto* t) {

@@ -15,7 +15,7 @@ namespace {
 
 template <int RULE, bool LAM, bool CHAIN>
 void go(const GlrParams& p, bool bwd, hipStream_t stream) {
-  const unsigned grid = (unsigned)(p.B * p.nblk) * (CHAIN ? (unsigned)p.ntiles : 1u);
+  const dim3 grid = wide_grid((int64_t)p.B * p.nblk * (CHAIN ? p.ntiles : 1));
   if (bwd) glr_bwd_kernel<InstT, RULE, LAM, kReset, CHAIN><<<grid, 64 * GlrGeom<InstT>::BW, 0, stream>>>(p);
   else glr_fwd_kernel<InstT, RULE, LAM, kReset, CHAIN><<<grid, 64 * GlrGeom<InstT>::FW, 0, stream>>>(p);
 }

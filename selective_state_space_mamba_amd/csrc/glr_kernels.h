@@ -26,6 +26,7 @@
 
 #include "colsum.h"
 #include "device_math.h"
+#include "wide_grid.h"
 
 namespace mscan {
 
@@ -284,20 +285,23 @@ __device__ __forceinline__ float chain_carry(const GlrParams& p, int row, int st
 // ---- forward ----
 
 // The tile a workgroup takes: its row of 64 channels and its place(s) along the scan.
+// False: a workgroup too many (the whole workgroup's answer, before any other barrier).
 template <bool CHAIN>
-__device__ __forceinline__ void glr_tile(const GlrParams& p, uint32_t* sTicket, int& row, int& step, int& step_end) {
+__device__ __forceinline__ bool glr_tile(const GlrParams& p, uint32_t* sTicket, int& row, int& step, int& step_end) {
+  const uint32_t rows = (uint32_t)(p.B * p.nblk);
   if constexpr (CHAIN) {
     if (threadIdx.x == 0) *sTicket = __hip_atomic_fetch_add(p.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
     const uint32_t t = __builtin_amdgcn_readfirstlane(*sTicket);
-    const uint32_t rows = (uint32_t)(p.B * p.nblk);
     step = (int)(t / rows);
     row = (int)(t % rows);
     step_end = step + 1;
+    return step < p.ntiles;
   } else {
-    row = blockIdx.x;
+    row = (int)wide_block();
     step = 0;
     step_end = p.ntiles;
+    return row < (int)rows;
   }
 }
 
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(64 * GlrGeom<T>::FW) glr_fwd_kernel(const GlrP
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int seg = lane / kGlrLanes, cl = lane % kGlrLanes;
   int row, tile, tile_end;
-  glr_tile<CHAIN>(p, &sTicket, row, tile, tile_end);
+  if (!glr_tile<CHAIN>(p, &sTicket, row, tile, tile_end)) return;
   const int b = row / p.nblk, dblk = (row % p.nblk) * kGlrCB;
   const bool dok = dblk + cl * V < p.D;
   const int d0 = dok ? dblk + cl * V : 0;  // lanes past the last channel repeat the first four and store nothing
@@ -512,7 +516,7 @@ __global__ void __launch_bounds__(64 * GlrGeom<T>::BW, 3) glr_bwd_kernel(const G
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int seg = lane / kGlrLanes, cl = lane % kGlrLanes;
   int row, step, step_end;  // step 0 is the last tile of the scan
-  glr_tile<CHAIN>(p, &sTicket, row, step, step_end);
+  if (!glr_tile<CHAIN>(p, &sTicket, row, step, step_end)) return;
   const int b = row / p.nblk, dblk = (row % p.nblk) * kGlrCB;
   const bool dok = dblk + cl * V < p.D;
   const int d0 = dok ? dblk + cl * V : 0;
@@ -798,7 +802,7 @@ template <typename T, int RULE, bool LAM>
 __global__ void __launch_bounds__(256) glr_step_kernel(float* state, const void* x, const void* r, const void* i, const void* z,
                                                        const float* lam, void* out, float scale, int64_t n, int D) {
   constexpr int V = kGlrV;
-  const int64_t e = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * V;
+  const int64_t e = (wide_block() * blockDim.x + threadIdx.x) * V;
   if (e >= n) return;
   const int d = (int)(e % D);
   Vec<T, V> xv, rv, iv, zv;

@@ -225,7 +225,7 @@ int mamba_group_norm_fwd(const void* x, const float* weight, const float* bias, 
       constexpr int V = decltype(v)::value, NV = decltype(nv)::value;
       const int64_t per = 256 / r.lanes;
       const size_t lds = V == 8 ? 0 : per * r.C * sizeof(T);
-      if constexpr (row_fwd(V, NV)) norm_rows_kernel<T, V, NV><<<(unsigned)((r.rows + per - 1) / per), 256, lds, stream>>>(r);
+      if constexpr (row_fwd(V, NV)) norm_rows_kernel<T, V, NV><<<wide_grid((r.rows + per - 1) / per), 256, lds, stream>>>(r);
     });
     return hipGetLastError() == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
   }
@@ -236,7 +236,7 @@ int mamba_group_norm_fwd(const void* x, const float* weight, const float* bias, 
     constexpr int A = decltype(act)::value;
     if (p.chunks == 1) {
       ok = lds_ok(norm_item_kernel<T, A>, pl.lds);
-      if (ok) norm_item_kernel<T, A><<<grid, pl.threads, pl.lds, stream>>>(p);
+      if (ok) norm_item_kernel<T, A><<<wide_grid(p.B), pl.threads, pl.lds, stream>>>(p);
     } else {
       ok = lds_ok(norm_stats_kernel<T>, pl.lds);
       if (ok) norm_stats_kernel<T><<<grid, pl.threads, pl.lds, stream>>>(p);

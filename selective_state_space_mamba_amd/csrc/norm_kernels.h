@@ -29,6 +29,7 @@
 
 #include "act_math.h"
 #include "colsum.h"
+#include "wide_grid.h"
 
 #include <type_traits>
 
@@ -278,7 +279,8 @@ __global__ void __launch_bounds__(kNormMaxThreads) norm_item_kernel(const NormPa
   extern __shared__ float lds[];
   float* const sMean = lds + 2 * p.slots * p.D;
   float* const sRstd = sMean + p.G;
-  const int b = blockIdx.x;
+  const int64_t b = wide_block();
+  if (b >= p.B) return;
   const T* const xb = static_cast<const T*>(p.x) + (int64_t)b * p.L * p.D;
   rows_stats<T>(p, xb, 0, p.L, lds);
   const float inv = 1.0f / ((float)p.L * (float)p.C);
@@ -628,7 +630,8 @@ __device__ __forceinline__ void row_norm(const NormRowParams& p, int64_t u, bool
 template <typename T, int V, int NV>
 __global__ void __launch_bounds__(256) norm_rows_kernel(const NormRowParams p) {
   const int li = threadIdx.x & (p.lanes - 1), per = 256 / p.lanes, k = threadIdx.x / p.lanes;
-  const int64_t r0 = (int64_t)blockIdx.x * per, u = r0 + k;
+  const int64_t r0 = wide_block() * per, u = r0 + k;
+  if (r0 >= p.rows) return;
   const T* const x = static_cast<const T*>(p.x) + r0 * p.C;
   T* const y = static_cast<T*>(p.out) + r0 * p.C;
   if constexpr (V == 8) {
