@@ -429,6 +429,13 @@ typedef struct {
 MAMBA_API size_t mamba_linear_fwd_workspace_bytes(const mamba_linear_dims* dims);
 MAMBA_API size_t mamba_linear_bwd_workspace_bytes(const mamba_linear_dims* dims);
 
+/* How a product is run, for tests and for reading profiles: the output tile of
+ * a workgroup (rows of few-row products: 16, 32 or 64) and the shares of its
+ * contraction, for product 0 (forward), 1 (dx) or 2 (dweight).  A pure function
+ * of the sizes.  Errors: MAMBA_ERR_INVALID, MAMBA_ERR_UNSUPPORTED as below. */
+MAMBA_API int mamba_linear_plan(const mamba_linear_dims* dims, int product, int32_t* tile_rows, int32_t* tile_cols,
+                                int32_t* shares);
+
 /*
  * Forward.  x [M][K], weight [N][K], out [M][N] dtype; bias [N] float32 or
  * NULL; residual [M][N] dtype or NULL, which may be out itself; pre [M][N]

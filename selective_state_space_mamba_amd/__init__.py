@@ -14,7 +14,7 @@ from ._binding import (DIR_BIDIR, DIR_BWD, DIR_CROSS2D, DIR_FWD, DTYPE_BF16, DTY
 from ._glr import (GLR_LERP, GLR_SQRT, GLR_UNIT, GlrDims, glr_bwd, glr_bwd_workspace_bytes, glr_fwd, glr_fwd_save,
                    glr_fwd_workspace_bytes, glr_saved_bytes, glr_step, make_glr_dims)
 from ._linear import (LinearDims, linear_bwd, linear_bwd_workspace_bytes, linear_fwd, linear_fwd_workspace_bytes,
-                      make_linear_dims)
+                      linear_plan, make_linear_dims)
 from ._norm import (ACT_GELU, ACT_NONE, ACT_RELU, ACT_SILU, NormDims, group_norm_bwd, group_norm_bwd_workspace_bytes,
                     group_norm_fwd, group_norm_fwd_workspace_bytes, make_norm_dims)
 
@@ -25,4 +25,4 @@ __all__ = ["DIR_BIDIR", "DIR_BWD", "DIR_CROSS2D", "DIR_FWD", "DTYPE_BF16", "DTYP
            "glr_fwd_workspace_bytes", "glr_saved_bytes", "glr_step", "make_glr_dims",
            "ACT_GELU", "ACT_NONE", "ACT_RELU", "ACT_SILU", "NormDims", "group_norm_bwd", "group_norm_bwd_workspace_bytes",
            "group_norm_fwd", "group_norm_fwd_workspace_bytes", "make_norm_dims",
-           "LinearDims", "linear_bwd", "linear_bwd_workspace_bytes", "linear_fwd", "linear_fwd_workspace_bytes", "make_linear_dims"]
+           "LinearDims", "linear_bwd", "linear_bwd_workspace_bytes", "linear_fwd", "linear_fwd_workspace_bytes", "linear_plan", "make_linear_dims"]

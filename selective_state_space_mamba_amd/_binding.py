@@ -22,7 +22,7 @@ EXPORTED = ("mamba_conv1d_silu", "mamba_glr_bwd", "mamba_glr_bwd_workspace_bytes
             "mamba_glr_fwd_workspace_bytes", "mamba_glr_saved_bytes", "mamba_glr_step",
             "mamba_group_norm_bwd", "mamba_group_norm_bwd_workspace_bytes", "mamba_group_norm_fwd",
             "mamba_group_norm_fwd_workspace_bytes", "mamba_linear_bwd", "mamba_linear_bwd_workspace_bytes",
-            "mamba_linear_fwd", "mamba_linear_fwd_workspace_bytes", "mamba_scan_bwd", "mamba_scan_bwd_workspace_bytes", "mamba_scan_fwd_workspace_bytes",
+            "mamba_linear_fwd", "mamba_linear_fwd_workspace_bytes", "mamba_linear_plan", "mamba_scan_bwd", "mamba_scan_bwd_workspace_bytes", "mamba_scan_fwd_workspace_bytes",
             "mamba_scan_fwd", "mamba_scan_fwd_noalloc", "mamba_scan_fwd_save", "mamba_scan_saved_bytes",
             "mamba_scan_step",
             "mamba_status_string")

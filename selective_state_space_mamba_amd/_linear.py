@@ -24,6 +24,8 @@ def declare(lib):
     for name in ("fwd_workspace_bytes", "bwd_workspace_bytes"):
         fn = getattr(lib, "mamba_linear_" + name)
         fn.restype, fn.argtypes = ctypes.c_size_t, [dims]
+    lib.mamba_linear_plan.restype = ctypes.c_int
+    lib.mamba_linear_plan.argtypes = [dims, ctypes.c_int] + [ctypes.POINTER(ctypes.c_int32)] * 3
     lib.mamba_linear_fwd.restype = ctypes.c_int
     lib.mamba_linear_fwd.argtypes = [vp] * 4 + [dims] + [vp] * 3
     lib.mamba_linear_bwd.restype = ctypes.c_int
@@ -41,6 +43,14 @@ def linear_fwd_workspace_bytes(dims: LinearDims) -> int:
 
 def linear_bwd_workspace_bytes(dims: LinearDims) -> int:
     return query("mamba_linear_bwd_workspace_bytes", dims)
+
+
+def linear_plan(dims: LinearDims, product: int):
+    """mamba_linear_plan: (tile rows, tile columns, shares of the contraction) of product 0 (forward), 1 (dx) or 2 (dweight)."""
+    out = [ctypes.c_int32() for _ in range(3)]
+    done(_b.load_library().mamba_linear_plan(ctypes.byref(dims), int(product), *(ctypes.byref(v) for v in out)),
+         "mamba_linear_plan")
+    return tuple(v.value for v in out)
 
 
 @functools.lru_cache(maxsize=512)

@@ -19,6 +19,7 @@ constexpr int kRowsMax = 64;  // rows that linear_rows_kernel takes
 
 // How one product of the three is run.
 enum { TILE_128 = 0, TILE_256x192 = 1, TILE_256x256 = 2 };
+int few_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }  // of linear_rows_kernel
 struct ProductPlan {
   int tile, tiles_m, tiles_n, splits, kt_per_split;
   size_t part;  // bytes
@@ -125,9 +126,11 @@ hipError_t forward(LinearParams p, const ProductPlan& pl, hipStream_t stream) {
   if (p.M <= kRowsMax) {
     const unsigned grid = (unsigned)ceil_div(p.N, 16);
     p.part = nullptr;
-    if (p.M <= 16) linear_rows_kernel<T, 1><<<grid, 512, 0, stream>>>(p);
-    else if (p.M <= 32) linear_rows_kernel<T, 2><<<grid, 512, 0, stream>>>(p);
-    else linear_rows_kernel<T, 4><<<grid, 512, 0, stream>>>(p);
+    switch (few_rows(p.M)) {
+      case 16: linear_rows_kernel<T, 1><<<grid, 512, 0, stream>>>(p); break;
+      case 32: linear_rows_kernel<T, 2><<<grid, 512, 0, stream>>>(p); break;
+      default: linear_rows_kernel<T, 4><<<grid, 512, 0, stream>>>(p);
+    }
     return hipGetLastError();
   }
   return product<T, false, false>(p, pl, stream);
@@ -162,6 +165,23 @@ size_t mamba_linear_bwd_workspace_bytes(const mamba_linear_dims* dims) {
   const size_t a = plan_product(dims->rows, dims->in_dim, dims->out_dim, bf16).part;
   const size_t b = plan_product(dims->out_dim, dims->in_dim, dims->rows, bf16).part;
   return gp.dp + gp.part + (a > b ? a : b);
+}
+
+int mamba_linear_plan(const mamba_linear_dims* dims, int product, int32_t* tile_rows, int32_t* tile_cols, int32_t* shares) {
+  if (!tile_rows || !tile_cols || !shares || product < 0 || product > 2) return MAMBA_ERR_INVALID;
+  const int rc = check(dims);
+  if (rc != MAMBA_OK) return rc;
+  if (product == 0 && dims->rows <= kRowsMax) {
+    *tile_rows = few_rows(dims->rows), *tile_cols = 16, *shares = 1;
+    return MAMBA_OK;
+  }
+  const int64_t m = product == 2 ? dims->out_dim : dims->rows, n = product == 0 ? dims->out_dim : dims->in_dim;
+  const int64_t k = product == 0 ? dims->in_dim : product == 1 ? dims->out_dim : dims->rows;
+  const ProductPlan pl = plan_product(m, n, k, dims->dtype == MAMBA_DTYPE_BF16);
+  *tile_rows = pl.tile == TILE_128 ? 128 : 256;
+  *tile_cols = pl.tile == TILE_128 ? 128 : pl.tile == TILE_256x192 ? 192 : 256;
+  *shares = pl.splits;
+  return MAMBA_OK;
 }
 
 int mamba_linear_fwd(const void* x, const void* weight, const float* bias, const void* residual, const mamba_linear_dims* dims,

@@ -38,3 +38,30 @@ def test_glr_alignment_of_batch_slices(lib):
         assert call(64, ms.DTYPE_BF16, 8) == E.MAMBA_ERR_UNSUPPORTED
         assert call(68, ms.DTYPE_F32, 8) == E.MAMBA_ERR_UNSUPPORTED
         assert call(68, ms.DTYPE_F32, 16) == E.MAMBA_ERR_WORKSPACE
+
+
+def test_linear_tiles_are_all_run(lib):
+    """The sizes that test_gpu_linear_tiles runs reach each tile in each operand layout, whole and in shares."""
+    from linear_tiles import CASES, sizes
+    seen = set()
+    for product, m, n, k, tile, shared in CASES:
+        M, K, N = sizes(product, m, n, k)
+        rows, cols, shares = ms.linear_plan(ms.make_linear_dims(M, K, N, ms.DTYPE_BF16), product)
+        assert ((rows, cols), shares > 1) == (tile, shared), (product, m, n, k, rows, cols, shares)
+        seen.add((product, tile, shared))
+    assert len(seen) == 3 * 3 * 2
+
+
+def test_linear_plan(lib):
+    def plan(M, K, N, product=0, **kw):
+        return ms.linear_plan(ms.make_linear_dims(M, K, N, kw.pop("dtype", ms.DTYPE_BF16), **kw), product)
+
+    assert [plan(M, 64, 64)[:2] for M in (1, 16, 17, 32, 33, 64, 65)] == [
+        (16, 16), (16, 16), (32, 16), (32, 16), (64, 16), (64, 16), (128, 128)]
+    assert plan(16384, 768, 1536, dtype=ms.DTYPE_F32) == (128, 128, 1)
+    for bad in (dict(product=3), dict(product=-1), dict(act=9)):
+        with pytest.raises(ms.MambaError):
+            plan(8, 64, 64, **bad)
+    with pytest.raises(ms.MambaError):
+        plan(8, 60, 64)
+    assert lib.mamba_linear_plan(None, 0, None, None, None) == E.MAMBA_ERR_INVALID
