@@ -5,7 +5,7 @@ import pytest
 
 import selective_state_space_mamba_amd as ms
 
-from layerutil import from_dev, glr_grads, glr_ref, rounded, to_dev
+from layerutil import from_dev, glr_grads, glr_ref, to_dev
 from scanutil import torch
 
 pytestmark = pytest.mark.gpu
@@ -170,3 +170,82 @@ def test_slices_of_a_batch(reverse):
             step = ms.glr_step(state, *(take(v[k][b, 7:8]) for k in "xriz"), lam, out=take(v["dout"][b, 7:8].clone()))
             got.append([out, last, step, state] + [grads[k] for k in sorted(grads)])
         assert all(t.equal(p, q) for p, q in zip(*got))
+
+
+# Sequences of several blocks of tiles, forward (128 positions a tile) and backward (64), for each length of a block:
+# 16 tiles below 8 rows (a batch item's 64 channels are one), 8 below 12, 4 from there on.
+BLOCKS = [
+    # B, L, D, dtype, rule, reverse, options                                   rows
+    (7, 2500, 12, "f32", "lerp", False, dict(reset=0.002)),                   # 7
+    (8, 2177, 20, "bf16", "sqrt", False, {}),                                 # 8
+    (1, 2309, 640, "f32", "sqrt", False, {}),                                 # 10
+    (1, 2309, 640, "bf16", "lerp", True, dict(reset=0.002)),                  # 10
+    (11, 1100, 64, "f32", "unit", True, dict(reset=0.004, lam=False)),        # 11
+    (12, 700, 8, "f32", "sqrt", True, {}),                                    # 12
+    (3, 1500, 392, "f32", "sqrt", False, dict(reset=0.003)),                  # 21
+    (3, 1500, 392, "bf16", "unit", True, dict(lam=False)),                    # 21
+    (1, 1025, 1300, "f32", "lerp", False, dict(z=False, reset=0.003)),        # 21
+    (2, 640, 2048, "bf16", "sqrt", False, {}),                                # 64: exactly 5 forward tiles, 10 backward
+]
+
+
+@pytest.mark.parametrize("case", BLOCKS, ids=lambda c: "B%d-L%d-D%d-%s-%s-rev%d" % c[:6])
+def test_chains_of_several_blocks(case):
+    """The tolerances of test_gpu_glr, whose inputs and checks these are."""
+    import test_gpu_glr as base
+    B, L, D, dtype, rule, reverse, opt = case
+    print("[gpu case] glr blocks", case, flush=True)
+    dev, ref = base.make(B, L, D, dtype, L + D, **opt)
+    kw, rkw = base.kwargs(dev, rule, reverse, False), base.kwargs(ref, rule, reverse, True)
+    out, last, saved = ms.glr_fwd_save(*base.args(dev), **kw)
+    g = ms.glr_bwd(*base.args(dev), dout=dev["dout"], dlast=dev["dlast"], saved=saved, **kw)
+    torch().cuda.synchronize()
+    want, want_last, _, _ = glr_ref(*base.args(ref), **rkw)
+    wg = glr_grads(*base.args(ref), ref["dout"], ref["dlast"], **rkw)
+    base.close("out", from_dev(out), want, dtype)
+    base.close("last_state", from_dev(last), want_last, "f32")
+    for k, w in wg.items():
+        assert (g[k] is None) == (w is None), k
+        if w is not None:
+            base.close(k, from_dev(g[k]), w, "f32" if k in ("dlam", "dinit") else dtype)
+
+
+def test_overlapping_calls_on_two_streams():
+    """Each waits in its own memory: what two streams run at once, and on one workspace each, is what one runs alone."""
+    t = torch()
+    gen = t.Generator(device="cuda:0")
+    gen.manual_seed(8)
+
+    def case(L, D):
+        v = [t.randn(1, L, D, generator=gen, device="cuda:0").bfloat16() for _ in range(5)]
+        lam = t.full((D,), -4.0, device="cuda:0")
+        w = (t.randn(D, D, generator=gen, device="cuda:0") / D ** 0.5).bfloat16()
+
+        def call(stream, ws):
+            k = dict(stream=stream)
+            n, mean, rstd = ms.group_norm_fwd(v[0], 4, act=ms.ACT_SILU, workspace=ws[0], **k)
+            p, pre = ms.linear_fwd(n, w, act=ms.ACT_SILU, want_pre=True, workspace=ws[1], **k)
+            out, last, saved = ms.glr_fwd_save(p, *v[1:4], lam, workspace=ws[2], **k)
+            g = ms.glr_bwd(p, *v[1:4], lam, dout=v[4], saved=saved, workspace=ws[2], **k)
+            d = ms.linear_bwd(n, w, dout=g["dx"], pre=pre, act=ms.ACT_SILU, workspace=ws[1], **k)
+            e = ms.group_norm_bwd(v[0], 4, dout=d["dx"], mean=mean, rstd=rstd, act=ms.ACT_SILU, workspace=ws[0], **k)
+            return [out, last, g["dr"], g["dlam"], d["dweight"], d["dbias"], e["dx"]]
+        return call
+
+    calls = [case(20000, 192), case(9000, 640)]
+    streams = [t.cuda.Stream(), t.cuda.Stream()]
+    none = (None, None, None)
+    print("[gpu case] two streams", flush=True)
+    want = [c(None, none) for c in calls]
+    t.cuda.synchronize()
+    spaces = [[t.empty(64 << 20, dtype=t.uint8, device="cuda:0") for _ in range(3)] for _ in calls]
+    t.cuda.synchronize()
+    for ws in ([none, none], spaces):
+        got = [[], []]
+        for _ in range(5):
+            for k, c in enumerate(calls):
+                got[k].append(c(streams[k], ws[k]))
+        t.cuda.synchronize()
+        for k in range(2):
+            for run in got[k]:
+                assert all(t.equal(a, b) for a, b in zip(run, want[k]))
