@@ -190,12 +190,18 @@ __device__ __forceinline__ float run_mul(float A, float B) {
 // Tickets hand the tiles out in the order of the chain, so a workgroup only
 // ever waits for one that has already started, and every wait ends.
 // Longer blocks cost their last tile more and the others a longer way to their
-// state: they pay where few rows leave the waits as all there is.  us forward /
-// backward in bf16 with blocks of 4, 8 and 16: 1 x 26155 x 16 (one row) 35 / 66,
-// 24 / 42, 19 / 32 (waiting for the tile before alone: 56 / 138); 1 x 200000 x
-// 640 (10 rows) 348 / 723, 342 / 637, 358 / 645; 12 x 28897 x 16 65 / 117, 66 /
-// 119, 68 / 122; 1 x 262144 x 2048 (32 rows) 1225 / 2234, 1296 / 2254, 1347 /
-// 2278 (of 2: 1248 / 2342).  So 16 below 8 rows, 8 below 12, else 4.
+// state: they pay where few rows leave the waits as all there is.  In bf16, us forward /
+// backward with blocks of 4, 8 and 16:
+//   rows  1 (1 x 26155 x 16)      35 / 66, 24 / 42, 19 / 32 (waiting for the tile before alone: 56 / 138)
+//   rows  6 (1 x 100000 x 384)   147 / 294, 115 / 213, 118 / 208
+//   rows  7 (7 x 30000 x 64)      53 / 101, 47 / 82, 48 / 84
+//   rows  8 (1 x 50000 x 512)     78 / 160, 74 / 136, 76 / 137
+//   rows 10 (1 x 200000 x 640)   356 / 734, 350 / 650, 367 / 657; 1 x 3000 x 640 16 / 25 with each
+//   rows 11 (1 x 50000 x 704)    101 / 196, 100 / 184, 104 / 187; 11 x 30000 x 64 62 / 110, 62 / 110, 63 / 111
+//   rows 12 (12 x 28897 x 16)     62 / 109, 62 / 110, 63 / 112
+//   rows 15 (1 x 100000 x 960)   243 / 460, 248 / 453, 257 / 458
+//   rows 32 (1 x 262144 x 2048) 1225 / 2234, 1296 / 2254, 1347 / 2278 (of 2: 1248 / 2342)
+// So 16 below 8 rows (what one row needs; within 3 % of blocks of 8 at 6 and 7), 8 below 12, else 4.
 constexpr int kGlrBatch = 3;  // runs fetched at a time (4 and 5: the longest sequence 1 % slower)
 
 __device__ __forceinline__ void word_put(uint64_t* p, uint32_t tag, float v) {

@@ -22,8 +22,8 @@ int pow2_at_least(int n) {
 }
 
 // Workgroups wanted of a map's passes.  Forward / backward in us at 512, 1024
-// and 2048: 32 x 4096 x 192 34.4 / 56.6, 34.0 / 58.7, 42.6 / 71.6; 128 x 197 x
-// 768 42 / 82, 38 / 71, 49 / 87; 2 x 16384 x 512 25, 28, 31 forward.
+// and 2048: 32 x 4096 x 192 32.6 / 55.8, 33.2 / 58.4, 39.0 / 67.2; 128 x 197 x
+// 768 37.4 / 60.9, 34.1 / 56.5, 40.3 / 70.7; 2 x 16384 x 512 25.3, 28.6, 28.9 forward.
 constexpr int64_t kNormBlocks = 1024;
 
 struct NormPlan {

@@ -70,8 +70,8 @@ __device__ __forceinline__ float lane_sum(float v, int width) {
 // repeat the last one and are not used.  BACK walks from the last row to the
 // first: a second pass then begins with what the first one has left in the
 // caches (bf16, second passes from the front and from the back: 64 x 4096 x 384,
-// whose 600 MB pass the last-level cache, backward 212 and 186 us; 32 x 4096 x
-// 192, whose do not, forward 33.0 and 32.3).
+// whose 600 MB pass the last-level cache, backward 211 and 186 us; 32 x 4096 x
+// 192, whose do not, forward 36.3 and 33.2).
 template <typename T, int NS, int U, bool BACK = false>
 struct RowWalk {
   const T* src[NS];
