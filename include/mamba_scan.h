@@ -460,6 +460,68 @@ MAMBA_API int mamba_linear_bwd(const void* x, const void* weight, const float* p
                                const mamba_linear_dims* dims, void* dx, void* dweight, float* dbias,
                                hipStream_t stream);
 
+/* ---- Root-mean-square norm with the residual's addition ----
+ *
+ *   s = x + residual, rounded to the residual's type (x without a residual)
+ *   rstd = 1/sqrt(mean(s²) + eps),  y = s·rstd·weight
+ * over rows of D channels; the sum as it is stored is what is normalised, so
+ * that the backward, which reads it, differentiates the same function.
+ * Statistics are float32: magnitudes above 1e19 / sqrt(D) pass their range.
+ * A row with a NaN or an infinity is NaN where that leaves it so, alone. */
+typedef struct {
+  int64_t rows;            /* >= 1 */
+  int64_t dim;             /* D in 1..16384 */
+  int32_t dtype;           /* mamba_dtype of x, out, dout and dx */
+  int32_t residual_dtype;  /* mamba_dtype of residual, added, s, dadded and dresidual: dtype, or float32 */
+  float eps;               /* >= 0 and finite; the forward's */
+  void* workspace;         /* device scratch owned by the caller, for dweight */
+  size_t workspace_bytes;
+} mamba_rms_dims;
+
+/* Bytes of workspace that the backward needs for dweight; a pure function of
+ * the sizes, (size_t)-1 when they are invalid or unsupported.  The contents
+ * need not be initialised. */
+MAMBA_API size_t mamba_rms_norm_bwd_workspace_bytes(const mamba_rms_dims* dims);
+
+/*
+ * Forward.  x, out [rows][D] dtype; residual, added [rows][D] residual_dtype or
+ * NULL (added is written with a residual only); weight [D] float32 or NULL (1);
+ * rstd [rows] float32, written, or NULL.  out may be x itself and added
+ * residual itself; nothing else may alias.  Any pointer aligned to its elements
+ * is taken; rows of a multiple of 8 channels on 16 bytes are read fastest.
+ * Errors: MAMBA_ERR_INVALID (NULL x or out, a size <= 0, an unknown type, eps
+ * negative or not finite), MAMBA_ERR_UNSUPPORTED (D above 16384, rows above
+ * 2^36, a bfloat16 residual of a float32 x, a pointer off its elements'
+ * alignment), MAMBA_ERR_HIP.
+ */
+MAMBA_API int mamba_rms_norm_fwd(const void* x, const void* residual, const float* weight, const mamba_rms_dims* dims,
+                                 void* out, void* added, float* rstd, hipStream_t stream);
+
+/*
+ * The same with y in 8 bits (e4m3, no infinities, largest 448), not rounded to
+ * dtype between:  scale = max(max|y| / 448, 2^-100) of a row, out = y / scale,
+ * rounded to nearest even.  out [rows][D] bytes, scale [rows] float32, written;
+ * a row of zeros has scale 2^-100, a row with a NaN is NaN throughout, its
+ * scale too.  Errors as above, and MAMBA_ERR_INVALID for a NULL scale.
+ */
+MAMBA_API int mamba_rms_norm_q8(const void* x, const void* residual, const float* weight, const mamba_rms_dims* dims,
+                                void* out, float* scale, void* added, hipStream_t stream);
+
+/*
+ * Backward for dout [rows][D] dtype and dadded [rows][D] residual_dtype or NULL
+ * (the gradient of added):  with xh = s·rstd and t = dout·weight,
+ *   ds = rstd·(t - xh·mean(t·xh)) + dadded,  dweight = Σ dout·xh
+ * ds is the gradient of x and of the residual: dx [rows][D] dtype, dresidual
+ * [rows][D] residual_dtype or NULL, dweight [D] float32 or NULL.  s is added,
+ * or x without a residual, residual_dtype; rstd what the forward wrote.  No
+ * output may alias an input or another output.  Sums are float32 and in a fixed
+ * order.  Errors as above, and MAMBA_ERR_WORKSPACE (dweight without its
+ * workspace).
+ */
+MAMBA_API int mamba_rms_norm_bwd(const void* s, const float* weight, const float* rstd, const void* dout,
+                                 const void* dadded, const mamba_rms_dims* dims, void* dx, void* dresidual,
+                                 float* dweight, hipStream_t stream);
+
 /* Static, human-readable text for a status code (never NULL). */
 MAMBA_API const char* mamba_status_string(int status);
 

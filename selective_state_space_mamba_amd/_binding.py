@@ -22,7 +22,9 @@ EXPORTED = ("mamba_conv1d_silu", "mamba_glr_bwd", "mamba_glr_bwd_workspace_bytes
             "mamba_glr_fwd_workspace_bytes", "mamba_glr_saved_bytes", "mamba_glr_step",
             "mamba_group_norm_bwd", "mamba_group_norm_bwd_workspace_bytes", "mamba_group_norm_fwd",
             "mamba_group_norm_fwd_workspace_bytes", "mamba_linear_bwd", "mamba_linear_bwd_workspace_bytes",
-            "mamba_linear_fwd", "mamba_linear_fwd_workspace_bytes", "mamba_linear_plan", "mamba_scan_bwd", "mamba_scan_bwd_workspace_bytes", "mamba_scan_fwd_workspace_bytes",
+            "mamba_linear_fwd", "mamba_linear_fwd_workspace_bytes", "mamba_linear_plan", "mamba_rms_norm_bwd",
+            "mamba_rms_norm_bwd_workspace_bytes", "mamba_rms_norm_fwd", "mamba_rms_norm_q8",
+            "mamba_scan_bwd", "mamba_scan_bwd_workspace_bytes", "mamba_scan_fwd_workspace_bytes",
             "mamba_scan_fwd", "mamba_scan_fwd_noalloc", "mamba_scan_fwd_save", "mamba_scan_saved_bytes",
             "mamba_scan_step",
             "mamba_status_string")
@@ -81,8 +83,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mamba_scan_fwd_save.argtypes = [vp] * 8 + [ctypes.POINTER(MambaDims), i32, vp, vp, vp, ctypes.c_size_t, vp]
     lib.mamba_conv1d_silu.restype = i32
     lib.mamba_conv1d_silu.argtypes = [vp, vp, vp, ctypes.POINTER(MambaDims), i32, i32, vp, vp]
-    from . import _glr, _linear, _norm
-    for part in (_glr, _norm, _linear):
+    from . import _glr, _linear, _norm, _rms
+    for part in (_glr, _norm, _linear, _rms):
         part.declare(lib)
     lib.mamba_status_string.restype = ctypes.c_char_p
     lib.mamba_status_string.argtypes = [i32]

@@ -1,0 +1,284 @@
+// rms_kernels.h -- gfx950 HIP kernels of the root-mean-square norm with the
+// residual's addition, over rows of D channels:
+//   s = round(x + residual)  (x without a residual),  rstd = 1/sqrt(mean(s²) + eps),  y = s·rstd·w
+// with y rounded to x's type, or to 8 bits (e4m3) by the row's own scale:
+//   scale = max(max|y|/448, 2^-100),  q = y/scale
+// Backward, with xh = s·rstd and t = dout·w:
+//   ds = rstd·(t - xh·mean(t·xh)) + dadded,  dw = Σ_rows dout·xh
+//
+// What is normalised is the sum as it is stored (in the residual's type), so
+// that the backward, which reads the stored sum, differentiates the function
+// that the forward computed.
+//
+// Layout.  A row lies in the registers of W waves, NV vectors of 8 channels a
+// lane, so every tensor is read once; one wave a row up to 2048 channels where
+// there are rows enough, four or eight beyond.  Bound by bytes.
+// RAG: rows that are no multiple of 8 channels, or that begin off 16 bytes.
+// Their vectors are loaded from wherever they lie (global memory takes 16 bytes
+// at any address) and the last one element by element.
+#pragma once
+
+#include "colsum.h"
+#include "device_math.h"
+#include "wide_grid.h"
+
+namespace mscan {
+
+constexpr float kTop8 = 448.0f;                    // the largest e4m3 value
+constexpr float kLeastScale = 7.888609052210118e-31f;  // 2^-100: its reciprocal is finite
+
+struct RmsParams {
+  const void* x;      // [rows][D]
+  const void* res;    // [rows][D] or null
+  const float* w;     // [D] or null
+  void* out;          // [rows][D], x's type or 8 bits
+  void* added;        // [rows][D], the residual's type, or null
+  float* rstd;        // [rows] or null
+  float* scale;       // [rows], 8 bits
+  int64_t rows;
+  int D;
+  float eps;
+};
+
+struct RmsGradParams {
+  const void* s;       // [rows][D], the residual's type
+  const float* w;      // [D] or null
+  const float* rstd;   // [rows]
+  const void* dout;    // [rows][D], x's type
+  const void* dadded;  // [rows][D], the residual's type, or null
+  void* dx;            // [rows][D], x's type
+  void* dres;          // [rows][D], the residual's type, or null
+  float* part;         // [workgroups][D] or null
+  int64_t rows;
+  int D;
+};
+
+// Vector i of a row of `full` whole vectors of 8 and `rest` elements more; zeros past the end.
+template <bool RAG, typename T>
+__device__ __forceinline__ void vec_load(Vec<T, 8>& v, const T* row, int i, int full, int rest) {
+  if (i < full) {
+    if constexpr (RAG) __builtin_memcpy(&v, row + i * 8, 8 * sizeof(T));
+    else v.load(row + i * 8);
+  } else {
+    v.zero();
+    if (RAG && i == full) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < rest) {
+          if constexpr (sizeof(T) == 2) v.w[j >> 1] |= (uint32_t)row[i * 8 + j] << (16 * (j & 1));
+          else v.f[j] = row[i * 8 + j];
+        }
+    }
+  }
+}
+template <bool RAG, typename T>
+__device__ __forceinline__ void vec_store(T* row, int i, int full, int rest, const float (&y)[8]) {
+  if (i < full) {
+    if constexpr (RAG) {
+      T tmp[8];
+      storeV<8>(tmp, y);
+      __builtin_memcpy(row + i * 8, tmp, sizeof(tmp));
+    } else {
+      storeV<8>(row + i * 8, y);
+    }
+  } else if (RAG && i == full) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < rest) store1(row + i * 8 + j, y[j]);
+  }
+}
+// The same in e4m3 (rounded to nearest even).
+template <bool RAG>
+__device__ __forceinline__ void vec_store8(uint8_t* row, int i, int full, int rest, const float (&y)[8]) {
+  uint32_t q[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * h], y[4 * h + 1], 0, false);
+    v = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * h + 2], y[4 * h + 3], v, true);
+    q[h] = (uint32_t)v;
+  }
+  if (i < full) {
+    if constexpr (RAG) __builtin_memcpy(row + i * 8, q, 8);
+    else *reinterpret_cast<uint2*>(row + i * 8) = make_uint2(q[0], q[1]);
+  } else if (RAG && i == full) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < rest) row[i * 8 + j] = (uint8_t)(q[j >> 2] >> (8 * (j & 3)));
+  }
+}
+
+// y as the element type holds it.
+__device__ __forceinline__ void round_to(float (&y)[8], uint16_t*) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const uint32_t w = pack_bf16x2(y[j], y[j + 1]);
+    y[j] = __uint_as_float(w << 16), y[j + 1] = __uint_as_float(w & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void round_to(float (&)[8], float*) {}
+
+struct AddOp {
+  __device__ static __forceinline__ float of(float a, float b) { return a + b; }
+};
+// A NaN on either side stays (the plain maximum drops it).
+struct MaxOp {
+  __device__ static __forceinline__ float of(float a, float b) { return a != a || a > b ? a : b; }
+};
+// Over the lanes of the W waves of a row, left in each of them; red: a float a wave.
+template <int W, typename OP>
+__device__ __forceinline__ float row_join(float v, float* red) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = OP::of(v, __shfl_xor(v, o));
+  if constexpr (W > 1) {
+    __syncthreads();  // the last join's values have been read
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    const float* const at = red + (threadIdx.x >> 6) / W * W;
+    v = at[0];
+#pragma unroll
+    for (int k = 1; k < W; ++k) v = OP::of(v, at[k]);
+  }
+  return v;
+}
+
+template <int W>
+constexpr int rms_threads() { return W > 4 ? 64 * W : 256; }
+
+// T: x's type, R: the residual's, Q8: 8-bit output
+template <typename T, typename R, bool Q8, bool RAG, int W, int NV>
+__global__ void __launch_bounds__(rms_threads<W>()) rms_fwd_kernel(const RmsParams p) {
+  __shared__ float red[rms_threads<W>() / 64];
+  constexpr int kPer = rms_threads<W>() / (64 * W);  // rows of a workgroup
+  const int li = threadIdx.x % (64 * W);
+  const int64_t row = wide_block() * kPer + threadIdx.x / (64 * W);
+  if (row >= p.rows) return;  // (a row's waves, all of a workgroup's for W > 1)
+  const int full = p.D >> 3, rest = p.D & 7;
+  const int64_t at = row * p.D;
+  float s[NV][8];
+  {
+    Vec<T, 8> x[NV];
+    Vec<R, 8> r[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) vec_load<RAG>(x[i], static_cast<const T*>(p.x) + at, li + i * 64 * W, full, rest);
+    if (p.res) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) vec_load<RAG>(r[i], static_cast<const R*>(p.res) + at, li + i * 64 * W, full, rest);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i][j] = x[i].get(j);
+      if (p.res) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[i][j] += r[i].get(j);
+        round_to(s[i], (R*)nullptr);
+        if (p.added) vec_store<RAG>(static_cast<R*>(p.added) + at, li + i * 64 * W, full, rest, s[i]);
+      }
+    }
+  }
+  float q = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q = __builtin_fmaf(s[i][j], s[i][j], q);
+  q = row_join<W, AddOp>(q, red);
+  const float rstd = 1.0f / __builtin_sqrtf(q / (float)p.D + p.eps);
+  if (p.rstd && li == 0) p.rstd[row] = rstd;
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    Vec<float, 8> w;
+    if (p.w) vec_load<RAG>(w, p.w, li + i * 64 * W, full, rest);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      s[i][j] *= rstd;
+      if (p.w) s[i][j] *= w.get(j);
+      if (Q8) top = MaxOp::of(top, __builtin_fabsf(s[i][j]));
+    }
+    if constexpr (!Q8) vec_store<RAG>(static_cast<T*>(p.out) + at, li + i * 64 * W, full, rest, s[i]);
+  }
+  if constexpr (Q8) {
+    const float scale = MaxOp::of(row_join<W, MaxOp>(top, red) / kTop8, kLeastScale), inv = 1.0f / scale;
+    if (li == 0) p.scale[row] = scale;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i][j] *= inv;
+      vec_store8<RAG>(static_cast<uint8_t*>(p.out) + at, li + i * 64 * W, full, rest, s[i]);
+    }
+  }
+}
+
+// A workgroup walks rows, its waves' sums for dw in registers until the end.
+template <typename T, typename R, bool RAG, int W, int NV>
+__global__ void __launch_bounds__(rms_threads<W>()) rms_bwd_kernel(const RmsGradParams p) {
+  constexpr int kPer = rms_threads<W>() / (64 * W);
+  __shared__ float red[rms_threads<W>() / 64];
+  __shared__ float sums[kPer > 1 ? (kPer - 1) * NV * 64 * 8 : 1];
+  const int li = threadIdx.x % (64 * W), k = threadIdx.x / (64 * W);
+  const int full = p.D >> 3, rest = p.D & 7;
+  const float inv = 1.0f / (float)p.D;
+  float w[NV][8], dw[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    Vec<float, 8> v;
+    if (p.w) vec_load<RAG>(v, p.w, li + i * 64 * W, full, rest);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[i][j] = p.w ? v.get(j) : 1.f, dw[i][j] = 0.f;
+  }
+  for (int64_t row = (int64_t)blockIdx.x * kPer + k; row < p.rows; row += (int64_t)gridDim.x * kPer) {
+    const int64_t at = row * p.D;
+    Vec<R, 8> s[NV], da[NV];
+    Vec<T, 8> dy[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      vec_load<RAG>(s[i], static_cast<const R*>(p.s) + at, li + i * 64 * W, full, rest);
+      vec_load<RAG>(dy[i], static_cast<const T*>(p.dout) + at, li + i * 64 * W, full, rest);
+      if (p.dadded) vec_load<RAG>(da[i], static_cast<const R*>(p.dadded) + at, li + i * 64 * W, full, rest);
+    }
+    const float rstd = p.rstd[row];
+    float c = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float xh = s[i].get(j) * rstd, g = dy[i].get(j);
+        c = __builtin_fmaf(g * w[i][j], xh, c);
+        dw[i][j] = __builtin_fmaf(g, xh, dw[i][j]);
+      }
+    c = row_join<W, AddOp>(c, red) * inv;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float d[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        d[j] = rstd * __builtin_fmaf(-(s[i].get(j) * rstd), c, dy[i].get(j) * w[i][j]);
+        if (p.dadded) d[j] += da[i].get(j);
+      }
+      vec_store<RAG>(static_cast<T*>(p.dx) + at, li + i * 64 * W, full, rest, d);
+      if (p.dres) vec_store<RAG>(static_cast<R*>(p.dres) + at, li + i * 64 * W, full, rest, d);
+    }
+  }
+  if (!p.part) return;
+  if constexpr (kPer > 1) {  // the waves' sums to the first one's, in order
+    if (k > 0) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sums[(((k - 1) * NV + i) * 8 + j) * 64 + li] = dw[i][j];
+    }
+    __syncthreads();
+    if (k > 0) return;
+#pragma unroll
+    for (int q = 0; q < kPer - 1; ++q)
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[i][j] += sums[((q * NV + i) * 8 + j) * 64 + li];
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    vec_store<RAG>(p.part + (int64_t)blockIdx.x * p.D, li + i * 64 * W, full, rest, dw[i]);
+}
+
+}  // namespace mscan
