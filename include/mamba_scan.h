@@ -522,6 +522,98 @@ MAMBA_API int mamba_rms_norm_bwd(const void* s, const float* weight, const float
                                  const void* dadded, const mamba_rms_dims* dims, void* dx, void* dresidual,
                                  float* dweight, hipStream_t stream);
 
+/* ---- Gated pair of products ----
+ *
+ *   g = x·w_gateᵀ + b_gate,  u = x·w_upᵀ + b_up,  out = act(g)·u
+ * the first half of a gated feed-forward block (with MAMBA_ACT_SILU, GELU, RELU
+ * or NONE), in one kernel; mamba_linear_fwd is the second.  Sums, biases,
+ * activation and product are taken in float32 and rounded once.  The sizes are
+ * a mamba_linear_dims: M rows of K channels to N. */
+
+/* Bytes of workspace; pure functions of the sizes, (size_t)-1 when the
+ * arguments are invalid or unsupported.  The contents need not be initialised. */
+MAMBA_API size_t mamba_gated_linear_fwd_workspace_bytes(const mamba_linear_dims* dims);
+MAMBA_API size_t mamba_gated_linear_bwd_workspace_bytes(const mamba_linear_dims* dims);
+
+/*
+ * Forward.  x [M][K], w_gate, w_up [N][K], out [M][N] dtype; b_gate, b_up [N]
+ * float32 or NULL, each; pre [2][M][N] float32 or NULL: g and u, written for
+ * the backward.  No output may alias an input.  Errors: MAMBA_ERR_INVALID (NULL
+ * x, a weight or out, a size <= 0, unknown dtype or act), MAMBA_ERR_UNSUPPORTED
+ * (K or N not a multiple of 8, K above 2^20, N above 2^19, M above 2^29, a
+ * pointer not 16-byte aligned), MAMBA_ERR_WORKSPACE, MAMBA_ERR_HIP.
+ */
+MAMBA_API int mamba_gated_linear_fwd(const void* x, const void* w_gate, const void* w_up, const float* b_gate,
+                                     const float* b_up, const mamba_linear_dims* dims, void* out, float* pre,
+                                     hipStream_t stream);
+
+/*
+ * Backward for dout [M][N] dtype and the forward's pre:  dg = dout·u·act'(g)
+ * and du = dout·act(g), rounded to dtype before the products,
+ *   dx = dg·w_gate + du·w_up,  dw_gate = dgᵀ·x,  dw_up = duᵀ·x,
+ * and unrounded in db_gate = Σ dg, db_up = Σ du.  dx [M][K], dw_gate, dw_up
+ * [N][K] dtype, db_gate, db_up [N] float32: dx, the dw pair and the db pair may
+ * each be NULL (not computed), not all three.  The weights are read for dx, x
+ * for the dw pair.  Sums run in a fixed order.  No output may alias an input.
+ * Errors as for mamba_gated_linear_fwd.
+ */
+MAMBA_API int mamba_gated_linear_bwd(const void* x, const void* w_gate, const void* w_up, const float* pre,
+                                     const void* dout, const mamba_linear_dims* dims, void* dx, void* dw_gate,
+                                     void* dw_up, float* db_gate, float* db_up, hipStream_t stream);
+
+/* ---- Matrix product of 8-bit operands ----
+ *
+ *   out[m][n] = act(x_scale[m]·w_scale[n]·Σ_k x[m][k]·weight[n][k] + bias[n]) + residual[m][n]
+ * with x [M][K] and weight [N][K] in e4m3 (as mamba_rms_norm_q8 writes it) and
+ * a float32 scale for each row of either.  Sums are float32, products exact.
+ * In the mamba_linear_dims dtype is that of residual and out; K is a multiple
+ * of 16. */
+
+/* Bytes of workspace; a pure function of the sizes, (size_t)-1 when the
+ * arguments are invalid or unsupported.  The contents need not be initialised. */
+MAMBA_API size_t mamba_linear_q8_workspace_bytes(const mamba_linear_dims* dims);
+
+/*
+ * x_scale [M], w_scale [N] float32; bias [N] float32 or NULL; residual, out
+ * [M][N] dtype, residual NULL or out itself.  No other output may alias an
+ * input.  Errors: MAMBA_ERR_INVALID (NULL x, weight, a scale or out, a size <=
+ * 0, unknown dtype or act), MAMBA_ERR_UNSUPPORTED (K not a multiple of 16 or N
+ * of 8, either above 2^20, M above 2^29, a pointer not 16-byte aligned),
+ * MAMBA_ERR_WORKSPACE, MAMBA_ERR_HIP.
+ */
+MAMBA_API int mamba_linear_q8(const void* x, const float* x_scale, const void* weight, const float* w_scale,
+                              const float* bias, const void* residual, const mamba_linear_dims* dims, void* out,
+                              hipStream_t stream);
+
+/* ---- Matrix product with 4-bit weights in groups ----
+ *
+ *   out[m][n] = act(Σ_k (q[n][k] - zero[n][k/group])·scale[n][k/group]·x[m][k] + bias[n]) + residual[m][n]
+ * for few rows (a token of each of some sequences): the weights are read once
+ * for 64 rows.  Weights are not rounded on the way: products are exact, sums
+ * float32.  A row of x with an infinity or a NaN is NaN throughout. */
+typedef struct {
+  int64_t rows;        /* M in 1..2^20 */
+  int64_t in_dim;      /* K in 32..2^20, a multiple of 32 */
+  int64_t out_dim;     /* N in 8..2^20, a multiple of 8 */
+  int64_t group;       /* 32, 64 or a multiple of 128, up to 2^20; K need not be a multiple of it */
+  int32_t dtype;       /* mamba_dtype of x, residual and out */
+  int32_t scale_dtype; /* mamba_dtype of scale */
+  int32_t act;         /* mamba_act */
+} mamba_q4_dims;
+
+/*
+ * x [M][K] dtype; weight [N][K/2] bytes, two weights q of 0..15 each, that of
+ * the even element in the low four bits; scale [N][ceil(K/group)] scale_dtype;
+ * zero [N][ceil(K/group)] bytes of 0..127, or NULL (8 throughout); bias [N]
+ * float32 or NULL; residual, out [M][N] dtype, residual NULL or out itself.  No
+ * other output may alias an input.  Errors: MAMBA_ERR_INVALID (NULL x, weight,
+ * scale or out, a size <= 0, an unknown type or act), MAMBA_ERR_UNSUPPORTED
+ * (sizes outside the above, x, weight, residual or out not 16-byte aligned, scale or bias off
+ * its elements' alignment), MAMBA_ERR_HIP.
+ */
+MAMBA_API int mamba_linear_q4(const void* x, const void* weight, const void* scale, const void* zero, const float* bias,
+                              const void* residual, const mamba_q4_dims* dims, void* out, hipStream_t stream);
+
 /* Static, human-readable text for a status code (never NULL). */
 MAMBA_API const char* mamba_status_string(int status);
 

@@ -18,16 +18,17 @@ MAMBA_OK, MAMBA_ERR_INVALID, MAMBA_ERR_UNSUPPORTED, MAMBA_ERR_WORKSPACE, MAMBA_E
 NOALLOC_SCRATCH_BYTES = 32 << 20
 DIR_FWD, DIR_BWD, DIR_BIDIR, DIR_CROSS2D = 0, 1, 2, 3
 DTYPE_F32, DTYPE_BF16 = 0, 1
-EXPORTED = ("mamba_conv1d_silu", "mamba_glr_bwd", "mamba_glr_bwd_workspace_bytes", "mamba_glr_fwd",
-            "mamba_glr_fwd_workspace_bytes", "mamba_glr_saved_bytes", "mamba_glr_step",
-            "mamba_group_norm_bwd", "mamba_group_norm_bwd_workspace_bytes", "mamba_group_norm_fwd",
-            "mamba_group_norm_fwd_workspace_bytes", "mamba_linear_bwd", "mamba_linear_bwd_workspace_bytes",
-            "mamba_linear_fwd", "mamba_linear_fwd_workspace_bytes", "mamba_linear_plan", "mamba_rms_norm_bwd",
-            "mamba_rms_norm_bwd_workspace_bytes", "mamba_rms_norm_fwd", "mamba_rms_norm_q8",
-            "mamba_scan_bwd", "mamba_scan_bwd_workspace_bytes", "mamba_scan_fwd_workspace_bytes",
-            "mamba_scan_fwd", "mamba_scan_fwd_noalloc", "mamba_scan_fwd_save", "mamba_scan_saved_bytes",
-            "mamba_scan_step",
-            "mamba_status_string")
+EXPORTED = ("mamba_conv1d_silu", "mamba_gated_linear_bwd", "mamba_gated_linear_bwd_workspace_bytes",
+            "mamba_gated_linear_fwd", "mamba_gated_linear_fwd_workspace_bytes", "mamba_glr_bwd",
+            "mamba_glr_bwd_workspace_bytes", "mamba_glr_fwd", "mamba_glr_fwd_workspace_bytes",
+            "mamba_glr_saved_bytes", "mamba_glr_step", "mamba_group_norm_bwd",
+            "mamba_group_norm_bwd_workspace_bytes", "mamba_group_norm_fwd", "mamba_group_norm_fwd_workspace_bytes",
+            "mamba_linear_bwd", "mamba_linear_bwd_workspace_bytes", "mamba_linear_fwd",
+            "mamba_linear_fwd_workspace_bytes", "mamba_linear_plan", "mamba_linear_q4", "mamba_linear_q8",
+            "mamba_linear_q8_workspace_bytes", "mamba_rms_norm_bwd", "mamba_rms_norm_bwd_workspace_bytes",
+            "mamba_rms_norm_fwd", "mamba_rms_norm_q8", "mamba_scan_bwd", "mamba_scan_bwd_workspace_bytes",
+            "mamba_scan_fwd", "mamba_scan_fwd_noalloc", "mamba_scan_fwd_save", "mamba_scan_fwd_workspace_bytes",
+            "mamba_scan_saved_bytes", "mamba_scan_step", "mamba_status_string")
 
 
 class MambaDims(ctypes.Structure):
@@ -83,8 +84,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mamba_scan_fwd_save.argtypes = [vp] * 8 + [ctypes.POINTER(MambaDims), i32, vp, vp, vp, ctypes.c_size_t, vp]
     lib.mamba_conv1d_silu.restype = i32
     lib.mamba_conv1d_silu.argtypes = [vp, vp, vp, ctypes.POINTER(MambaDims), i32, i32, vp, vp]
-    from . import _glr, _linear, _norm, _rms
-    for part in (_glr, _norm, _linear, _rms):
+    from . import _gated, _glr, _linear, _norm, _quant, _rms
+    for part in (_glr, _norm, _linear, _rms, _gated, _quant):
         part.declare(lib)
     lib.mamba_status_string.restype = ctypes.c_char_p
     lib.mamba_status_string.argtypes = [i32]

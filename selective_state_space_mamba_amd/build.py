@@ -22,11 +22,11 @@ INST = os.path.join(CSRC, "scan_inst.hip")
 ROWS = os.path.join(CSRC, "row_inst.hip")
 GLR_HOST = os.path.join(CSRC, "glr.hip")
 GLR = os.path.join(CSRC, "glr_inst.hip")
-HOSTS = [HOST, GLR_HOST, os.path.join(CSRC, "norm.hip"), os.path.join(CSRC, "linear.hip"),
-         os.path.join(CSRC, "rms.hip")]
+HOSTS = [HOST, GLR_HOST] + [os.path.join(CSRC, f) for f in ("norm.hip", "linear.hip", "gated.hip", "linear_q8.hip", "linear_q4.hip",
+                                                            "rms.hip")]
 SOURCES = HOSTS + [INST, ROWS, GLR]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("scan_launch.h", "scan_kernels.h", "scan_row.h", "scan_bwd.h", "conv_kernels.h",
-                                                  "device_math.h", "glr_kernels.h", "glr_launch.h", "act_math.h", "colsum.h", "wide_grid.h", "norm_kernels.h", "linear_kernels.h", "rms_kernels.h")] + [
+                                                  "device_math.h", "glr_kernels.h", "glr_launch.h", "act_math.h", "colsum.h", "wide_grid.h", "norm_kernels.h", "linear_kernels.h", "linear_launch.h", "q4_kernels.h", "rms_kernels.h")] + [
     os.path.join(ROOT, "include", "mamba_scan.h")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # (bf16, exact) flags of the four instantiation units

@@ -60,6 +60,24 @@ __device__ __forceinline__ float act_d(float u) {
   return 1.f;
 }
 
+// Both at once.
+template <int ACT>
+__device__ __forceinline__ void act_fd(float u, float& f, float& d) {
+  if constexpr (ACT == ACT_SILU) {
+    const float q = rcp(1.0f + ex2(-u * kLog2e));
+    f = u * q;
+    d = q * __builtin_fmaf(u, 1.0f - q, 1.0f);
+  } else if constexpr (ACT == ACT_GELU) {
+    float e;
+    const float cdf = normal_cdf(u, e);
+    f = u * cdf;
+    d = __builtin_fmaf(u * 0.39894228040143267794f, e, cdf);
+  } else {
+    f = act_f<ACT>(u);
+    d = act_d<ACT>(u);
+  }
+}
+
 template <int ACT, int V>
 __device__ __forceinline__ void act_each(float (&v)[V]) {
 #pragma unroll

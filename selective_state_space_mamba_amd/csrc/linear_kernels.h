@@ -13,6 +13,13 @@
 // instructions with float32 sums; the output's column axis N takes the
 // instruction's row side, which leaves each lane with four neighbouring
 // columns of one output row.
+//
+// The same kernels serve, as modes of the product: the gated pair of products
+// out = act(x·Wgᵀ + bg)·(x·Wuᵀ + bu), whose tile takes blocks of 32 rows of the
+// two weights in turn so that a wave holds both products of its outputs; that
+// pair's dx, one product whose contraction runs through both weights, and its
+// dW, one product with two outputs; and the product of 8-bit operands (e4m3),
+// whose outputs take a scale of their row and one of their column.
 #pragma once
 
 #include "act_math.h"
@@ -25,6 +32,8 @@ typedef float f32x4v __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+enum { PLAIN = 0, GATED = 1, TWO_K = 2, TWO_OUT = 3, SCALED = 4 };
+
 struct LinearParams {
   const void* a;         // rows of the output (M side)
   const void* b;         // columns of the output (N side)
@@ -36,6 +45,16 @@ struct LinearParams {
   float* pre;            // [M][N] or null
   float* part;           // [splits][M][N] or null: sums of a share of the contraction
   int act, splits, kt_per_split, tiles_m, tiles_n;
+  // GATED: b, bias, N of the gate, b2 and bias2 of the factor beside it; pre [2][M][N], part [splits][2][M][N]
+  // TWO_K: K elements of a's rows with b, then, a_seg further on, K with b2; kt_seg stages each
+  // TWO_OUT: rows from m_split on go to out2
+  // SCALED: sums times sx[row]·sw[column]
+  const void* b2;
+  const float* bias2;
+  void* out2;
+  const float *sx, *sw;
+  int64_t a_seg;
+  int kt_seg, m_split;
 };
 
 // V neighbouring outputs of one row, whose bias and residual are at hand.
@@ -43,9 +62,14 @@ struct LinearParams {
 // stores past it hold up the end of every tile (16384 x 768 x 1536 with pre
 // 79 -> 64 us, 4096 x 1024 x 4096 60 -> 47; 32768 x 2048 x 2048, whose outputs
 // the cache does not hold, 304 with either).
-template <typename T, int V>
-__device__ __forceinline__ void linear_finish(const LinearParams& p, int64_t at, const float (&bias)[V], const Vec<T, V>& res,
-                                              float (&v)[V]) {
+template <typename T, int MODE, int V>
+__device__ __forceinline__ void linear_finish(const LinearParams& p, int m, int64_t at, const float (&bias)[V], const float (&sw)[V],
+                                              const Vec<T, V>& res, float (&v)[V]) {
+  if constexpr (MODE == SCALED) {
+    const float sx = p.sx[m];
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] = v[j] * sx * sw[j];
+  }
 #pragma unroll
   for (int j = 0; j < V; ++j) v[j] += bias[j];
   if (p.pre) storeV<V>(p.pre + at, v);
@@ -54,13 +78,42 @@ __device__ __forceinline__ void linear_finish(const LinearParams& p, int64_t at,
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] += res.get(j);
   }
-  storeV<V>(static_cast<T*>(p.out) + at, v);
+  T* to = static_cast<T*>(p.out) + at;
+  if constexpr (MODE == TWO_OUT)
+    if (m >= p.m_split) to = static_cast<T*>(p.out2) + (at - (int64_t)p.m_split * p.N);
+  storeV<V>(to, v);
 }
-template <int V>
-__device__ __forceinline__ void linear_bias(const LinearParams& p, int n, float (&bias)[V]) {
+// The same for V outputs of a gated pair; g and u: the two sums.
+template <typename T, int V>
+__device__ __forceinline__ void gated_finish(const LinearParams& p, int64_t at, const float (&bg)[V], const float (&bu)[V], float (&g)[V],
+                                             float (&u)[V]) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) bias[j] = p.bias && n < p.N ? p.bias[n + j] : 0.f;
+  for (int j = 0; j < V; ++j) g[j] += bg[j], u[j] += bu[j];
+  if (p.pre) {
+    storeV<V>(p.pre + at, g);
+    storeV<V>(p.pre + (int64_t)p.M * p.N + at, u);
+  }
+  act_all(g, p.act);
+#pragma unroll
+  for (int j = 0; j < V; ++j) g[j] *= u[j];
+  storeV<V>(static_cast<T*>(p.out) + at, g);
 }
+// V values of a vector of the N columns from n on, zeros for none and past the end.
+template <int V>
+__device__ __forceinline__ void linear_cols(const LinearParams& p, const float* of, int n, float (&v)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) v[j] = of && n < p.N ? of[n + j] : 0.f;
+}
+// A lane's values of the vectors over columns that its mode needs: the bias, and the scale or the other bias.
+template <int MODE>
+struct Cols {
+  float bias[8], more[8];
+  __device__ __forceinline__ Cols(const LinearParams& p, int n) {
+    linear_cols(p, p.bias, n, bias);
+    if constexpr (MODE == GATED) linear_cols(p, p.bias2, n, more);
+    if constexpr (MODE == SCALED) linear_cols(p, p.sw, n, more);
+  }
+};
 
 // Where a lane's 8 columns begin among the wave's, of which it holds the c-th eight.
 template <int STEP>
@@ -73,26 +126,34 @@ __device__ __forceinline__ int linear_col(int c) {
 // columns apart from row m0 and column n0 on.  Each band of 32 rows goes through the wave's own LDS, so that a
 // lane then holds 8 neighbouring columns and a few lanes a whole row segment:
 // stores and residual loads of 16 bytes a lane and whole cache lines.
-template <typename T, int STEP, int FM, int FN>
-__device__ __forceinline__ void linear_out(const LinearParams& p, f32x16 (&acc)[FN][FM], const float (&bias)[8], float* lds, int m0,
+// GATED: of a wave's two blocks of columns the first is the gate's, the other the factor's, for the same 32 outputs.
+template <typename T, int MODE, int STEP, int FM, int FN>
+__device__ __forceinline__ void linear_out(const LinearParams& p, f32x16 (&acc)[FN][FM], const Cols<MODE>& cols, float* lds, int m0,
                                            int n0, int share, int lane) {
+  static_assert(MODE != GATED || FN == 2, "one pair of blocks");
   constexpr int W = FN * 32, kRow = W + 4;  // (rows 16 bytes apart in the banks)
-  constexpr int LPR = W / 8, RPI = 64 / LPR, IT = (32 + RPI - 1) / RPI;
+  constexpr int LPR = (MODE == GATED ? 32 : W) / 8, RPI = 64 / LPR, IT = (32 + RPI - 1) / RPI;
   const int r0 = lane / LPR, n = n0 + linear_col<STEP>(lane % LPR);
   const bool on = lane < LPR * RPI && n < p.N;
-  Vec<T, 8> res[FM][IT];  // all at once: they wait for memory one time, in the registers that the fragments have left
-  if (p.residual && !p.part) {
+  // Residuals all at once, where the registers that the fragments have left hold them: they wait for memory one time.
+  constexpr bool kAtOnce = FM * IT * 2 * sizeof(T) <= 64;
+  Vec<T, 8> res[kAtOnce ? FM : 1][IT];
+  auto residuals = [&](int j) {
 #pragma unroll
-    for (int j = 0; j < FM; ++j)
+    for (int it = 0; it < IT; ++it) {
+      const int r = it * RPI + r0, m = m0 + j * STEP + r;
+      if (on && r < 32 && m < p.M) res[kAtOnce ? j : 0][it].load(static_cast<const T*>(p.residual) + (int64_t)m * p.N + n);
+    }
+  };
+  const bool add = MODE != GATED && p.residual && !p.part;
+  if (kAtOnce && add) {
 #pragma unroll
-      for (int it = 0; it < IT; ++it) {
-        const int r = it * RPI + r0, m = m0 + j * STEP + r;
-        if (on && r < 32 && m < p.M) res[j][it].load(static_cast<const T*>(p.residual) + (int64_t)m * p.N + n);
-      }
+    for (int j = 0; j < FM; ++j) residuals(j);
   }
 #pragma unroll
   for (int j = 0; j < FM; ++j) {
     const int mb = m0 + j * STEP;
+    if (!kAtOnce && add) residuals(j);
 #pragma unroll
     for (int i = 0; i < FN; ++i)
 #pragma unroll
@@ -109,8 +170,24 @@ __device__ __forceinline__ void linear_out(const LinearParams& p, f32x16 (&acc)[
 #pragma unroll
         for (int c = 0; c < 8; ++c) v[c] = f.get(c);
         const int64_t at = (int64_t)(mb + r) * p.N + n;
-        if (p.part) storeV<8>(p.part + (int64_t)share * p.M * p.N + at, v);
-        else linear_finish(p, at, bias, res[j][it], v);
+        if constexpr (MODE == GATED) {
+          Vec<float, 8> h;
+          h.load(lds + r * kRow + 32 + (lane % LPR) * 8);
+          float u[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) u[c] = h.get(c);
+          if (p.part) {
+            float* const part = p.part + (int64_t)share * 2 * p.M * p.N + at;
+            storeV<8>(part, v);
+            storeV<8>(part + (int64_t)p.M * p.N, u);
+          } else {
+            gated_finish<T>(p, at, cols.bias, cols.more, v, u);
+          }
+        } else if (p.part) {
+          storeV<8>(p.part + (int64_t)share * p.M * p.N + at, v);
+        } else {
+          linear_finish<T, MODE>(p, mb + r, at, cols.bias, cols.more, res[kAtOnce ? j : 0][it], v);
+        }
       }
     }
   }
@@ -145,6 +222,22 @@ struct Elem<float> {
   }
 };
 
+// e4m3: a half stage is one instruction of 64 contraction elements, of which a
+// lane gives the 32 of its two chunks, on both sides the same.
+template <>
+struct Elem<uint8_t> {
+  static constexpr int BK = 128;
+  static constexpr int KS = 32;
+  static constexpr int CH = 16;
+  typedef u32x4 Frag;
+  __device__ static __forceinline__ f32x16 mma2(const Frag& a0, const Frag& a1, const Frag& b0, const Frag& b1, f32x16 c) {
+    typedef int i32x8 __attribute__((ext_vector_type(8)));
+    const i32x8 a = {(int)a0[0], (int)a0[1], (int)a0[2], (int)a0[3], (int)a1[0], (int)a1[1], (int)a1[2], (int)a1[3]};
+    const i32x8 b = {(int)b0[0], (int)b0[1], (int)b0[2], (int)b0[3], (int)b1[0], (int)b1[1], (int)b1[2], (int)b1[3]};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);  // (no block scales)
+  }
+};
+
 // A stage of one operand in LDS, 128 bytes of contraction deep, filled by loads
 // that go from memory straight to LDS: a wave's instruction fills 1 KB in lane
 // order, and which 16 bytes a lane fetches is free, so the bank swizzle is made
@@ -156,12 +249,15 @@ struct Elem<float> {
 // at block ^ swz(k), for the 4 rows of a transposing read.
 // Chunks past the operand's edge are fetched from beyond the buffer's range,
 // which gives zeros.
-template <typename T, int R, bool TR, int NW>
+// PAIR > 0 (the gated pair's weights): blocks of PAIR rows, in turn of either
+// operand; each of a wave's loads, 8 rows, lies in one of them.
+template <typename T, int R, bool TR, int NW, int PAIR = 0>
 struct Stage {
   typedef Elem<T> E;
   static constexpr int kRow = TR ? R : E::BK;  // elements of a row in LDS
   static constexpr int kCpr = kRow / E::CH;    // its chunks
   static constexpr int kElems = R * E::BK;
+  static constexpr int kBlock = PAIR > 0 ? PAIR : R;
   static constexpr int kLoads = kElems * (int)sizeof(T) / (1024 * NW);  // of a wave
   static_assert(kElems * (int)sizeof(T) % (1024 * NW) == 0, "whole loads");
   uint32_t off[kLoads];  // the lane's bytes from the stage's first element
@@ -177,19 +273,24 @@ struct Stage {
     for (int i = 0; i < kLoads; ++i) {
       const int at = (i * NW + wave) * 64 + lane, r = at / kCpr, slot = at % kCpr;
       const int c = TR ? slot ^ (swz(r) << 2) : slot ^ ((r >> 1) & 7);
-      const bool in = (TR ? c * E::CH : r) < rows;
+      const int row = PAIR == 0 ? r : r / (2 * kBlock) * kBlock + r % kBlock;
+      const bool in = (TR ? c * E::CH : row) < rows;
       kk[i] = TR ? r : c * E::CH;
-      off[i] = in ? (uint32_t)(r * (int)ld + c * E::CH) * (uint32_t)sizeof(T) : kDrop;
+      off[i] = in ? (uint32_t)(row * (int)ld + c * E::CH) * (uint32_t)sizeof(T) : kDrop;
     }
   }
   // base: the stage's first element in memory; ks: contraction elements left there
-  __device__ __forceinline__ void fetch(const T* base, T* lds, int wave, int ks) const {
+  // (base2: the other operand's, for PAIR)
+  __device__ __forceinline__ void fetch(const T* base, const T* base2, T* lds, int wave, int ks) const {
 #ifdef __HIP_DEVICE_COMPILE__  // (the host pass, which only needs the kernels' names, does not take the builtin)
-    const auto rsrc = make_rsrc(base, 0x7fffffffu);
+    const auto first = make_rsrc(base, 0x7fffffffu);
+    const auto second = make_rsrc(PAIR > 0 ? base2 : base, 0x7fffffffu);
     typedef __attribute__((address_space(3))) uint32_t* P;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const P to = (P)(lds + (i * NW + wave) * (1024 / (int)sizeof(T)));
+      static_assert(PAIR == 0 || kCpr == 8, "8 rows a load");
+      const auto rsrc = PAIR > 0 && ((i * NW + wave) * 8 / kBlock & 1) ? second : first;
       if (ks >= E::BK) __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, to, 16, (int)off[i], 0, 0, 0);
       else __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, to, 16, (int)(kk[i] < ks ? off[i] : kDrop), 0, 0, 0);
     }
@@ -261,37 +362,45 @@ __device__ __forceinline__ void tile_of(const LinearParams& p, int bid, int& tm,
 }
 
 // What both tile kernels start from: the workgroup's tile, its operands and its share of the contraction.
-template <typename T, bool TA, bool TB, int BM, int BN, int NW>
+template <typename T, int MODE, bool TA, bool TB, int BM, int BN, int NW>
 struct Tile {
   typedef Elem<T> E;
+  // (rows of a block of the pair: what a wave's two blocks of columns are apart)
+  static constexpr int kPair = MODE != GATED ? 0 : sizeof(T) == 4 ? 64 : 32;
+  static constexpr int kCols = MODE == GATED ? BN / 2 : BN;  // columns of the output
   typedef Stage<T, BM, TA, NW> SA;
-  typedef Stage<T, BN, TB, NW> SB;
+  typedef Stage<T, BN, TB, NW, kPair> SB;
   static constexpr int kStage = SA::kElems + SB::kElems;  // elements of a stage
   static constexpr int kLoads = SA::kLoads + SB::kLoads;  // loads of a wave
   int m0, n0, share, kt0, kt1;
-  const T *a, *b;
+  const T *a, *b, *b2;
   SA sa;
   SB sb;
   __device__ __forceinline__ Tile(const LinearParams& p, int wave, int lane) {
     int tm, tn;
     tile_of(p, blockIdx.x, tm, tn, share);
     m0 = tm * BM;
-    n0 = tn * BN;
+    n0 = tn * kCols;
     kt0 = share * p.kt_per_split;
-    kt1 = min((p.K + E::BK - 1) / E::BK, kt0 + p.kt_per_split);
+    kt1 = min(MODE == TWO_K ? 2 * p.kt_seg : (p.K + E::BK - 1) / E::BK, kt0 + p.kt_per_split);
     a = static_cast<const T*>(p.a) + (TA ? (int64_t)m0 : m0 * p.lda);
     b = static_cast<const T*>(p.b) + (TB ? (int64_t)n0 : n0 * p.ldb);
+    b2 = MODE == GATED || MODE == TWO_K ? static_cast<const T*>(p.b2) + (TB ? (int64_t)n0 : n0 * p.ldb) : b;
     sa.init(wave, lane, p.lda, p.M - m0);
     sb.init(wave, lane, p.ldb, p.N - n0);
   }
   __device__ __forceinline__ T* stage(T* lds, int kt) const { return lds + ((kt - kt0) & 1) * kStage; }
   __device__ __forceinline__ void fetch_a(const LinearParams& p, T* lds, int kt, int wave) const {
-    const int k0 = kt * E::BK;
-    sa.fetch(a + (TA ? k0 * p.lda : (int64_t)k0), stage(lds, kt), wave, p.K - k0);
+    const bool more = MODE == TWO_K && kt >= p.kt_seg;  // in the second part of the contraction
+    const int k0 = (more ? kt - p.kt_seg : kt) * E::BK;
+    const T* const at = a + (TA ? k0 * p.lda : (int64_t)k0) + (more ? p.a_seg : 0);
+    sa.fetch(at, at, stage(lds, kt), wave, p.K - k0);
   }
   __device__ __forceinline__ void fetch_b(const LinearParams& p, T* lds, int kt, int wave) const {
-    const int k0 = kt * E::BK;
-    sb.fetch(b + (TB ? k0 * p.ldb : (int64_t)k0), stage(lds, kt) + SA::kElems, wave, p.K - k0);
+    const bool more = MODE == TWO_K && kt >= p.kt_seg;
+    const int k0 = (more ? kt - p.kt_seg : kt) * E::BK;
+    const int64_t at = TB ? k0 * p.ldb : (int64_t)k0;
+    sb.fetch((more ? b2 : b) + at, b2 + at, stage(lds, kt) + SA::kElems, wave, p.K - k0);
   }
   __device__ __forceinline__ void fetch(const LinearParams& p, T* lds, int kt, int wave) const {
     fetch_a(p, lds, kt, wave);
@@ -302,11 +411,14 @@ struct Tile {
 template <typename E, int FM, int FN>
 __device__ __forceinline__ void mma_half(const typename E::Frag (&fa)[2][FM], const typename E::Frag (&fb)[2][FN], f32x16 (&acc)[FN][FM]) {
 #pragma unroll
-  for (int ks = 0; ks < 2; ++ks)
+  for (int ks = 0; ks < (E::CH == 16 ? 1 : 2); ++ks)
 #pragma unroll
     for (int i = 0; i < FN; ++i)
 #pragma unroll
-      for (int j = 0; j < FM; ++j) acc[i][j] = E::mma(fb[ks][i], fa[ks][j], acc[i][j]);
+      for (int j = 0; j < FM; ++j) {
+        if constexpr (E::CH == 16) acc[i][j] = E::mma2(fb[0][i], fb[1][i], fa[0][j], fa[1][j], acc[i][j]);
+        else acc[i][j] = E::mma(fb[ks][i], fa[ks][j], acc[i][j]);
+      }
 }
 // float32's instructions are slow enough (16 to a bf16 one's work) that blocks
 // without outputs are worth a branch: dw of 641 x 24 x 16 28 -> 9 us, with the
@@ -314,7 +426,9 @@ __device__ __forceinline__ void mma_half(const typename E::Frag (&fa)[2][FM], co
 template <typename E, int FM, int FN>
 __device__ __forceinline__ void mma_live(const typename E::Frag (&fa)[2][FM], const typename E::Frag (&fb)[2][FN], f32x16 (&acc)[FN][FM],
                                          int live_m, int live_n) {
-  if (E::CH == 8 || (live_m >= FM && live_n >= FN)) {
+  if constexpr (E::CH > 4) {
+    mma_half<E>(fa, fb, acc);
+  } else if (live_m >= FM && live_n >= FN) {
     mma_half<E>(fa, fb, acc);
   } else {
 #pragma unroll
@@ -354,20 +468,22 @@ __device__ __forceinline__ void meet() {
 // float32, where 32 columns are one and the matrix instructions are what costs,
 // every second one, so that an edge with half its columns or fewer keeps all
 // four waves at work (14352 x 2664 x 56: forward 78 -> 67 us, dw 96 -> 60).
-template <typename T, bool TA, bool TB>
+template <typename T, typename O, int MODE, bool TA, bool TB>
 __global__ void __launch_bounds__(256, 2) linear_tile_kernel(const LinearParams p) {
-  typedef Tile<T, TA, TB, 128, 128, 4> Tl;
+  typedef Tile<T, MODE, TA, TB, 128, 128, 4> Tl;
   typedef Elem<T> E;
   __shared__ __align__(1024) T lds[2 * Tl::kStage];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  constexpr int kStep = sizeof(T) == 2 ? 32 : 64;
+  constexpr int kStep = sizeof(T) == 4 ? 64 : 32;
   const int wm = (wave >> 1) * (96 - kStep), wn = (wave & 1) * (96 - kStep);
   const Tl t(p, wave, lane);
-  float bias[8];  // of the lane's columns in linear_out, here so that it has arrived by then
-  linear_bias(p, t.n0 + wn + linear_col<kStep>(lane & 7), bias);
+  const int n0 = t.n0 + (MODE == GATED && kStep == 32 ? wn / 2 : wn);  // the wave's first column of the output
+  // of the lane's columns in linear_out, here so that they have arrived by then
+  const Cols<MODE> cols(p, n0 + linear_col<kStep>(lane & (MODE == GATED ? 3 : 7)));
   f32x16 acc[2][2];
   acc_zero(acc);
-  const int live_m = (p.M - t.m0 - wm + kStep - 1) / kStep, live_n = (p.N - t.n0 - wn + kStep - 1) / kStep;  // blocks with outputs
+  // blocks with outputs
+  const int live_m = (p.M - t.m0 - wm + kStep - 1) / kStep, live_n = MODE == GATED ? (p.N > n0 ? 2 : 0) : (p.N - n0 + kStep - 1) / kStep;
   if (t.kt0 < t.kt1) t.fetch(p, lds, t.kt0, wave);
   for (int kt = t.kt0; kt < t.kt1; ++kt) {
     wait_loads();  // of this stage, and the last one's fragments, before anyone refills its buffer
@@ -392,7 +508,7 @@ __global__ void __launch_bounds__(256, 2) linear_tile_kernel(const LinearParams 
   }
   __syncthreads();
   static_assert(4 * 32 * 68 * 4 <= (int)sizeof(lds), "the bands fit the stages");
-  linear_out<T, kStep>(p, acc, bias, reinterpret_cast<float*>(lds) + wave * 32 * 68, t.m0 + wm, t.n0 + wn, t.share, lane);
+  linear_out<O, MODE, kStep>(p, acc, cols, reinterpret_cast<float*>(lds) + wave * 32 * 68, t.m0 + wm, n0, t.share, lane);
 }
 
 // ---- the large tile: 256 x BN, eight waves, one workgroup a compute unit ----
@@ -416,18 +532,18 @@ __global__ void __launch_bounds__(256, 2) linear_tile_kernel(const LinearParams 
 //     lets the early group read it: the late group at the end of its last
 //     reading half step before, the early one at the end of its last
 //     multiplying one.
-template <typename T, bool TA, bool TB, int BN, int WM, int WN>
+template <typename T, typename O, int MODE, bool TA, bool TB, int BN, int WM, int WN>
 __global__ void __launch_bounds__(512) linear_large_kernel(const LinearParams p) {
   static_assert(WM * WN == 8, "eight waves");
-  typedef Tile<T, TA, TB, 256, BN, 8> Tl;
+  typedef Tile<T, MODE, TA, TB, 256, BN, 8> Tl;
   typedef Elem<T> E;
   constexpr int TM = 256 / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
   __shared__ __align__(1024) T lds[2 * Tl::kStage];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = (wave / WN) * TM, wn = (wave % WN) * TN;
   const Tl t(p, wave, lane);
-  float bias[8];
-  linear_bias(p, t.n0 + wn + linear_col<32>(lane % (TN / 8)), bias);
+  const int n0 = t.n0 + (MODE == GATED ? wn / 2 : wn);
+  const Cols<MODE> cols(p, n0 + linear_col<32>(lane % ((MODE == GATED ? TN / 2 : TN) / 8)));
   f32x16 acc[FN][FM];
   acc_zero(acc);
   const bool late = wave >= 4;
@@ -461,26 +577,42 @@ __global__ void __launch_bounds__(512) linear_large_kernel(const LinearParams p)
   if (!late) meet();
   constexpr int kWave = 32 * (TN + 4);  // floats of a wave's band
   static_assert(8 * kWave * 4 <= (int)sizeof(lds), "the bands fit the stages");
-  linear_out<T, 32>(p, acc, bias, reinterpret_cast<float*>(lds) + wave * kWave, t.m0 + wm, t.n0 + wn, t.share, lane);
+  linear_out<O, MODE, 32>(p, acc, cols, reinterpret_cast<float*>(lds) + wave * kWave, t.m0 + wm, n0, t.share, lane);
 }
 
 // Joins the shares of a split contraction, in order, and finishes the output.
-template <typename T>
+template <typename T, int MODE>
 __global__ void __launch_bounds__(256) linear_join_kernel(const LinearParams p) {
   const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, n = (int64_t)p.M * p.N;
   if (e >= n) return;
-  float bias[4], v[4] = {0.f, 0.f, 0.f, 0.f};
-  linear_bias(p, (int)(e % p.N), bias);
-  Vec<T, 4> res;
-  if (p.residual) res.load(static_cast<const T*>(p.residual) + e);
-#pragma unroll 8
-  for (int k = 0; k < p.splits; ++k) {
-    Vec<float, 4> s;
-    s.load(p.part + k * n + e);
+  const int m = (int)(e / p.N), col = (int)(e % p.N);
+  float bias[4], more[4], v[4] = {0.f, 0.f, 0.f, 0.f};
+  linear_cols(p, p.bias, col, bias);
+  if constexpr (MODE == GATED) {
+    linear_cols(p, p.bias2, col, more);
+    float u[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = 0; k < p.splits; ++k) {
+      Vec<float, 4> s, t;
+      s.load(p.part + 2 * k * n + e);
+      t.load(p.part + (2 * k + 1) * n + e);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] += s.get(j);
+      for (int j = 0; j < 4; ++j) v[j] += s.get(j), u[j] += t.get(j);
+    }
+    gated_finish<T>(p, e, bias, more, v, u);
+  } else {
+    if constexpr (MODE == SCALED) linear_cols(p, p.sw, col, more);
+    Vec<T, 4> res;
+    if (p.residual) res.load(static_cast<const T*>(p.residual) + e);
+#pragma unroll 8
+    for (int k = 0; k < p.splits; ++k) {
+      Vec<float, 4> s;
+      s.load(p.part + k * n + e);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += s.get(j);
+    }
+    linear_finish<T, MODE>(p, m, e, bias, more, res, v);
   }
-  linear_finish(p, e, bias, res, v);
 }
 
 // ---- few rows ----
@@ -491,66 +623,87 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinearParams p) 
 // end a load gives zeros; with pointers and a branch around the load, as a first
 // form had it, 64 x 4096 x 4096 took 26.3 us against 20.2, in float32 49.4
 // against 37.7), and join their sums through LDS in order.
-template <typename T, int MT>
+// GATED: the same columns of both weights; 8-bit: two instructions a chunk.
+template <typename T, typename O, int MODE, int MT>
 __global__ void __launch_bounds__(512) linear_rows_kernel(const LinearParams p) {
+  constexpr int NB = MODE == GATED ? 2 : 1;
   constexpr int CH = Elem<T>::CH, KS = 4 * CH;  // contraction elements of a turn (a chunk a lane)
   constexpr int U = 4;  // (8 turns: 64 x 4096 x 4096 20.2 us either way, 1 x 768 x 1536 2.95 -> 3.4)
-  __shared__ float red[8][MT][256];
+  __shared__ float red[8][NB][MT][256];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, kq = (lane >> 4) * CH;
   const int n0 = blockIdx.x * 16;
   // (16 rows of W, or 64 of x, are at most 2^28 bytes)
   const auto wr = make_rsrc(static_cast<const T*>(p.b) + (int64_t)n0 * p.ldb, 0x7fffffffu), xr = make_rsrc(p.a, 0x7fffffffu);
+  const auto wr2 = make_rsrc(static_cast<const T*>(NB > 1 ? p.b2 : p.b) + (int64_t)n0 * p.ldb, 0x7fffffffu);
   const uint32_t w = (uint32_t)((min(n0 + i, p.N - 1) - n0) * (int)p.ldb + kq) * (uint32_t)sizeof(T);
   uint32_t x[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) x[t] = (uint32_t)(min(t * 16 + i, p.M - 1) * (int)p.lda + kq) * (uint32_t)sizeof(T);
-  f32x4v acc[MT];
+  f32x4v acc[NB][MT];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) acc[t] = f32x4v{0.f, 0.f, 0.f, 0.f};
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[b][t] = f32x4v{0.f, 0.f, 0.f, 0.f};
   for (int k0 = wave * KS; k0 < p.K; k0 += U * 8 * KS) {
-    u32x4 wv[U], xv[U][MT];
+    u32x4 wv[U][NB], xv[U][MT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = k0 + u * 8 * KS;
       const uint32_t at = k + kq < p.K ? (uint32_t)k * (uint32_t)sizeof(T) : kDrop;
-      wv[u] = __builtin_amdgcn_raw_buffer_load_b128(wr, (int)(w + at), 0, 0);
+      wv[u][0] = __builtin_amdgcn_raw_buffer_load_b128(wr, (int)(w + at), 0, 0);
+      if constexpr (NB > 1) wv[u][1] = __builtin_amdgcn_raw_buffer_load_b128(wr2, (int)(w + at), 0, 0);
 #pragma unroll
       for (int t = 0; t < MT; ++t) xv[u][t] = __builtin_amdgcn_raw_buffer_load_b128(xr, (int)(x[t] + at), 0, 0);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        if constexpr (sizeof(T) == 2) {
-          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wv[u]), __builtin_bit_cast(bf16x8, xv[u][t]), acc[t],
-                                                           0, 0, 0);
-        } else {
-          const f32x4v wf = __builtin_bit_cast(f32x4v, wv[u]), xf = __builtin_bit_cast(f32x4v, xv[u][t]);
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[j], xf[j], acc[t], 0, 0, 0);
+        for (int t = 0; t < MT; ++t) {
+          if constexpr (sizeof(T) == 2) {
+            acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wv[u][b]), __builtin_bit_cast(bf16x8, xv[u][t]),
+                                                                acc[b][t], 0, 0, 0);
+          } else if constexpr (sizeof(T) == 1) {
+            typedef long i64x2 __attribute__((ext_vector_type(2)));
+            const i64x2 wf = __builtin_bit_cast(i64x2, wv[u][b]), xf = __builtin_bit_cast(i64x2, xv[u][t]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(wf[j], xf[j], acc[b][t], 0, 0, 0);
+          } else {
+            const f32x4v wf = __builtin_bit_cast(f32x4v, wv[u][b]), xf = __builtin_bit_cast(f32x4v, xv[u][t]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[j], xf[j], acc[b][t], 0, 0, 0);
+          }
         }
-      }
   }
   // lane: output row lane%16, columns 4·(lane/16) onwards
 #pragma unroll
-  for (int t = 0; t < MT; ++t) *reinterpret_cast<f32x4v*>(&red[wave][t][lane * 4]) = acc[t];
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) *reinterpret_cast<f32x4v*>(&red[wave][b][t][lane * 4]) = acc[b][t];
   __syncthreads();
   if (threadIdx.x < MT * 32) {
     const int t = threadIdx.x >> 5, l = threadIdx.x & 15, half = (threadIdx.x >> 4) & 1, m = t * 16 + l, n = n0 + half * 8;
-    float v[8];
+    float v[NB][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    for (int b = 0; b < NB; ++b) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+      for (int j = 0; j < 8; ++j) v[b][j] = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += red[k][t][(half * 32 + (j >> 2) * 16 + l) * 4 + (j & 3)];
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[b][j] += red[k][b][t][(half * 32 + (j >> 2) * 16 + l) * 4 + (j & 3)];
+    }
     if (m < p.M && n < p.N) {
       const int64_t at = (int64_t)m * p.N + n;
-      float bias[8];
-      linear_bias(p, n, bias);
-      Vec<T, 8> res;
-      if (p.residual) res.load(static_cast<const T*>(p.residual) + at);
-      linear_finish(p, at, bias, res, v);
+      const Cols<MODE> cols(p, n);
+      if constexpr (MODE == GATED) {
+        gated_finish<O>(p, at, cols.bias, cols.more, v[0], v[1]);
+      } else {
+        Vec<O, 8> res;
+        if (p.residual) res.load(static_cast<const O*>(p.residual) + at);
+        linear_finish<O, MODE>(p, m, at, cols.bias, cols.more, res, v[0]);
+      }
     }
   }
 }
@@ -604,6 +757,66 @@ __global__ void __launch_bounds__(256) linear_grad_kernel(const LinearGradParams
     for (int c = threadIdx.x; c < 512; c += 256) {
       const int col = blockIdx.x * 512 + c;
       if (col < p.N) p.part[(int64_t)blockIdx.y * p.N + col] = ((red[0][c] + red[1][c]) + red[2][c]) + red[3][c];
+    }
+  }
+}
+
+// The gated pair's: with a = act(g) and the pair's sums g and u,
+//   dg = dout·u·act'(g),  du = dout·a,
+// side by side in rows of 2N, so that dx is one product over both and dW one
+// product with 2N rows; and both columns' sums over a run of rows.
+struct GatedGradParams {
+  const void* dout;  // [M][N]
+  const float* pre;  // [2][M][N]
+  void* dp;          // [M][2N] or null
+  float2* part;      // [chunks][N] or null
+  int M, N, chunk;
+};
+
+template <typename T, int ACT>
+__global__ void __launch_bounds__(256) gated_grad_kernel(const GatedGradParams p) {
+  __shared__ float2 red[4][512];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n = (blockIdx.x * 64 + lane) * 8;
+  const int m0 = blockIdx.y * p.chunk, m1 = min(p.M, m0 + p.chunk);
+  float sg[8], su[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sg[j] = su[j] = 0.f;
+  if (n < p.N) {
+#pragma unroll 2
+    for (int m = m0 + wave; m < m1; m += 4) {
+      const int64_t at = (int64_t)m * p.N + n;
+      Vec<T, 8> dy;
+      Vec<float, 8> g, u;
+      dy.load(static_cast<const T*>(p.dout) + at);
+      g.load(p.pre + at);
+      u.load(p.pre + (int64_t)p.M * p.N + at);
+      float dg[8], du[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float f, d;
+        act_fd<ACT>(g.get(j), f, d);
+        dg[j] = dy.get(j) * u.get(j) * d;
+        du[j] = dy.get(j) * f;
+        sg[j] += dg[j], su[j] += du[j];
+      }
+      if (p.dp) {
+        T* const to = static_cast<T*>(p.dp) + (int64_t)m * 2 * p.N + n;
+        storeV<8>(to, dg);
+        storeV<8>(to + p.N, du);
+      }
+    }
+  }
+  if (p.part) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) red[wave][lane * 8 + j] = make_float2(sg[j], su[j]);
+    __syncthreads();
+    for (int c = threadIdx.x; c < 512; c += 256) {
+      const int col = blockIdx.x * 512 + c;
+      float2 s = red[0][c];
+#pragma unroll
+      for (int k = 1; k < 4; ++k) col_add(s, red[k][c]);
+      if (col < p.N) p.part[(int64_t)blockIdx.y * p.N + col] = s;
     }
   }
 }

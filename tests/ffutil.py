@@ -66,3 +66,69 @@ def within(name, got, want, tol):
     worst = float((d / tol.clamp(min=1e-300)).max()) if d.numel() else 0.0
     print("%s: worst %.3f of the tolerance" % (name, worst), flush=True)
     assert not bool(bad.any()), (name, worst)
+
+
+# Products.  A float32 sum of K products errs by about sqrt(K)·2^-24 of its scale,
+# 4e-6 at K = 4096: 2e-4 of the largest value and 2e-5 in the L2 norm.  bfloat16
+# outputs carry one rounding (2^-9/sqrt(3) = 1.1e-3 in L2): 1e-2 and 3e-3;
+# gradients behind an activation one more, of what enters the products: 4e-3.
+TOL = {"f32": (2e-4, 2e-5), "bf16": (1e-2, 3e-3), "bf16 grad": (2e-2, 4e-3)}
+
+
+def close(name, got, want, kind):
+    assert got.shape == want.shape, (name, got.shape, want.shape)
+    assert bool(got.isfinite().all()), name
+    d = got.double() - want
+    top, norm = float(want.abs().max()), float(want.norm())
+    a, b = float(d.abs().max()) / (top or 1.0), float(d.norm()) / (norm or 1.0)
+    print("%s: max %.2e l2 %.2e" % (name, a, b), flush=True)
+    assert a <= TOL[kind][0] and b <= TOL[kind][1], (name, a, b)
+
+
+def mm(a, b):
+    """a·bᵀ in float64."""
+    return torch().matmul(a.double(), b.double().t().contiguous())
+
+
+def gated_ref(x, wg, wu, bg, bu, act, dout=None):
+    """out, g, u and, for dout, the gradients."""
+    g, u = mm(x, wg), mm(x, wu)
+    if bg is not None:
+        g = g + bg.double()
+    if bu is not None:
+        u = u + bu.double()
+    a, da = act64(g, act)
+    if dout is None:
+        return a * u, g, u
+    dg, du = dout.double() * u * da, dout.double() * a
+    t = lambda v: v.t().contiguous()  # noqa: E731
+    return a * u, g, u, dict(dx=mm(dg, t(wg)) + mm(du, t(wu)), dw_gate=mm(t(dg), t(x)), dw_up=mm(t(du), t(x)),
+                             db_gate=dg.sum(0), db_up=du.sum(0))
+
+
+def finish_ref(u, b, act, res):
+    u = act64(u if b is None else u + b.double(), act)[0]
+    return u if res is None else u + res.double()
+
+
+def rows8(v):
+    """Rows in e4m3 with their scales."""
+    t = torch()
+    scale = (v.float().abs().amax(1) / 448).clamp(min=1e-30)
+    return (v.float() / scale[:, None]).to(t.float8_e4m3fn), scale
+
+
+def weights4(N, K, group, seed, zero, scale_type="bf16", device="cuda:0"):
+    """Packed weights, scale, zero, and what they stand for in float64."""
+    t = torch()
+    g = t.Generator(device="cpu")
+    g.manual_seed(seed)
+    G = -(-K // group)
+    q = t.randint(0, 16, (N, K), generator=g, dtype=t.uint8)
+    scale = (0.05 + 0.2 * t.rand(N, G, generator=g)).to(dtype_of(scale_type)) * (K ** -0.5)
+    scale = scale.to(dtype_of(scale_type))
+    z = t.randint(0, 16, (N, G), generator=g, dtype=t.uint8) if zero else None
+    at = t.arange(K) // group
+    w = (q.double() - (8.0 if z is None else z.double()[:, at])) * scale.double()[:, at]
+    packed = q[:, 0::2] | (q[:, 1::2] << 4)
+    return packed.contiguous().to(device), scale.to(device), None if z is None else z.to(device), w.to(device)

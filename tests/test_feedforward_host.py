@@ -9,7 +9,7 @@ import pytest
 import selective_state_space_mamba_amd as ms
 from selective_state_space_mamba_amd import _binding as E
 
-from ffutil import maker, rms_grads, rms_ref
+from ffutil import gated_ref, maker, rms_grads, rms_ref
 
 FAKE = 0x100000  # 16-byte aligned stand-in pointer: every call below fails validation first
 
@@ -91,3 +91,118 @@ def test_rms_reference_gradients_against_differences():
         num = (loss(**dict(v, **{k: v[k] + eps * d})) - loss(**dict(v, **{k: v[k] - eps * d}))) / (2 * eps)
         want = float((g * d).sum())
         assert abs(num - want) <= 1e-7 * max(1.0, abs(want)), (k, num, want)
+
+
+def linear_dims(**kw):
+    base = dict(rows=100, in_dim=64, out_dim=32, dtype=ms.DTYPE_BF16)
+    base.update(kw)
+    return ms.make_linear_dims(base.pop("rows"), base.pop("in_dim"), base.pop("out_dim"), base.pop("dtype"), **base)
+
+
+LINEAR_BAD = [(dict(rows=0), E.MAMBA_ERR_INVALID), (dict(in_dim=0), E.MAMBA_ERR_INVALID), (dict(out_dim=-8), E.MAMBA_ERR_INVALID),
+              (dict(dtype=2), E.MAMBA_ERR_INVALID), (dict(act=4), E.MAMBA_ERR_INVALID), (dict(in_dim=12), E.MAMBA_ERR_UNSUPPORTED),
+              (dict(out_dim=20), E.MAMBA_ERR_UNSUPPORTED), (dict(in_dim=(1 << 20) + 16), E.MAMBA_ERR_UNSUPPORTED),
+              (dict(rows=(1 << 29) + 1), E.MAMBA_ERR_UNSUPPORTED)]
+
+
+def test_gated_sizes(lib):
+    assert ms.gated_linear_fwd_workspace_bytes(linear_dims()) == 0
+    assert ms.gated_linear_fwd_workspace_bytes(linear_dims(rows=8, in_dim=65536)) == 0  # few rows: no scratch
+    split = ms.gated_linear_fwd_workspace_bytes(linear_dims(rows=200, in_dim=65536))
+    assert split >= 2 * 200 * 2 * 32 * 4  # both products of two shares at least
+    assert ms.gated_linear_bwd_workspace_bytes(linear_dims()) >= 100 * 2 * 32 * 2
+    for bad, _ in LINEAR_BAD + [(dict(out_dim=(1 << 19) + 8), 0)]:
+        for query in (ms.gated_linear_fwd_workspace_bytes, ms.gated_linear_bwd_workspace_bytes):
+            with pytest.raises(ms.MambaError):
+                query(linear_dims(**bad))
+
+
+def test_gated_refusals(lib):
+    def fwd(d, x=FAKE, wg=FAKE, wu=FAKE, bg=None, bu=None, out=FAKE, pre=None):
+        return lib.mamba_gated_linear_fwd(x, wg, wu, bg, bu, d and ctypes.byref(d), out, pre, None)
+
+    def bwd(d, x=FAKE, wg=FAKE, wu=FAKE, pre=FAKE, dout=FAKE, dx=FAKE, dwg=FAKE, dwu=FAKE, dbg=FAKE, dbu=FAKE):
+        return lib.mamba_gated_linear_bwd(x, wg, wu, pre, dout, d and ctypes.byref(d), dx, dwg, dwu, dbg, dbu, None)
+
+    for call, needed in ((fwd, ("x", "wg", "wu", "out")), (bwd, ("x", "wg", "wu", "pre", "dout", "dwg", "dwu", "dbg", "dbu"))):
+        assert call(None) == E.MAMBA_ERR_INVALID
+        for miss in needed:  # (of a pair of outputs, one alone)
+            assert call(linear_dims(), **{miss: None}) == E.MAMBA_ERR_INVALID, miss
+        for bad, code in LINEAR_BAD + [(dict(out_dim=(1 << 19) + 8), E.MAMBA_ERR_UNSUPPORTED)]:
+            assert call(linear_dims(**bad)) == code, bad
+    assert bwd(linear_dims(), dx=None, dwg=None, dwu=None, dbg=None, dbu=None) == E.MAMBA_ERR_INVALID
+    for call, odd in ((fwd, ("x", "wg", "wu", "out", "pre")), (bwd, ("x", "wg", "wu", "pre", "dout", "dx", "dwg", "dwu"))):
+        for k in odd:
+            assert call(linear_dims(), **{k: FAKE + 8}) == E.MAMBA_ERR_UNSUPPORTED, k
+    for call, odd in ((fwd, ("bg", "bu")), (bwd, ("dbg", "dbu"))):
+        for k in odd:
+            assert call(linear_dims(), **{k: FAKE + 2}) == E.MAMBA_ERR_UNSUPPORTED, k
+    assert fwd(linear_dims(rows=200, in_dim=65536)) == E.MAMBA_ERR_WORKSPACE
+    need = ms.gated_linear_fwd_workspace_bytes(linear_dims(rows=200, in_dim=65536))
+    assert fwd(linear_dims(rows=200, in_dim=65536, workspace=FAKE, workspace_bytes=need - 1)) == E.MAMBA_ERR_WORKSPACE
+    assert bwd(linear_dims()) == E.MAMBA_ERR_WORKSPACE
+    need = ms.gated_linear_bwd_workspace_bytes(linear_dims())
+    assert bwd(linear_dims(workspace=FAKE, workspace_bytes=need - 1)) == E.MAMBA_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu"])
+def test_gated_reference_gradients_against_differences(act):
+    n = maker(9, "cpu")
+    v = dict(x=n((5, 12)).double(), wg=n((7, 12)).double(), wu=n((7, 12)).double(), bg=n((7,)).double(), bu=n((7,)).double())
+    dout = n((5, 7)).double()
+    _, g, _, grads = gated_ref(**v, act=act, dout=dout)
+    eps = 1e-6
+    assert float(g.abs().min()) > 100 * eps  # no step crosses relu's kink
+    for k, gk in (("x", "dx"), ("wg", "dw_gate"), ("wu", "dw_up"), ("bg", "db_gate"), ("bu", "db_up")):
+        d = n(tuple(v[k].shape)).double()
+        f = lambda s: float((gated_ref(**dict(v, **{k: v[k] + s * d}), act=act)[0] * dout).sum())  # noqa: E731
+        num = (f(eps) - f(-eps)) / (2 * eps)
+        want = float((grads[gk] * d).sum())
+        assert abs(num - want) <= 1e-6 * max(1.0, abs(want)), (k, num, want)
+
+
+def test_quant_sizes_and_refusals(lib):
+    assert ms.linear_q8_workspace_bytes(linear_dims()) == 0
+    assert ms.linear_q8_workspace_bytes(linear_dims(rows=8, in_dim=65536)) == 0
+    need = ms.linear_q8_workspace_bytes(linear_dims(rows=200, in_dim=65536))
+    assert need > 0
+
+    def q8(d, x=FAKE, sx=FAKE, w=FAKE, sw=FAKE, b=None, res=None, out=FAKE):
+        return lib.mamba_linear_q8(x, sx, w, sw, b, res, d and ctypes.byref(d), out, None)
+
+    assert q8(None) == E.MAMBA_ERR_INVALID
+    for miss in ("x", "sx", "w", "sw", "out"):
+        assert q8(linear_dims(), **{miss: None}) == E.MAMBA_ERR_INVALID
+    for bad, code in LINEAR_BAD + [(dict(in_dim=72), E.MAMBA_ERR_UNSUPPORTED)]:
+        assert q8(linear_dims(**bad)) == code, bad
+        with pytest.raises(ms.MambaError):
+            ms.linear_q8_workspace_bytes(linear_dims(**bad))
+    for odd in ("x", "w", "res", "out"):
+        assert q8(linear_dims(), **{odd: FAKE + 8}) == E.MAMBA_ERR_UNSUPPORTED
+    for odd in ("sx", "sw", "b"):
+        assert q8(linear_dims(), **{odd: FAKE + 2}) == E.MAMBA_ERR_UNSUPPORTED
+    assert q8(linear_dims(rows=200, in_dim=65536)) == E.MAMBA_ERR_WORKSPACE
+    assert q8(linear_dims(rows=200, in_dim=65536, workspace=FAKE, workspace_bytes=need - 1)) == E.MAMBA_ERR_WORKSPACE
+
+    def dims4(**kw):
+        base = dict(rows=4, in_dim=64, out_dim=32, group=64, dtype=ms.DTYPE_BF16)
+        base.update(kw)
+        return ms.make_q4_dims(base.pop("rows"), base.pop("in_dim"), base.pop("out_dim"), base.pop("group"), base.pop("dtype"), **base)
+
+    def q4(d, x=FAKE, w=FAKE, s=FAKE, z=None, b=None, res=None, out=FAKE):
+        return lib.mamba_linear_q4(x, w, s, z, b, res, d and ctypes.byref(d), out, None)
+
+    assert q4(None) == E.MAMBA_ERR_INVALID
+    for miss in ("x", "w", "s", "out"):
+        assert q4(dims4(), **{miss: None}) == E.MAMBA_ERR_INVALID
+    for bad in (dict(rows=0), dict(in_dim=0), dict(out_dim=-8), dict(group=0), dict(group=-32), dict(dtype=2), dict(scale_dtype=2),
+                dict(act=-1)):
+        assert q4(dims4(**bad)) == E.MAMBA_ERR_INVALID, bad
+    for bad in (dict(in_dim=48), dict(out_dim=20), dict(group=16), dict(group=96), dict(group=160), dict(in_dim=(1 << 20) + 32),
+                dict(out_dim=(1 << 20) + 8), dict(rows=(1 << 20) + 1), dict(group=(1 << 20) + 128)):
+        assert q4(dims4(**bad)) == E.MAMBA_ERR_UNSUPPORTED, bad
+    for odd in ("x", "w", "res", "out"):
+        assert q4(dims4(), **{odd: FAKE + 8}) == E.MAMBA_ERR_UNSUPPORTED
+    assert q4(dims4(), s=FAKE + 1) == E.MAMBA_ERR_UNSUPPORTED
+    assert q4(dims4(scale_dtype=ms.DTYPE_F32), s=FAKE + 2) == E.MAMBA_ERR_UNSUPPORTED
+    assert q4(dims4(), b=FAKE + 2) == E.MAMBA_ERR_UNSUPPORTED
