@@ -565,7 +565,9 @@ MAMBA_API int mamba_gated_linear_bwd(const void* x, const void* w_gate, const vo
  *
  *   out[m][n] = act(x_scale[m]·w_scale[n]·Σ_k x[m][k]·weight[n][k] + bias[n]) + residual[m][n]
  * with x [M][K] and weight [N][K] in e4m3 (as mamba_rms_norm_q8 writes it) and
- * a float32 scale for each row of either.  Sums are float32, products exact.
+ * a float32 scale for each row of either.  Products are exact; sums are float32
+ * where dtype is, and otherwise those of the 8-bit matrix instructions, which
+ * are off by 1.3e-5 of their scale, far below a bfloat16 output's rounding.
  * In the mamba_linear_dims dtype is that of residual and out; K is a multiple
  * of 16. */
 
@@ -589,10 +591,10 @@ MAMBA_API int mamba_linear_q8(const void* x, const float* x_scale, const void* w
  *
  *   out[m][n] = act(Σ_k (q[n][k] - zero[n][k/group])·scale[n][k/group]·x[m][k] + bias[n]) + residual[m][n]
  * for few rows (a token of each of some sequences): the weights are read once
- * for 64 rows.  Weights are not rounded on the way: products are exact, sums
+ * for 16 or 32 rows.  Weights are not rounded on the way: products are exact, sums
  * float32.  A row of x with an infinity or a NaN is NaN throughout. */
 typedef struct {
-  int64_t rows;        /* M in 1..2^20 */
+  int64_t rows;        /* M in 1..2^18 */
   int64_t in_dim;      /* K in 32..2^20, a multiple of 32 */
   int64_t out_dim;     /* N in 8..2^20, a multiple of 8 */
   int64_t group;       /* 32, 64 or a multiple of 128, up to 2^20; K need not be a multiple of it */

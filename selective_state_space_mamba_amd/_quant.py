@@ -70,16 +70,16 @@ def linear_q8(x, x_scale, weight, w_scale, bias=None, residual=None, *, act=ACT_
     check_f32(x, xs[:-1], ("x_scale", x_scale))
     check_f32(x, (N,), ("w_scale", w_scale), ("bias", bias))
     shape = xs[:-1] + wsh[:1]
-    given = out if out is not None else residual
-    if given is None:
-        out = torch.empty(shape, dtype=torch.bfloat16 if dtype is None else dtype, device=x.device)
-    elif dtype is not None and given.dtype is not dtype:
-        raise TypeError("out and residual must be %s, got %s" % (dtype, given.dtype))
-    elif out is None:
-        out = torch.empty(shape, dtype=given.dtype, device=x.device)
-    dt = _b._dtype_code(out)
-    for name, t in (("out", out), ("residual", residual)):
-        _b._check(t, name, shape, out.dtype, x.device)
+    given = residual if out is None else out
+    if given is not None:
+        dt = _b._dtype_code(given)
+        if dtype is not None and given.dtype is not dtype:
+            raise TypeError("out and residual must be %s, got %s" % (dtype, given.dtype))
+        for name, t in (("out", out), ("residual", residual)):
+            _b._check(t, name, shape, given.dtype, x.device)
+    if out is None:
+        out = x.new_empty(shape, dtype=torch.bfloat16 if dtype is None else dtype) if given is None else torch.empty_like(given)
+        dt = _b._dtype_code(out)
     dims = make_linear_dims(M, K, N, dt, act=act)
     workspace = use_workspace(dims, _q8_bytes(M, K, N), workspace, x)
     done(_b.load_library().mamba_linear_q8(x.data_ptr(), x_scale.data_ptr(), weight.data_ptr(), w_scale.data_ptr(),

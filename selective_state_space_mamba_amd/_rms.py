@@ -100,7 +100,7 @@ def rms_norm_fwd(x, weight=None, residual=None, *, eps=1e-5, out=None, added=Non
     else:
         check_like(x, shape, ("out", out))
     if rstd is None:
-        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = x.new_empty(shape[:-1], dtype=torch.float32)
     else:
         check_f32(x, shape[:-1], ("rstd", rstd))
     done(_b.load_library().mamba_rms_norm_fwd(x.data_ptr(), ptr(residual), ptr(weight), ctypes.byref(dims),
@@ -120,11 +120,11 @@ def rms_norm_q8(x, weight=None, residual=None, *, eps=1e-5, out=None, scale=None
     shape, dims, added = _fwd(x, weight, residual, eps, added)
     raw = launch_stream(x, stream)
     if out is None:
-        out = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
+        out = torch.empty_like(x, dtype=torch.float8_e4m3fn)
     else:
         _b._check(out, "out", shape, torch.float8_e4m3fn, x.device)
     if scale is None:
-        scale = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+        scale = x.new_empty(shape[:-1], dtype=torch.float32)
     else:
         check_f32(x, shape[:-1], ("scale", scale))
     done(_b.load_library().mamba_rms_norm_q8(x.data_ptr(), ptr(residual), ptr(weight), ctypes.byref(dims),

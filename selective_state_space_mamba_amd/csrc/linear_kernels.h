@@ -223,7 +223,11 @@ struct Elem<float> {
 };
 
 // e4m3: a half stage is one instruction of 64 contraction elements, of which a
-// lane gives the 32 of its two chunks, on both sides the same.
+// lane gives the 32 of its two chunks, on both sides the same.  The 8-bit
+// instructions add their products with fewer bits than float32 has (measured,
+// both of them: 1.3e-5 of the result in the L2 norm, whatever K), a two
+// hundredth of a bfloat16 output's rounding.  float32 outputs therefore take
+// the elements as bfloat16, which holds them, at half the rate (1e-7).
 template <>
 struct Elem<uint8_t> {
   static constexpr int BK = 128;
@@ -235,6 +239,19 @@ struct Elem<uint8_t> {
     const i32x8 a = {(int)a0[0], (int)a0[1], (int)a0[2], (int)a0[3], (int)a1[0], (int)a1[1], (int)a1[2], (int)a1[3]};
     const i32x8 b = {(int)b0[0], (int)b0[1], (int)b0[2], (int)b0[3], (int)b1[0], (int)b1[1], (int)b1[2], (int)b1[3]};
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);  // (no block scales)
+  }
+  // Eight elements, the h-th half of a chunk, as bfloat16.
+  __device__ static __forceinline__ bf16x8 wide(const Frag& f, int h) {
+    bf16x8 v;
+#ifdef __HIP_DEVICE_COMPILE__
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const auto lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[2 * h + j], 1.0f, false);
+      const auto hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(f[2 * h + j], 1.0f, true);
+      v[4 * j] = lo[0], v[4 * j + 1] = lo[1], v[4 * j + 2] = hi[0], v[4 * j + 3] = hi[1];
+    }
+#endif
+    return v;
   }
 };
 
@@ -408,8 +425,24 @@ struct Tile {
   }
 };
 
-template <typename E, int FM, int FN>
+// WIDE: 8-bit elements taken as bfloat16
+template <typename E, bool WIDE, int FM, int FN>
 __device__ __forceinline__ void mma_half(const typename E::Frag (&fa)[2][FM], const typename E::Frag (&fb)[2][FN], f32x16 (&acc)[FN][FM]) {
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      bf16x8 a[FM], b[FN];
+#pragma unroll
+      for (int j = 0; j < FM; ++j) a[j] = E::wide(fa[q >> 1][j], q & 1);
+#pragma unroll
+      for (int i = 0; i < FN; ++i) b[i] = E::wide(fb[q >> 1][i], q & 1);
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[i], a[j], acc[i][j], 0, 0, 0);
+    }
+    return;
+  }
 #pragma unroll
   for (int ks = 0; ks < (E::CH == 16 ? 1 : 2); ++ks)
 #pragma unroll
@@ -423,13 +456,13 @@ __device__ __forceinline__ void mma_half(const typename E::Frag (&fa)[2][FM], co
 // float32's instructions are slow enough (16 to a bf16 one's work) that blocks
 // without outputs are worth a branch: dw of 641 x 24 x 16 28 -> 9 us, with the
 // contraction in more shares.
-template <typename E, int FM, int FN>
+template <typename E, bool WIDE, int FM, int FN>
 __device__ __forceinline__ void mma_live(const typename E::Frag (&fa)[2][FM], const typename E::Frag (&fb)[2][FN], f32x16 (&acc)[FN][FM],
                                          int live_m, int live_n) {
   if constexpr (E::CH > 4) {
-    mma_half<E>(fa, fb, acc);
+    mma_half<E, WIDE>(fa, fb, acc);
   } else if (live_m >= FM && live_n >= FN) {
-    mma_half<E>(fa, fb, acc);
+    mma_half<E, false>(fa, fb, acc);
   } else {
 #pragma unroll
     for (int i = 0; i < FN; ++i)
@@ -475,6 +508,7 @@ __global__ void __launch_bounds__(256, 2) linear_tile_kernel(const LinearParams 
   __shared__ __align__(1024) T lds[2 * Tl::kStage];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   constexpr int kStep = sizeof(T) == 4 ? 64 : 32;
+  constexpr bool kWide = sizeof(T) == 1 && sizeof(O) == 4;
   const int wm = (wave >> 1) * (96 - kStep), wn = (wave & 1) * (96 - kStep);
   const Tl t(p, wave, lane);
   const int n0 = t.n0 + (MODE == GATED && kStep == 32 ? wn / 2 : wn);  // the wave's first column of the output
@@ -498,13 +532,13 @@ __global__ void __launch_bounds__(256, 2) linear_tile_kernel(const LinearParams 
     if constexpr (!TA && !TB) {
       Tl::SA::template frags<2, kStep>(la, wm, 1, lane, fa[1]);
       Tl::SB::template frags<2, kStep>(lb, wn, 1, lane, fb[1]);
-      mma_live<E>(fa[0], fb[0], acc, live_m, live_n);
+      mma_live<E, kWide>(fa[0], fb[0], acc, live_m, live_n);
     } else {
-      mma_live<E>(fa[0], fb[0], acc, live_m, live_n);
+      mma_live<E, kWide>(fa[0], fb[0], acc, live_m, live_n);
       Tl::SA::template frags<2, kStep>(la, wm, 1, lane, fa[1]);
       Tl::SB::template frags<2, kStep>(lb, wn, 1, lane, fb[1]);
     }
-    mma_live<E>(fa[1], fb[1], acc, live_m, live_n);
+    mma_live<E, kWide>(fa[1], fb[1], acc, live_m, live_n);
   }
   __syncthreads();
   static_assert(4 * 32 * 68 * 4 <= (int)sizeof(lds), "the bands fit the stages");
@@ -538,6 +572,7 @@ __global__ void __launch_bounds__(512) linear_large_kernel(const LinearParams p)
   typedef Tile<T, MODE, TA, TB, 256, BN, 8> Tl;
   typedef Elem<T> E;
   constexpr int TM = 256 / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;
+  constexpr bool kWide = sizeof(T) == 1 && sizeof(O) == 4;
   __shared__ __align__(1024) T lds[2 * Tl::kStage];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = (wave / WN) * TM, wn = (wave % WN) * TN;
@@ -569,7 +604,7 @@ __global__ void __launch_bounds__(512) linear_large_kernel(const LinearParams p)
       meet();
       if (h == 0 && (!late || kt > t.kt0) && kt + 1 < t.kt1) t.fetch_b(p, lds, kt + 1, wave);
       if (h == 1 && late && kt + 2 < t.kt1) t.fetch_a(p, lds, kt + 2, wave);
-      mma_half<E>(fa, fb, acc);
+      mma_half<E, kWide>(fa, fb, acc);
       if (h == 1 && !late) wait_loads();
       meet();
     }
@@ -664,6 +699,10 @@ __global__ void __launch_bounds__(512) linear_rows_kernel(const LinearParams p) 
           if constexpr (sizeof(T) == 2) {
             acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, wv[u][b]), __builtin_bit_cast(bf16x8, xv[u][t]),
                                                                 acc[b][t], 0, 0, 0);
+          } else if constexpr (sizeof(T) == 1 && sizeof(O) == 4) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              acc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Elem<T>::wide(wv[u][b], j), Elem<T>::wide(xv[u][t], j), acc[b][t], 0, 0, 0);
           } else if constexpr (sizeof(T) == 1) {
             typedef long i64x2 __attribute__((ext_vector_type(2)));
             const i64x2 wf = __builtin_bit_cast(i64x2, wv[u][b]), xf = __builtin_bit_cast(i64x2, xv[u][t]);

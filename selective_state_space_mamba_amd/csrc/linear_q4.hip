@@ -20,26 +20,59 @@ int check(const mamba_q4_dims* g) {
   if (g->rows <= 0 || g->in_dim <= 0 || g->out_dim <= 0 || g->group <= 0) return MAMBA_ERR_INVALID;
   if (g->in_dim % 32 != 0 || g->out_dim % 8 != 0) return MAMBA_ERR_UNSUPPORTED;
   if (g->group != 32 && g->group != 64 && g->group % 128 != 0) return MAMBA_ERR_UNSUPPORTED;
-  if (g->in_dim > (1 << 20) || g->out_dim > (1 << 20) || g->group > (1 << 20) || g->rows > (1 << 20)) return MAMBA_ERR_UNSUPPORTED;
+  if (g->in_dim > (1 << 20) || g->out_dim > (1 << 20) || g->group > (1 << 20) || g->rows > (1 << 18)) return MAMBA_ERR_UNSUPPORTED;
   return MAMBA_OK;
 }
 
-template <typename T, int GS>
+// Row tiles MT and column tiles CT of a workgroup: the least expected time.  A
+// round is a workgroup a compute unit; one of MT x CT tiles takes, against one
+// of 1 x 1, the time below (four tiles of columns more with short groups), and
+// each further round half of its own beside the one before, a third where x is
+// next to nothing (4096 elements of the contraction, 16 or 32 bfloat16 rows, in
+// us: 1 round of 1 x 1, 1 x 2, 1 x 4 tiles 8.1, 9.9, 12.0, of 2 x 1, 2 x 2, 2 x
+// 4 11.6, 13.6, 17.4; 2 rounds of 1 x 1 13.1).  Over 9 weights from 1536 x 768
+// to 16384 x 8192 and 1 to 64 rows, 99 in all, the choice took 0.5 % longer than
+// the best on average, at worst 17 % (one row, 5000 x 2080 in groups of 32, 6.7
+// us against 5.7); tiles of 4 x CT gained nothing on it.
+struct Q4Plan {
+  int mt, ct;
+};
+Q4Plan plan_q4(int64_t M, int64_t N, int64_t group) {
+  const double kTime[2][3] = {{1.0, 1.25, group < 128 ? 2.1 : 1.7}, {1.45, 1.7, group < 128 ? 2.4 : 2.2}};
+  Q4Plan best{1, 1};
+  double least = 1e300;
+  for (int mt = 1; mt <= 2; ++mt)
+    for (int c = 0; c < 3; ++c) {
+      const int64_t wgs = ((M + 16 * mt - 1) / (16 * mt)) * ((N + (16 << c) - 1) / (16 << c)), rounds = (wgs + 255) / 256;
+      const double t = kTime[mt - 1][c] * (1.0 + (M <= 4 ? 0.35 : 0.5) * (double)(rounds - 1));
+      if (t < least) least = t, best = Q4Plan{mt, 1 << c};
+    }
+  return best;
+}
+
+template <typename T, int GS, int MT, int CT>
 void launch(const Q4Params& p, hipStream_t stream) {
-  const unsigned cols = (unsigned)ceil_div(p.N, 16);
-  const int mt = p.M <= 16 ? 1 : p.M <= 32 ? 2 : 4;
-  const dim3 grid(cols, (unsigned)ceil_div(p.M, 16 * mt));
-  constexpr int U = sizeof(T) == 2 ? 2 : 1;
-  if (mt == 1) q4_kernel<T, GS, 1, 1, U><<<grid, 64 * kQ4Waves, 0, stream>>>(p);
-  else if (mt == 2) q4_kernel<T, GS, 2, 1, 1><<<grid, 64 * kQ4Waves, 0, stream>>>(p);
-  else q4_kernel<T, GS, 4, 1, 1><<<grid, 64 * kQ4Waves, 0, stream>>>(p);
+  const dim3 grid((unsigned)ceil_div(p.N, 16 * CT), (unsigned)ceil_div(p.M, 16 * MT));
+  q4_kernel<T, GS, MT, CT><<<grid, 64 * kQ4Waves, 0, stream>>>(p);
+}
+template <typename T, int GS>
+void by_tile(const Q4Params& p, hipStream_t stream) {
+  const Q4Plan pl = plan_q4(p.M, p.N, p.group);
+  switch (pl.mt * 8 + pl.ct) {
+    case 9: launch<T, GS, 1, 1>(p, stream); break;
+    case 10: launch<T, GS, 1, 2>(p, stream); break;
+    case 12: launch<T, GS, 1, 4>(p, stream); break;
+    case 17: launch<T, GS, 2, 1>(p, stream); break;
+    case 18: launch<T, GS, 2, 2>(p, stream); break;
+    default: launch<T, GS, 2, 4>(p, stream);
+  }
 }
 
 template <typename T>
 void by_group(const Q4Params& p, hipStream_t stream) {
-  if (p.group == 32) launch<T, 4>(p, stream);
-  else if (p.group == 64) launch<T, 2>(p, stream);
-  else launch<T, 1>(p, stream);
+  if (p.group == 32) by_tile<T, 4>(p, stream);
+  else if (p.group == 64) by_tile<T, 2>(p, stream);
+  else by_tile<T, 1>(p, stream);
 }
 
 }  // namespace

@@ -199,7 +199,7 @@ def test_quant_sizes_and_refusals(lib):
                 dict(act=-1)):
         assert q4(dims4(**bad)) == E.MAMBA_ERR_INVALID, bad
     for bad in (dict(in_dim=48), dict(out_dim=20), dict(group=16), dict(group=96), dict(group=160), dict(in_dim=(1 << 20) + 32),
-                dict(out_dim=(1 << 20) + 8), dict(rows=(1 << 20) + 1), dict(group=(1 << 20) + 128)):
+                dict(out_dim=(1 << 20) + 8), dict(rows=(1 << 18) + 1), dict(group=(1 << 20) + 128)):
         assert q4(dims4(**bad)) == E.MAMBA_ERR_UNSUPPORTED, bad
     for odd in ("x", "w", "res", "out"):
         assert q4(dims4(), **{odd: FAKE + 8}) == E.MAMBA_ERR_UNSUPPORTED
