@@ -425,10 +425,51 @@ struct Tile {
   }
 };
 
-// WIDE: 8-bit elements taken as bfloat16
+// Eight float32 elements as three bfloat16 terms, 8 bits of the value each: their sum is the value.
+__device__ __forceinline__ void three_terms(const f32x4v& lo, const f32x4v& hi, bf16x8 (&t)[3]) {
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = j < 4 ? lo[j] : hi[j - 4];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    u32x4 w;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = __builtin_amdgcn_perm(__float_as_uint(v[2 * j + 1]), __float_as_uint(v[2 * j]), 0x07060302u);
+    t[k] = __builtin_bit_cast(bf16x8, w);
+    if (k < 2) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] -= __uint_as_float(__float_as_uint(v[j]) & 0xffff0000u);
+    }
+  }
+}
+
+// WIDE: 8-bit elements taken as bfloat16; float32 ones as three bfloat16 terms,
+// of whose nine products the six down to 2^-16 of the largest are taken: what is
+// left out is below a product's own rounding, and six products at the bfloat16
+// rate take less than one at float32's, a sixteenth of it (the gated pair of 1037
+// x 520 x 1384: forward 50 -> 42 us, dx 46 -> 33, dW 50 -> 35, error 6e-7 ->
+// 5e-7).  The terms' making, 44 instructions for 8 elements, is the other half
+// of the time.  An infinity becomes a NaN.  PLAIN keeps float32's own instructions
+// and with them its results.
 template <typename E, bool WIDE, int FM, int FN>
 __device__ __forceinline__ void mma_half(const typename E::Frag (&fa)[2][FM], const typename E::Frag (&fb)[2][FN], f32x16 (&acc)[FN][FM]) {
-  if constexpr (WIDE) {
+  if constexpr (WIDE && E::CH == 4) {
+    bf16x8 a[FM][3], b[FN][3];
+#pragma unroll
+    for (int j = 0; j < FM; ++j) three_terms(fa[0][j], fa[1][j], a[j]);
+#pragma unroll
+    for (int i = 0; i < FN; ++i) three_terms(fb[0][i], fb[1][i], b[i]);
+#pragma unroll
+    for (int q = 2; q >= 0; --q)  // products of terms down to 2^-16 of the largest, the small ones first
+#pragma unroll
+      for (int r = 0; r <= q; ++r)
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+          for (int j = 0; j < FM; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[i][r], a[j][q - r], acc[i][j], 0, 0, 0);
+    return;
+  }
+  if constexpr (WIDE && E::CH == 16) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       bf16x8 a[FM], b[FN];
@@ -462,15 +503,22 @@ __device__ __forceinline__ void mma_live(const typename E::Frag (&fa)[2][FM], co
   if constexpr (E::CH > 4) {
     mma_half<E, WIDE>(fa, fb, acc);
   } else if (live_m >= FM && live_n >= FN) {
-    mma_half<E, false>(fa, fb, acc);
+    mma_half<E, WIDE>(fa, fb, acc);
   } else {
 #pragma unroll
     for (int i = 0; i < FN; ++i)
 #pragma unroll
       for (int j = 0; j < FM; ++j)
         if (i < live_n && j < live_m) {
+          if constexpr (WIDE) {
+            typename E::Frag a[2][1] = {{fa[0][j]}, {fa[1][j]}}, b[2][1] = {{fb[0][i]}, {fb[1][i]}};
+            f32x16 c[1][1] = {{acc[i][j]}};
+            mma_half<E, true>(a, b, c);
+            acc[i][j] = c[0][0];
+          } else {
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks) acc[i][j] = E::mma(fb[ks][i], fa[ks][j], acc[i][j]);
+            for (int ks = 0; ks < 2; ++ks) acc[i][j] = E::mma(fb[ks][i], fa[ks][j], acc[i][j]);
+          }
         }
   }
 }
@@ -508,7 +556,7 @@ __global__ void __launch_bounds__(256, 2) linear_tile_kernel(const LinearParams 
   __shared__ __align__(1024) T lds[2 * Tl::kStage];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   constexpr int kStep = sizeof(T) == 4 ? 64 : 32;
-  constexpr bool kWide = sizeof(T) == 1 && sizeof(O) == 4;
+  constexpr bool kWide = sizeof(T) == 1 ? sizeof(O) == 4 : sizeof(T) == 4 && MODE != PLAIN;
   const int wm = (wave >> 1) * (96 - kStep), wn = (wave & 1) * (96 - kStep);
   const Tl t(p, wave, lane);
   const int n0 = t.n0 + (MODE == GATED && kStep == 32 ? wn / 2 : wn);  // the wave's first column of the output
