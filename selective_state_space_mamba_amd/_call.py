@@ -16,22 +16,28 @@ def _raw_current():
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-_current = None
+def _device():
+    """-> the current device's index.  torch.cuda's own way asks first whether
+    there is a GPU in use (0.2 us more); a tensor on one says so."""
+    import torch
+    return getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+_current = _current_device = None
 
 
 def launch_stream(x, stream) -> int:
     """The raw stream to launch on (torch's current one where stream is None).
     x has to be on the current GPU: that is the device the library launches on."""
-    global _current
-    import torch
+    global _current, _current_device
     dev = x.get_device()
     if dev < 0 or not x.is_cuda:
         raise ValueError("x is on %s, a GPU is needed" % x.device)
-    if dev != torch.cuda.current_device():
-        raise ValueError("x is on cuda:%d, the current device is cuda:%d" % (dev, torch.cuda.current_device()))
+    if _current is None:
+        _current, _current_device = _raw_current(), _device()
+    if dev != _current_device():
+        raise ValueError("x is on cuda:%d, the current device is cuda:%d" % (dev, _current_device()))
     if stream is None:
-        if _current is None:
-            _current = _raw_current()
         return _current(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 

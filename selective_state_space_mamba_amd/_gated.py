@@ -45,7 +45,7 @@ def gated_linear_fwd(x, w_gate, w_up, b_gate=None, b_up=None, *, act=ACT_SILU, o
     pre); pre holds both products, [2, ..., N] float32, which gated_linear_bwd
     takes (None unless want_pre or a buffer for it is given)."""
     import torch
-    ts = _b._foreign_stream(stream)
+    ts = None if stream is None else _b._foreign_stream(stream)
     if ts is not None:
         with torch.cuda.stream(ts):
             return gated_linear_fwd(x, w_gate, w_up, b_gate, b_up, act=act, out=out, pre=pre, want_pre=want_pre,
@@ -77,7 +77,7 @@ def gated_linear_bwd(x, w_gate, w_up, *, dout, pre, act=ACT_SILU, want_dx=True, 
     gated_linear_fwd returned.  Returns a dict with dx, dw_gate, dw_up, db_gate
     and db_up [N] float32 (None unless wanted)."""
     import torch
-    ts = _b._foreign_stream(stream)
+    ts = None if stream is None else _b._foreign_stream(stream)
     if ts is not None:
         with torch.cuda.stream(ts):
             return gated_linear_bwd(x, w_gate, w_up, dout=dout, pre=pre, act=act, want_dx=want_dx,

@@ -52,7 +52,7 @@ def linear_q8(x, x_scale, weight, w_scale, bias=None, residual=None, *, act=ACT_
     residual).  Returns out; its type is out's, residual's or dtype, bfloat16
     where none is given."""
     import torch
-    ts = _b._foreign_stream(stream)
+    ts = None if stream is None else _b._foreign_stream(stream)
     if ts is not None:
         with torch.cuda.stream(ts):
             return linear_q8(x, x_scale, weight, w_scale, bias, residual, act=act, dtype=dtype, out=out,
@@ -95,7 +95,7 @@ def linear_q4(x, weight, scale, zero=None, bias=None, residual=None, *, group=12
     (None: 8), bias [N] float32, residual and out [..., N] of x's type (out may
     be residual).  A weight stands for (q - zero)·scale.  Returns out."""
     import torch
-    ts = _b._foreign_stream(stream)
+    ts = None if stream is None else _b._foreign_stream(stream)
     if ts is not None:
         with torch.cuda.stream(ts):
             return linear_q4(x, weight, scale, zero, bias, residual, group=group, act=act, out=out, stream=ts)

@@ -89,7 +89,7 @@ def rms_norm_fwd(x, weight=None, residual=None, *, eps=1e-5, out=None, added=Non
     may be given for it), rstd [...] float32 what rms_norm_bwd takes.  out may
     be x itself."""
     import torch
-    ts = _b._foreign_stream(stream)
+    ts = None if stream is None else _b._foreign_stream(stream)
     if ts is not None:
         with torch.cuda.stream(ts):
             return rms_norm_fwd(x, weight, residual, eps=eps, out=out, added=added, rstd=rstd, stream=ts)
@@ -113,7 +113,7 @@ def rms_norm_q8(x, weight=None, residual=None, *, eps=1e-5, out=None, scale=None
     Returns (out [..., D] float8_e4m3fn, scale [...] float32, added): the
     normalised row is out·scale."""
     import torch
-    ts = _b._foreign_stream(stream)
+    ts = None if stream is None else _b._foreign_stream(stream)
     if ts is not None:
         with torch.cuda.stream(ts):
             return rms_norm_q8(x, weight, residual, eps=eps, out=out, scale=scale, added=added, stream=ts)
@@ -139,7 +139,7 @@ def rms_norm_bwd(s, weight=None, *, dout, rstd, dadded=None, want_dweight=True, 
     dx (of dout's type), dresidual (of s's type: dx itself where the types are
     the same) and dweight (None without a weight, or unless wanted)."""
     import torch
-    ts = _b._foreign_stream(stream)
+    ts = None if stream is None else _b._foreign_stream(stream)
     if ts is not None:
         with torch.cuda.stream(ts):
             return rms_norm_bwd(s, weight, dout=dout, rstd=rstd, dadded=dadded, want_dweight=want_dweight,

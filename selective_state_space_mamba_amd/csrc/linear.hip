@@ -75,7 +75,8 @@ int mamba_linear_fwd(const void* x, const void* weight, const float* bias, const
   p.M = (int)dims->rows, p.N = (int)dims->out_dim, p.K = (int)dims->in_dim;
   p.bias = bias, p.residual = residual, p.out = out, p.pre = pre, p.act = dims->act;
   p.part = static_cast<float*>(dims->workspace);
-  const hipError_t e = bf16 ? forward<uint16_t, uint16_t, PLAIN>(p, pl, stream) : forward<float, float, PLAIN>(p, pl, stream);
+  const int tiles = dims->rows <= kRowsMax ? few_rows(dims->rows) / 16 : 0;
+  const hipError_t e = bf16 ? forward<uint16_t, uint16_t, PLAIN>(p, pl, tiles, stream) : forward<float, float, PLAIN>(p, pl, tiles, stream);
   return e == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
 }
 

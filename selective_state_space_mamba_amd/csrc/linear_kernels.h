@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const LinearParams p) 
 }
 
 // ---- few rows ----
-// Up to 16·MT rows: bound by reading W once (and, at a decode step's sizes, by
+// Up to 16·MT rows, or blocks of them: bound by reading W once (and, at a decode step's sizes, by
 // the launch).  A workgroup takes 16 columns; its 8 waves share the contraction
 // in turn, each lane reading its fragments of W and x straight into registers,
 // U turns at once so that they wait for memory together (past the contraction's
@@ -736,14 +736,15 @@ __global__ void __launch_bounds__(512) linear_rows_kernel(const LinearParams p) 
   constexpr int U = 4;  // (8 turns: 64 x 4096 x 4096 20.2 us either way, 1 x 768 x 1536 2.95 -> 3.4)
   __shared__ float red[8][NB][MT][256];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, i = lane & 15, kq = (lane >> 4) * CH;
-  const int n0 = blockIdx.x * 16;
+  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * MT, rows = min(16 * MT, p.M - m0);
   // (16 rows of W, or 64 of x, are at most 2^28 bytes)
-  const auto wr = make_rsrc(static_cast<const T*>(p.b) + (int64_t)n0 * p.ldb, 0x7fffffffu), xr = make_rsrc(p.a, 0x7fffffffu);
+  const auto wr = make_rsrc(static_cast<const T*>(p.b) + (int64_t)n0 * p.ldb, 0x7fffffffu);
+  const auto xr = make_rsrc(static_cast<const T*>(p.a) + m0 * p.lda, 0x7fffffffu);
   const auto wr2 = make_rsrc(static_cast<const T*>(NB > 1 ? p.b2 : p.b) + (int64_t)n0 * p.ldb, 0x7fffffffu);
   const uint32_t w = (uint32_t)((min(n0 + i, p.N - 1) - n0) * (int)p.ldb + kq) * (uint32_t)sizeof(T);
   uint32_t x[MT];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) x[t] = (uint32_t)(min(t * 16 + i, p.M - 1) * (int)p.lda + kq) * (uint32_t)sizeof(T);
+  for (int t = 0; t < MT; ++t) x[t] = (uint32_t)(min(t * 16 + i, rows - 1) * (int)p.lda + kq) * (uint32_t)sizeof(T);
   f32x4v acc[NB][MT];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
@@ -757,8 +758,10 @@ __global__ void __launch_bounds__(512) linear_rows_kernel(const LinearParams p) 
       const uint32_t at = k + kq < p.K ? (uint32_t)k * (uint32_t)sizeof(T) : kDrop;
       wv[u][0] = __builtin_amdgcn_raw_buffer_load_b128(wr, (int)(w + at), 0, 0);
       if constexpr (NB > 1) wv[u][1] = __builtin_amdgcn_raw_buffer_load_b128(wr2, (int)(w + at), 0, 0);
+      if (MT > 1 || i < rows) {  // (a lane without a row: what it holds reaches only outputs that there are not)
 #pragma unroll
-      for (int t = 0; t < MT; ++t) xv[u][t] = __builtin_amdgcn_raw_buffer_load_b128(xr, (int)(x[t] + at), 0, 0);
+        for (int t = 0; t < MT; ++t) xv[u][t] = __builtin_amdgcn_raw_buffer_load_b128(xr, (int)(x[t] + at), 0, 0);
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -792,7 +795,7 @@ __global__ void __launch_bounds__(512) linear_rows_kernel(const LinearParams p) 
     for (int t = 0; t < MT; ++t) *reinterpret_cast<f32x4v*>(&red[wave][b][t][lane * 4]) = acc[b][t];
   __syncthreads();
   if (threadIdx.x < MT * 32) {
-    const int t = threadIdx.x >> 5, l = threadIdx.x & 15, half = (threadIdx.x >> 4) & 1, m = t * 16 + l, n = n0 + half * 8;
+    const int t = threadIdx.x >> 5, l = threadIdx.x & 15, half = (threadIdx.x >> 4) & 1, m = m0 + t * 16 + l, n = n0 + half * 8;
     float v[NB][8];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {

@@ -22,6 +22,7 @@ inline int few_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 6
 struct ProductPlan {
   int tile, tiles_m, tiles_n, splits, kt_per_split;
   size_t part;  // bytes
+  double us;    // expected
 };
 
 // The tile and the number of shares of the contraction with the least expected
@@ -63,7 +64,7 @@ inline ProductPlan plan_product(int64_t M, int64_t N, int64_t K, bool bf16, bool
       if (splits > 1) us += 4.0 + (double)splits * (double)M * (double)N * 8.0 / 5.0e6;
       if (us < best_us) {
         best_us = us;
-        best = ProductPlan{t, (int)tm, (int)tn, (int)splits, (int)per, splits > 1 ? up256((size_t)splits * M * N * sizeof(float)) : 0};
+        best = ProductPlan{t, (int)tm, (int)tn, (int)splits, (int)per, splits > 1 ? up256((size_t)splits * M * N * sizeof(float)) : 0, us};
       }
       if (s >= most) break;
     }
@@ -127,21 +128,53 @@ hipError_t product(LinearParams p, const ProductPlan& pl, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Few rows.  The plain product takes up to 64 in one block of 16, 32 or 64.  The
+// gated pair and the 8-bit product take blocks of them side by side where that
+// fills more compute units: a round is a workgroup of 16 columns a compute unit,
+// a block of 32 rows takes 1.25 times one of 16, of 64 1.8 times (the gated pair
+// of 4096 x 4096, in us: 16 rows 17.0, 32 18.5 to 19.9, 64 27.3; of 4096 x 2048,
+// 64 rows in one block 24.3, in two 17.6), each further round 0.6 of its first.
+struct RowsPlan {
+  int tiles;    // of 16 rows in a block; 0: not this way
+  double time;  // against one round of one tile
+};
+inline RowsPlan rows_plan(int64_t M, int64_t N) {
+  static const struct { int tiles; double time; } kBlock[3] = {{1, 1.0}, {2, 1.25}, {4, 1.8}};
+  RowsPlan best{0, 1e300};
+  for (const auto& b : kBlock) {
+    const int64_t wgs = ((M + 16 * b.tiles - 1) / (16 * b.tiles)) * ((N + 15) / 16), rounds = (wgs + 255) / 256;
+    const double t = b.time * (1.0 + 0.6 * (double)(rounds - 1));
+    if (t < best.time) best = RowsPlan{b.tiles, t};
+  }
+  return best;
+}
+// For a product of these modes whose tiles are planned as pl and whose round of
+// 16 rows takes round_us: always up to 64 rows, up to 256 where it is expected
+// to be the faster (the tiles' expectation is a quarter long at so few rows;
+// 128 rows of 1536 x 768 bfloat16 in a gated pair 12.8 us in tiles, 9.1 so; 65
+// rows of 4096 x 2048 15.3 and 24.7).
+inline RowsPlan rows_or_tiles(int64_t M, int64_t N, const ProductPlan& pl, double round_us) {
+  if (M > 256) return RowsPlan{0, 0.0};
+  const RowsPlan rp = rows_plan(M, N);
+  return M <= kRowsMax || rp.time * round_us < 0.8 * pl.us ? rp : RowsPlan{0, 0.0};
+}
+
 template <typename T, typename O, int MODE>
-hipError_t product_rows(LinearParams p, hipStream_t stream) {
-  const unsigned grid = (unsigned)ceil_div(p.N, 16);
+hipError_t product_rows(LinearParams p, int tiles, hipStream_t stream) {
+  const dim3 grid((unsigned)ceil_div(p.N, 16), (unsigned)ceil_div(p.M, 16 * tiles));
   p.part = nullptr;
-  switch (few_rows(p.M)) {
-    case 16: linear_rows_kernel<T, O, MODE, 1><<<grid, 512, 0, stream>>>(p); break;
-    case 32: linear_rows_kernel<T, O, MODE, 2><<<grid, 512, 0, stream>>>(p); break;
+  switch (tiles) {
+    case 1: linear_rows_kernel<T, O, MODE, 1><<<grid, 512, 0, stream>>>(p); break;
+    case 2: linear_rows_kernel<T, O, MODE, 2><<<grid, 512, 0, stream>>>(p); break;
     default: linear_rows_kernel<T, O, MODE, 4><<<grid, 512, 0, stream>>>(p);
   }
   return hipGetLastError();
 }
 
+// tiles: the few-rows kernel's, 0 for the tile kernels
 template <typename T, typename O, int MODE>
-hipError_t forward(const LinearParams& p, const ProductPlan& pl, hipStream_t stream) {
-  return p.M <= kRowsMax ? product_rows<T, O, MODE>(p, stream) : product<T, O, MODE, false, false>(p, pl, stream);
+hipError_t forward(const LinearParams& p, const ProductPlan& pl, int tiles, hipStream_t stream) {
+  return tiles > 0 ? product_rows<T, O, MODE>(p, tiles, stream) : product<T, O, MODE, false, false>(p, pl, stream);
 }
 
 }  // namespace mscan

@@ -43,7 +43,9 @@ CASES = [
     (127, 8, 8, "bf16", "none", (False, False)),
     (129, 72, 136, "f32", "relu", (True, True)),
     (128, 128, 64, "bf16", "none", (False, False)),
-    (200, 2056, 264, "bf16", "silu", (True, False)),   # split contraction
+    (200, 2056, 264, "bf16", "silu", (True, False)),   # blocks of few rows; in dx and dw, shares of the contraction
+    (300, 4104, 264, "bf16", "silu", (True, True)),    # shares of the contraction in the forward too
+    (250, 520, 4104, "bf16", "relu", (False, True)),
     (200, 2056, 264, "f32", "gelu", (False, True)),
     (1000, 200, 96, "f32", "none", (True, True)),
     (70, 136, 48, "f32", "silu", (True, True)),

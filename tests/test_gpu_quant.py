@@ -36,6 +36,7 @@ Q8 = [
     (33, 272, 1032, "f32", "silu", True, True), (64, 48, 136, "bf16", "gelu", True, True), (65, 48, 136, "bf16", "gelu", True, True),
     (127, 16, 8, "bf16", "none", False, False), (129, 144, 136, "f32", "relu", True, True), (128, 128, 128, "bf16", "none", False, False),
     (200, 4112, 264, "bf16", "silu", True, True), (200, 4112, 264, "f32", "gelu", True, True), (1000, 208, 96, "f32", "none", True, False),
+    (300, 8208, 264, "bf16", "silu", True, True), (300, 8208, 264, "f32", "gelu", True, True), (250, 1040, 4104, "bf16", "none", True, True),
     (1500, 768, 1544, "bf16", "silu", True, False), (5003, 528, 256, "bf16", "gelu", True, True),
     (16300, 656, 1528, "bf16", "silu", True, True), (16300, 656, 1528, "f32", "silu", True, True),
     (8200, 2000, 2056, "bf16", "none", True, True), (8200, 2000, 2056, "f32", "none", True, True),
