@@ -44,6 +44,21 @@ def _q8_bytes(M, K, N):
     return linear_q8_workspace_bytes(make_linear_dims(M, K, N, _b.DTYPE_BF16))
 
 
+@functools.lru_cache(maxsize=512)
+def _bare_q8_dims(M, K, N, dt, act):
+    """A reference to the sizes of a call without workspace, which only reads them."""
+    return ctypes.byref(make_linear_dims(M, K, N, dt, act=act))
+
+
+@functools.lru_cache(maxsize=512)
+def _q4_dims(*sizes):
+    return ctypes.byref(Q4Dims(*sizes))
+
+
+def _out_shape(xs, N):
+    return (xs[0], N) if len(xs) == 2 else tuple(xs[:-1]) + (N,)
+
+
 def linear_q8(x, x_scale, weight, w_scale, bias=None, residual=None, *, act=ACT_NONE, dtype=None, out=None,
               workspace=None, stream=None):
     """mamba_linear_q8 on torch tensors: x [..., K] and weight [N][K]
@@ -60,16 +75,24 @@ def linear_q8(x, x_scale, weight, w_scale, bias=None, residual=None, *, act=ACT_
     xs, wsh = x.shape, weight.shape
     if len(wsh) != 2 or len(xs) < 1 or xs[-1] != wsh[1]:
         raise ValueError("x must be [..., K] and weight [N][K], got %s and %s" % (tuple(xs), tuple(wsh)))
-    if x.dtype is not torch.float8_e4m3fn:
-        raise TypeError("x must be float8_e4m3fn, got %s" % x.dtype)
-    check_like(x, xs, ("x", x))
-    check_like(x, wsh, ("weight", weight))
-    raw = launch_stream(x, stream)
+    e4m3, f32, dev = torch.float8_e4m3fn, torch.float32, x.get_device()
     N, K = wsh
+    # (written out: a step is a few microseconds)
+    if not (x.dtype is e4m3 and weight.dtype is e4m3 and x.is_contiguous() and weight.is_contiguous()
+            and x_scale.shape == xs[:-1] and x_scale.dtype is f32 and x_scale.is_contiguous()
+            and w_scale.shape == wsh[:1] and w_scale.dtype is f32 and w_scale.is_contiguous()
+            and weight.get_device() == dev and x_scale.get_device() == dev and w_scale.get_device() == dev):
+        if x.dtype is not e4m3:
+            raise TypeError("x must be float8_e4m3fn, got %s" % x.dtype)
+        check_like(x, xs, ("x", x))
+        check_like(x, wsh, ("weight", weight))
+        check_f32(x, xs[:-1], ("x_scale", x_scale))
+        check_f32(x, (N,), ("w_scale", w_scale))
+    raw = launch_stream(x, stream)
     M = x.numel() // K if K else 0
-    check_f32(x, xs[:-1], ("x_scale", x_scale))
-    check_f32(x, (N,), ("w_scale", w_scale), ("bias", bias))
-    shape = xs[:-1] + wsh[:1]
+    if bias is not None:
+        check_f32(x, (N,), ("bias", bias))
+    shape = _out_shape(xs, N)
     given = residual if out is None else out
     if given is not None:
         dt = _b._dtype_code(given)
@@ -80,10 +103,15 @@ def linear_q8(x, x_scale, weight, w_scale, bias=None, residual=None, *, act=ACT_
     if out is None:
         out = x.new_empty(shape, dtype=torch.bfloat16 if dtype is None else dtype) if given is None else torch.empty_like(given)
         dt = _b._dtype_code(out)
-    dims = make_linear_dims(M, K, N, dt, act=act)
-    workspace = use_workspace(dims, _q8_bytes(M, K, N), workspace, x)
+    need, act = _q8_bytes(M, K, N), int(act)  # (a tensor would be looked up by its identity)
+    if need == 0 and workspace is None:
+        dims = _bare_q8_dims(M, K, N, dt, act)
+    else:
+        held = make_linear_dims(M, K, N, dt, act=act)
+        workspace = use_workspace(held, need, workspace, x)
+        dims = ctypes.byref(held)
     done(_b.load_library().mamba_linear_q8(x.data_ptr(), x_scale.data_ptr(), weight.data_ptr(), w_scale.data_ptr(),
-                                           ptr(bias), ptr(residual), ctypes.byref(dims), out.data_ptr(), raw),
+                                           ptr(bias), ptr(residual), dims, out.data_ptr(), raw),
          "mamba_linear_q8")
     return out
 
@@ -103,7 +131,8 @@ def linear_q4(x, weight, scale, zero=None, bias=None, residual=None, *, group=12
     if len(wsh) != 2 or len(xs) < 1 or xs[-1] != 2 * wsh[1]:
         raise ValueError("x must be [..., K] and weight [N][K/2], got %s and %s" % (tuple(xs), tuple(wsh)))
     dt = _b._dtype_code(x)
-    check_like(x, xs, ("x", x))
+    if not x.is_contiguous():
+        check_like(x, xs, ("x", x))  # raises with the reason
     raw = launch_stream(x, stream)
     N, K = wsh[0], xs[-1]
     group = int(group)
@@ -116,11 +145,12 @@ def linear_q4(x, weight, scale, zero=None, bias=None, residual=None, *, group=12
     _b._check(zero, "zero", table, torch.uint8, x.device)
     if bias is not None:
         check_f32(x, (N,), ("bias", bias))
-    shape = xs[:-1] + (N,)
-    check_like(x, shape, ("residual", residual), ("out", out))
+    shape = _out_shape(xs, N)
+    if residual is not None or out is not None:
+        check_like(x, shape, ("residual", residual), ("out", out))
     if out is None:
-        out = x.new_empty(shape)
-    dims = make_q4_dims(x.numel() // K if K else 0, K, N, group, dt, scale_dtype=scale_dt, act=act)
+        out = x.new_empty(shape) if residual is None else torch.empty_like(residual)
+    dims = _q4_dims(x.numel() // K if K else 0, K, N, group, dt, scale_dt, int(act))
     done(_b.load_library().mamba_linear_q4(x.data_ptr(), weight.data_ptr(), scale.data_ptr(), ptr(zero), ptr(bias),
-                                           ptr(residual), ctypes.byref(dims), out.data_ptr(), raw), "mamba_linear_q4")
+                                           ptr(residual), dims, out.data_ptr(), raw), "mamba_linear_q4")
     return out

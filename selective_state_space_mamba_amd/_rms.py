@@ -45,14 +45,22 @@ def _bwd_bytes(rows, D, dt, rt):
     return rms_norm_bwd_workspace_bytes(make_rms_dims(rows, D, dt, residual_dtype=rt))
 
 
+@functools.lru_cache(maxsize=512)
+def _bare_dims(rows, D, dt, rt, eps):
+    """A reference to the sizes of a forward, which only reads them."""
+    return ctypes.byref(make_rms_dims(rows, D, dt, residual_dtype=rt, eps=eps))
+
+
 def _check_inputs(x, weight):
-    if x.dim() < 1:
+    shape = x.shape
+    if len(shape) < 1:
         raise ValueError("x must be [..., D], got a scalar")
     dt = _b._dtype_code(x)
-    shape = x.shape
-    check_like(x, shape, ("x", x))
-    check_f32(x, shape[-1:], ("weight", weight))
+    if not x.is_contiguous():
+        check_like(x, shape, ("x", x))  # raises with the reason
     D = shape[-1]
+    if weight is not None:
+        check_f32(x, (D,), ("weight", weight))
     return x.numel() // D if D else 0, D, shape, dt
 
 
@@ -73,13 +81,13 @@ def _fwd(x, weight, residual, eps, added):
     if residual is None:
         if added is not None:
             raise ValueError("added is what x and residual add up to; there is no residual")
-        return shape, make_rms_dims(rows, D, dt, eps=eps), None
+        return shape, _bare_dims(rows, D, dt, dt, float(eps)), None
     rt = _stream_code(x, dt, shape, "residual", residual)
     if added is None:
         added = torch.empty_like(residual)
     else:
         check_like(residual, shape, ("added", added))
-    return shape, make_rms_dims(rows, D, dt, residual_dtype=rt, eps=eps), added
+    return shape, _bare_dims(rows, D, dt, rt, float(eps)), added
 
 
 def rms_norm_fwd(x, weight=None, residual=None, *, eps=1e-5, out=None, added=None, rstd=None, stream=None):
@@ -103,7 +111,7 @@ def rms_norm_fwd(x, weight=None, residual=None, *, eps=1e-5, out=None, added=Non
         rstd = x.new_empty(shape[:-1], dtype=torch.float32)
     else:
         check_f32(x, shape[:-1], ("rstd", rstd))
-    done(_b.load_library().mamba_rms_norm_fwd(x.data_ptr(), ptr(residual), ptr(weight), ctypes.byref(dims),
+    done(_b.load_library().mamba_rms_norm_fwd(x.data_ptr(), ptr(residual), ptr(weight), dims,
                                               out.data_ptr(), ptr(added), rstd.data_ptr(), raw), "mamba_rms_norm_fwd")
     return out, added, rstd
 
@@ -127,7 +135,7 @@ def rms_norm_q8(x, weight=None, residual=None, *, eps=1e-5, out=None, scale=None
         scale = x.new_empty(shape[:-1], dtype=torch.float32)
     else:
         check_f32(x, shape[:-1], ("scale", scale))
-    done(_b.load_library().mamba_rms_norm_q8(x.data_ptr(), ptr(residual), ptr(weight), ctypes.byref(dims),
+    done(_b.load_library().mamba_rms_norm_q8(x.data_ptr(), ptr(residual), ptr(weight), dims,
                                              out.data_ptr(), scale.data_ptr(), ptr(added), raw), "mamba_rms_norm_q8")
     return out, scale, added
 
