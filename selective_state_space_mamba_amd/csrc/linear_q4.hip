@@ -26,19 +26,20 @@ int check(const mamba_q4_dims* g) {
 
 // Row tiles MT and column tiles CT of a workgroup: the least expected time.  A
 // round is a workgroup a compute unit; one of MT x CT tiles takes, against one
-// of 1 x 1, the time below (four tiles of columns more with short groups), and
+// of 1 x 1, the time below (more with short groups, whose scales are more), and
 // each further round half of its own beside the one before, a third where x is
 // next to nothing (4096 elements of the contraction, 16 or 32 bfloat16 rows, in
-// us: 1 round of 1 x 1, 1 x 2, 1 x 4 tiles 8.1, 9.9, 12.0, of 2 x 1, 2 x 2, 2 x
-// 4 11.6, 13.6, 17.4; 2 rounds of 1 x 1 13.1).  Over 9 weights from 1536 x 768
-// to 16384 x 8192 and 1 to 64 rows, 99 in all, the choice took 0.5 % longer than
-// the best on average, at worst 17 % (one row, 5000 x 2080 in groups of 32, 6.7
-// us against 5.7); tiles of 4 x CT gained nothing on it.
+// us: 1 round of 1 x 1, 1 x 2, 1 x 4 tiles 8.1, 9.1, 12.3, of 2 x 1, 2 x 2, 2 x
+// 4 11.5, 12.9, 16.9; 2 rounds of 1 x 1 11.8).  Over 6 weights from 1536 x 768
+// to 16384 x 8192 and 1 to 64 rows, 66 in all, the choice took 0.6 % longer than
+// the best on average, at worst 9 % (40 rows, 5000 x 2080 in groups of 32, 12.0
+// us against 11.0); tiles of 4 x CT gained nothing on it.
 struct Q4Plan {
   int mt, ct;
 };
 Q4Plan plan_q4(int64_t M, int64_t N, int64_t group) {
-  const double kTime[2][3] = {{1.0, 1.25, group < 128 ? 2.1 : 1.7}, {1.45, 1.7, group < 128 ? 2.4 : 2.2}};
+  const bool small = group < 128;
+  const double kTime[2][3] = {{1.0, small ? 1.4 : 1.25, small ? 2.05 : 1.7}, {1.45, 1.7, small ? 2.4 : 2.2}};
   Q4Plan best{1, 1};
   double least = 1e300;
   for (int mt = 1; mt <= 2; ++mt)

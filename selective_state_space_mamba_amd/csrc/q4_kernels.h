@@ -221,8 +221,10 @@ __device__ __forceinline__ void q4_finish(const Q4Params& p, const float* red, i
 // hold a row fetch it (all lanes: 16384 x 8192, one row, 29 us against 24).
 // (x through LDS, shared by waves of other columns, with a barrier a step, took
 // 28 us at 16 rows of 16384 x 8192 against 28, 9 against 7.7 of 2048 x 4096.)
-// GS: groups of a turn (128 / group, 1 for groups of 128 and more).  (Two turns' loads in flight: no faster
-// at any of 9 sizes, 5 to 30 % slower where a wave has few turns.)
+// A turn's weights, and its x where the registers allow, are fetched while the
+// turn before is multiplied, the first ones before the scales (all at the turn's
+// start: one row of 16384 x 8192 QA us, now QB; of 8192 x 4096 QC and QD).
+// GS: groups of a turn (128 / group, 1 for groups of 128 and more).
 template <typename T, int GS, int MT, int CT>
 __global__ void __launch_bounds__(64 * kQ4Waves) q4_kernel(const Q4Params p) {
   typedef Q4Rows<T> Rows;
@@ -248,22 +250,42 @@ __global__ void __launch_bounds__(64 * kQ4Waves) q4_kernel(const Q4Params p) {
   for (int c = 0; c < CT; ++c)
 #pragma unroll
     for (int t = 0; t < MT; ++t) acc[c][t] = f32x4v{0.f, 0.f, 0.f, 0.f};
+  constexpr int kTurns = kQ4Waves * 128;             // elements of a turn of every wave
+  constexpr bool kAhead = MT * sizeof(T) <= 4;       // x of the next turn too
+  static_assert(S * 32 % kTurns == 0, "the table holds whole turns");
+  u32x4 wv[CT], wn[CT];
+  Rows xv[4][MT], xn[4][MT];
+  auto fetch_w = [&](int k) {
+#pragma unroll
+    for (int c = 0; c < CT; ++c) wn[c] = __builtin_amdgcn_raw_buffer_load_b128(qr, (int)(w[c] + (uint32_t)k / 2), 0, 0);
+  };
+  auto fetch_x = [&](int k) {
+    if (MT > 1 || i < rows) {  // (a lane without a row: what it holds reaches only outputs that there are not)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) xn[j][t].load(xr, k + j * 32 < p.K ? x[t] : kDrop, (uint32_t)(k + j * 32) * ES);
+    }
+  };
+  int k0 = wave * 128;
+  fetch_w(k0);
+  if (kAhead) fetch_x(k0);
   for (int first = 0; first < p.groups; first += S) {  // as many groups as the table holds
     const int ng = min(S, p.groups - first), k1 = min((int64_t)(first + ng) * p.group, (int64_t)p.K);
     if (first > 0) __syncthreads();
     q4_table<W>(p, table, n0, cols, first, ng);
     __syncthreads();
-    for (int k0 = first * p.group + wave * 128; k0 < k1; k0 += kQ4Waves * 128) {
-      u32x4 wv[CT];
-      Rows xv[4][MT];
+    for (; k0 < k1; k0 += kTurns) {
+      if (!kAhead) fetch_x(k0);
 #pragma unroll
-      for (int c = 0; c < CT; ++c) wv[c] = __builtin_amdgcn_raw_buffer_load_b128(qr, (int)(w[c] + (uint32_t)k0 / 2), 0, 0);
-      // (a lane without a row: what it holds reaches only outputs that there are not)
-      if (MT > 1 || i < rows) {
+      for (int c = 0; c < CT; ++c) wv[c] = wn[c];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int t = 0; t < MT; ++t) xv[j][t].load(xr, k0 + j * 32 < k1 ? x[t] : kDrop, (uint32_t)(k0 + j * 32) * ES);
+        for (int t = 0; t < MT; ++t) xv[j][t] = xn[j][t];
+      if (k0 + kTurns < p.K) {
+        fetch_w(k0 + kTurns);
+        if (kAhead) fetch_x(k0 + kTurns);
       }
       float2 sg[CT][GS];
       q4_scales<GS, CT, W>(p, table, k0, first, ng, i, sg);
