@@ -39,6 +39,8 @@ ProductPlan plan_dw(const mamba_linear_dims* g) {
   return plan_product(2 * g->out_dim, g->in_dim, g->rows, g->dtype == MAMBA_DTYPE_BF16);
 }
 
+// Runs of rows of the backward's first pass: as many workgroups as the plain
+// product's takes (16384 x 2048: 512 runs, 103 us for 515 MB, 5.0 TB/s).
 struct GatedGradPlan {
   int chunk, chunks;
   size_t dp, part;  // bytes

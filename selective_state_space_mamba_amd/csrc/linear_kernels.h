@@ -876,7 +876,8 @@ __global__ void __launch_bounds__(256) linear_grad_kernel(const LinearGradParams
 // The gated pair's: with a = act(g) and the pair's sums g and u,
 //   dg = dout·u·act'(g),  du = dout·a,
 // side by side in rows of 2N, so that dx is one product over both and dW one
-// product with 2N rows; and both columns' sums over a run of rows.
+// product with 2N rows; and both columns' sums over a run of rows.  pre is
+// float32, as the plain product's and for the same reason.
 struct GatedGradParams {
   const void* dout;  // [M][N]
   const float* pre;  // [2][M][N]

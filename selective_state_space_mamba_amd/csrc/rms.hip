@@ -24,22 +24,28 @@ struct RmsPlan {
 };
 
 // One wave a row up to 2048 channels, unless the rows are so few that four
-// waves each still leave compute units idle.
-RmsPlan plan_rows(int64_t rows, int64_t D) {
+// waves each leave the chip room (bfloat16 with a residual, one and four waves,
+// us: 256 rows of 768 3.3 and 3.0, of 2048 4.3 and 3.1; 1024 rows of 768 3.6 and
+// 3.6, 8-bit 3.9 and 4.3, of 2048 5.2 and 4.4; backward, whose workgroups each
+// leave a row of sums: 64 rows of 2048 6.6 and 5.2, 256 7.1 and 7.3).
+RmsPlan plan_rows(int64_t rows, int64_t D, bool backward) {
   const int vecs = (int)((D + 7) / 8);
   if (vecs <= 256) {
-    if (rows <= 256 && vecs > 64) return RmsPlan{4, 1};
+    const int64_t few = backward ? 128 : vecs > 128 ? 1024 : 256;
+    if (rows <= few && vecs > 64) return RmsPlan{4, 1};
     return RmsPlan{1, (vecs + 63) / 64};
   }
   if (vecs <= 1024) return RmsPlan{4, (vecs + 255) / 256};
   return RmsPlan{8, 4};
 }
 
-// Workgroups of the backward, each with a row of partial sums of dweight.
+// Workgroups of the backward, each with a row of partial sums of dweight (16384
+// rows of 768, 1536, 2048 in bfloat16: 512 of them 21.5, 34.9, 46.6 us, 1024
+// 23.4, 37.1, 49.0, 2048 25.6, 41.7, 55.5).
 int bwd_blocks(const mamba_rms_dims* g) {
-  const RmsPlan pl = plan_rows(g->rows, g->dim);
+  const RmsPlan pl = plan_rows(g->rows, g->dim, true);
   const int64_t per = pl.w == 1 ? 4 : 1, all = (g->rows + per - 1) / per;
-  return (int)(all < 1024 ? all : 1024);
+  return (int)(all < 512 ? all : 512);
 }
 
 int check(const mamba_rms_dims* g) {
@@ -97,7 +103,7 @@ int forward(const void* x, const void* residual, const float* weight, const mamb
   bool rag = g->dim % 8 != 0;
   for (const void* q : {x, residual, (const void*)weight, (const void*)p.added}) rag |= !aligned(q, 16);
   rag |= !aligned(out, Q8 ? 8 : 16);
-  const RmsPlan pl = plan_rows(g->rows, g->dim);
+  const RmsPlan pl = plan_rows(g->rows, g->dim, false);
   const int64_t per = pl.w == 1 ? 4 : 1;
   by_types(g, [&](auto* t, auto* r) {
     using T = std::remove_pointer_t<decltype(t)>;
@@ -155,7 +161,7 @@ int mamba_rms_norm_bwd(const void* s, const float* weight, const float* rstd, co
   by_types(dims, [&](auto* t, auto* r) {
     using T = std::remove_pointer_t<decltype(t)>;
     using R = std::remove_pointer_t<decltype(r)>;
-    by_shape(plan_rows(dims->rows, dims->dim), rag, [&](auto rg, auto w, auto nv) {
+    by_shape(plan_rows(dims->rows, dims->dim, true), rag, [&](auto rg, auto w, auto nv) {
       constexpr int W = decltype(w)::value, NV = decltype(nv)::value;
       rms_bwd_kernel<T, R, decltype(rg)::value, W, NV><<<(unsigned)blocks, rms_threads<W>(), 0, stream>>>(p);
     });

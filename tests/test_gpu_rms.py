@@ -8,7 +8,7 @@ three more: 2^-19 covers each.  A bfloat16 output adds half a step, 2^-8, an
 8-bit one 2^-4 (2^-10 absolute below 2^-6, where the steps are 2^-9).  mean(t·xh)
 errs by the same chains relative to the mean of |t·xh|, and each term of ds by a
 few roundings: 2^-18 of the terms' magnitudes.  dweight is a sum over rows in
-chains of at most rows/1024 + 4 + 32 + 16 terms, each with xh's error: 2^-17 of
+chains of at most rows/512 + 4 + 32 + 16 terms, each with xh's error: 2^-17 of
 its terms' magnitudes for up to 70000 rows."""
 import pytest
 
@@ -263,14 +263,14 @@ def test_more_elements_than_32_bits_count():
     x[M // 64 * 64:] = part[: M % 64]
     w = n((D,))
     out, _, rstd = ms.rms_norm_fwd(x, w)
-    # (320 rows of it: fewer than 257 are summed up by more waves each, in another order)
-    some = x[:320].clone()
+    # (1088 rows of it: up to 1024 are summed up by more waves each, in another order)
+    some = x[:1088].clone()
     want, _, wr = ms.rms_norm_fwd(some, w)
     assert t.equal(out[M // 64 * 64:], want[: M % 64]) and t.equal(rstd[-(M % 64):], wr[: M % 64])
-    assert t.equal(out[:320], want)
+    assert t.equal(out[:1088], want)
     q, scale, _ = ms.rms_norm_q8(x, w)
     wq = ms.rms_norm_q8(some, w)
-    assert t.equal(q[M // 64 * 64:].view(t.uint8), wq[0][: M % 64].view(t.uint8)) and t.equal(scale[:320], wq[1])
+    assert t.equal(q[M // 64 * 64:].view(t.uint8), wq[0][: M % 64].view(t.uint8)) and t.equal(scale[:1088], wq[1])
     g = ms.rms_norm_bwd(x, w, dout=x, rstd=rstd)
     wg = ms.rms_norm_bwd(some, w, dout=some, rstd=wr)
     assert t.equal(g["dx"][M // 64 * 64:], wg["dx"][: M % 64])
