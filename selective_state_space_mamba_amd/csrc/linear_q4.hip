@@ -33,21 +33,25 @@ int check(const mamba_q4_dims* g) {
 // 4 11.5, 12.9, 16.9; 2 rounds of 1 x 1 11.8).  Over 6 weights from 1536 x 768
 // to 16384 x 8192 and 1 to 64 rows, 66 in all, the choice took 0.6 % longer than
 // the best on average, at worst 9 % (40 rows, 5000 x 2080 in groups of 32, 12.0
-// us against 11.0); tiles of 4 x CT gained nothing on it.
+// us against 11.0); tiles of 4 x CT gained nothing on it.  Two row tiles stand
+// for two workgroups of one with twice the columns each, which take less time
+// with one column tile and, but for short groups, no more with two: those are
+// left out.
 struct Q4Plan {
   int mt, ct;
 };
 Q4Plan plan_q4(int64_t M, int64_t N, int64_t group) {
   const bool small = group < 128;
-  const double kTime[2][3] = {{1.0, small ? 1.4 : 1.25, small ? 2.05 : 1.7}, {1.45, 1.7, small ? 2.4 : 2.2}};
+  const struct { int mt, ct; double time; } kinds[5] = {{1, 1, 1.0}, {1, 2, small ? 1.4 : 1.25}, {1, 4, small ? 2.05 : 1.7},
+                                                        {2, 4, small ? 2.4 : 2.2}, {2, 2, 1.7}};
   Q4Plan best{1, 1};
   double least = 1e300;
-  for (int mt = 1; mt <= 2; ++mt)
-    for (int c = 0; c < 3; ++c) {
-      const int64_t wgs = ((M + 16 * mt - 1) / (16 * mt)) * ((N + (16 << c) - 1) / (16 << c)), rounds = (wgs + 255) / 256;
-      const double t = kTime[mt - 1][c] * (1.0 + (M <= 4 ? 0.35 : 0.5) * (double)(rounds - 1));
-      if (t < least) least = t, best = Q4Plan{mt, 1 << c};
-    }
+  for (int c = 0; c < (small ? 5 : 4); ++c) {
+    const auto& k = kinds[c];
+    const int64_t wgs = ((M + 16 * k.mt - 1) / (16 * k.mt)) * ((N + 16 * k.ct - 1) / (16 * k.ct)), rounds = (wgs + 255) / 256;
+    const double t = k.time * (1.0 + (M <= 4 ? 0.35 : 0.5) * (double)(rounds - 1));
+    if (t < least) least = t, best = Q4Plan{k.mt, k.ct};
+  }
   return best;
 }
 
@@ -59,13 +63,14 @@ void launch(const Q4Params& p, hipStream_t stream) {
 template <typename T, int GS>
 void by_tile(const Q4Params& p, hipStream_t stream) {
   const Q4Plan pl = plan_q4(p.M, p.N, p.group);
-  switch (pl.mt * 8 + pl.ct) {
-    case 9: launch<T, GS, 1, 1>(p, stream); break;
-    case 10: launch<T, GS, 1, 2>(p, stream); break;
-    case 12: launch<T, GS, 1, 4>(p, stream); break;
-    case 17: launch<T, GS, 2, 1>(p, stream); break;
-    case 18: launch<T, GS, 2, 2>(p, stream); break;
-    default: launch<T, GS, 2, 4>(p, stream);
+  if (pl.mt == 1) {
+    if (pl.ct == 1) launch<T, GS, 1, 1>(p, stream);
+    else if (pl.ct == 2) launch<T, GS, 1, 2>(p, stream);
+    else launch<T, GS, 1, 4>(p, stream);
+  } else if (pl.ct == 4) {
+    launch<T, GS, 2, 4>(p, stream);
+  } else {
+    if constexpr (GS > 1) launch<T, GS, 2, 2>(p, stream);
   }
 }
 

@@ -113,6 +113,46 @@ def test_exact_products():
                 assert t.equal(got[k], v.float().to(got[k].dtype)), (dtype, M, K, N, k)
 
 
+# Sizes at which the three products of the pair take each tile, whole and in shares of the contraction.
+TILED = [(300, 136, 64), (300, 136, 512), (1000, 136, 64), (300, 1024, 4104), (300, 1536, 4104), (700, 4104, 4104),
+         (8192, 136, 4104), (16384, 136, 2048), (16384, 200, 4104), (40000, 136, 64), (40000, 136, 128), (9000, 136, 1032)]
+
+
+def test_every_tile():
+    """Whole numbers through every tile of dx (as the plain product with twice the rows of a weight, whole stages each)
+    and dW (with 2N rows), without a tolerance; and that TILED is what the comment says."""
+    t = torch()
+    gen = t.Generator(device="cpu")
+    gen.manual_seed(4)
+    seen = set()
+    for M, K, N in TILED:
+        print("[gpu case] gated tiles", M, K, N, flush=True)
+        stages = -(-N // 64) * 64
+        for product, dims in ((1, ms.make_linear_dims(M, K, 2 * stages, ms.DTYPE_BF16)),
+                              (2, ms.make_linear_dims(M, K, 2 * N, ms.DTYPE_BF16))):
+            rows, cols, shares = ms.linear_plan(dims, product)
+            seen.add((product, rows, cols, shares > 1))
+
+        def ints(lo, hi, *shape):
+            return t.randint(lo, hi, shape, generator=gen).double().to("cuda:0")
+
+        x, wg, wu = ints(-2, 3, M, K), ints(-1, 2, N, K), ints(-1, 2, N, K)
+        wg[:, 8:] = 0
+        wu[:, 60:] = 0  # factors that bfloat16 holds
+        dout = ints(-1, 2, M, N)
+        a = [v.bfloat16() for v in (x, wg, wu, dout)]
+        out, pre = ms.gated_linear_fwd(a[0], a[1], a[2], act=ms.ACT_RELU, want_pre=True)
+        want, g, u, grads = gated_ref(x, wg, wu, None, None, "relu", dout)
+        assert t.equal(pre[0].double(), g) and t.equal(pre[1].double(), u) and t.equal(out, want.float().bfloat16())
+        assert float(u.abs().max()) <= 256
+        got = ms.gated_linear_bwd(a[0], a[1], a[2], dout=a[3], pre=pre, act=ms.ACT_RELU)
+        for k, v in grads.items():
+            assert float(v.abs().max()) < 1 << 24
+            assert t.equal(got[k], v.float().to(got[k].dtype)), (M, K, N, k)
+    tiles = [(128, 128), (256, 192), (256, 256)]
+    assert seen >= {(p,) + tile + (split,) for p in (1, 2) for tile in tiles for split in (False, True)}, seen
+
+
 @pytest.mark.parametrize("M", [4, 500])
 def test_rows_stay_apart_and_stacked_weights(M):
     t = torch()

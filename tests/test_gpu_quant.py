@@ -85,6 +85,32 @@ def test_8bit_exact_products():
         assert t.equal(got, x.float())
 
 
+# Sizes at which the product takes each tile, whole and in shares of the contraction.
+TILED = [(300, 144, 64), (300, 2064, 64), (40000, 528, 136), (1000, 8208, 4104), (40000, 144, 136), (400, 8208, 8200)]
+
+
+def test_8bit_every_tile():
+    """Whole numbers through every tile, without a tolerance, for both types of output; and that TILED is what the
+    comment says (the plain product's plan for as many bytes of bfloat16)."""
+    t = torch()
+    gen = t.Generator(device="cpu")
+    gen.manual_seed(3)
+    seen = set()
+    for M, K, N in TILED:
+        print("[gpu case] q8 tiles", M, K, N, flush=True)
+        rows, cols, shares = ms.linear_plan(ms.make_linear_dims(M, K // 2, N, ms.DTYPE_BF16), 0)
+        seen.add((rows, cols, shares > 1))
+        x = t.randint(-1, 2, (M, K), generator=gen).float().to("cuda:0")
+        w = t.randint(-1, 2, (N, K), generator=gen).float().to("cuda:0")
+        res = t.randint(-9, 10, (M, N), generator=gen).float().to("cuda:0")
+        sx, sw = t.full((M,), 0.5, device="cuda:0"), t.full((N,), 2.0, device="cuda:0")
+        want = mm(x, w) + res.double()
+        for dt in (t.float32, t.bfloat16):
+            got = ms.linear_q8(x.to(t.float8_e4m3fn), sx, w.to(t.float8_e4m3fn), sw, None, res.to(dt))
+            assert t.equal(got, want.float().to(dt)), (M, K, N, dt)
+    assert seen == {tile + (split,) for tile in ((128, 128), (256, 192), (256, 256)) for split in (False, True)}, seen
+
+
 @pytest.mark.parametrize("M", [4, 300])
 def test_8bit_rows_stay_apart(M):
     t = torch()
@@ -111,6 +137,9 @@ Q4 = [
     (20, 16384, 1000, "bf16", "bf16", 16384, True, "none", False, True), (5, 11008, 2048, "f32", "f32", 64, False, "none", False, False),
     (3, 1536, 16384, "bf16", "bf16", 128, True, "none", False, False),
 ]
+# every kind of tiles (rows x columns 1x1, 1x2, 1x4, 2x2, 2x4) with each kind of group
+Q4 += [(M, K, N, dtype, "bf16", group, True, "silu", True, True) for dtype in ("bf16", "f32") for group in (32, 64, 256)
+       for M, K, N in ((12, 1120, 1000), (12, 1120, 8200), (16, 480, 20008), (40, 480, 4104), (37, 480, 12296), (100, 2208, 9000))]
 
 
 @pytest.mark.parametrize("case", Q4, ids=lambda c: "%dx%dx%d-%s-s%s-g%d-z%d-%s-b%d-r%d" % c)
