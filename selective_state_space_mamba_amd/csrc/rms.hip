@@ -48,6 +48,14 @@ int bwd_blocks(const mamba_rms_dims* g) {
   return (int)(all < 512 ? all : 512);
 }
 
+// Rows up to which dweight is added up column by column beside the rows, without
+// a workspace and a second launch.  Bfloat16, with the second launch and without:
+// 8 x 1536 4.8 and 2.7 us, 256 x 2048 7.0 and 4.2, 256 x 8192 15.2 and 5.2; 512 x
+// 768 6.0 and 6.2, x 2048 7.7 and 6.5, x 8192 19 and 13; 1024 x 768 6.9 and 10.5,
+// x 8192 22 and 22: the columns' workgroups walk every row, so that more rows take
+// the longer the narrower they are.
+constexpr int64_t kFewRows = 512;
+
 int check(const mamba_rms_dims* g) {
   if (!g) return MAMBA_ERR_INVALID;
   for (int32_t t : {g->dtype, g->residual_dtype})
@@ -123,7 +131,7 @@ extern "C" {
 
 size_t mamba_rms_norm_bwd_workspace_bytes(const mamba_rms_dims* dims) {
   if (check(dims) != MAMBA_OK) return (size_t)-1;
-  return up256((size_t)bwd_blocks(dims) * dims->dim * sizeof(float));
+  return dims->rows <= kFewRows ? 0 : up256((size_t)bwd_blocks(dims) * dims->dim * sizeof(float));
 }
 
 int mamba_rms_norm_fwd(const void* x, const void* residual, const float* weight, const mamba_rms_dims* dims, void* out, void* added,
@@ -149,13 +157,16 @@ int mamba_rms_norm_bwd(const void* s, const float* weight, const float* rstd, co
   for (const float* q : {weight, rstd, (const float*)dweight})
     if (!aligned(q, 4)) return MAMBA_ERR_UNSUPPORTED;
   if (!aligned(dims->workspace, 16)) return MAMBA_ERR_UNSUPPORTED;
-  if (dweight && (!dims->workspace || dims->workspace_bytes < mamba_rms_norm_bwd_workspace_bytes(dims))) return MAMBA_ERR_WORKSPACE;
+  const size_t need = mamba_rms_norm_bwd_workspace_bytes(dims);
+  if (dweight && need > 0 && (!dims->workspace || dims->workspace_bytes < need)) return MAMBA_ERR_WORKSPACE;
   const int blocks = bwd_blocks(dims);
   RmsGradParams p{};
   p.s = s, p.w = weight, p.rstd = rstd, p.dout = dout, p.dadded = dadded, p.dx = dx, p.dres = dresidual;
   p.rows = dims->rows, p.D = (int)dims->dim;
-  // (one workgroup's sums are dweight as they are)
-  p.part = !dweight ? nullptr : blocks == 1 ? dweight : static_cast<float*>(dims->workspace);
+  const bool few = dims->rows <= kFewRows;
+  p.dw = dweight, p.row_blocks = blocks;
+  p.part = dweight && !few ? static_cast<float*>(dims->workspace) : nullptr;
+  const unsigned grid = (unsigned)(blocks + (dweight && few ? (p.D + 127) / 128 : 0));
   bool rag = dims->dim % 8 != 0;
   for (const void* q : {s, (const void*)weight, dout, dadded, (const void*)dx, (const void*)dresidual, (const void*)p.part}) rag |= !aligned(q, 16);
   by_types(dims, [&](auto* t, auto* r) {
@@ -163,11 +174,11 @@ int mamba_rms_norm_bwd(const void* s, const float* weight, const float* rstd, co
     using R = std::remove_pointer_t<decltype(r)>;
     by_shape(plan_rows(dims->rows, dims->dim, true), rag, [&](auto rg, auto w, auto nv) {
       constexpr int W = decltype(w)::value, NV = decltype(nv)::value;
-      rms_bwd_kernel<T, R, decltype(rg)::value, W, NV><<<(unsigned)blocks, rms_threads<W>(), 0, stream>>>(p);
+      rms_bwd_kernel<T, R, decltype(rg)::value, W, NV><<<grid, rms_threads<W>(), 0, stream>>>(p);
     });
   });
   if (hipGetLastError() != hipSuccess) return MAMBA_ERR_HIP;
-  if (dweight && blocks > 1) {
+  if (p.part) {
     colsum_kernel<float><<<(unsigned)((p.D + 15) / 16), 1024, 0, stream>>>(p.part, blocks, p.D, ColStore{dweight, nullptr});
     if (hipGetLastError() != hipSuccess) return MAMBA_ERR_HIP;
   }

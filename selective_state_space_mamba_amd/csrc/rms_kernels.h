@@ -52,8 +52,9 @@ struct RmsGradParams {
   void* dx;            // [rows][D], x's type
   void* dres;          // [rows][D], the residual's type, or null
   float* part;         // [workgroups][D] or null
+  float* dw;           // [D]; of few rows, whose columns the workgroups from row_blocks on add up
   int64_t rows;
-  int D;
+  int D, row_blocks;
 };
 
 // Vector i of a row of `full` whole vectors of 8 and `rest` elements more; zeros past the end.
@@ -212,12 +213,48 @@ __global__ void __launch_bounds__(rms_threads<W>()) rms_fwd_kernel(const RmsPara
   }
 }
 
+// dw of few rows, which needs nothing of a row but its rstd: 128 channels a
+// workgroup, its threads 16 vectors wide down the rows, joined in order.
+template <typename T, typename R, bool RAG, int THREADS>
+__device__ __forceinline__ void rms_columns(const RmsGradParams& p, int block) {
+  constexpr int G = THREADS / 16;
+  __shared__ float red[G][128 + 4];
+  const int v = threadIdx.x & 15, g = threadIdx.x >> 4, full = p.D >> 3, rest = p.D & 7, i = block * 16 + v;
+  float sum[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum[j] = 0.f;
+#pragma unroll 4
+  for (int row = g; row < (int)p.rows; row += G) {
+    Vec<R, 8> s;
+    Vec<T, 8> dy;
+    vec_load<RAG>(s, static_cast<const R*>(p.s) + (int64_t)row * p.D, i, full, rest);
+    vec_load<RAG>(dy, static_cast<const T*>(p.dout) + (int64_t)row * p.D, i, full, rest);
+    const float rstd = p.rstd[row];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] = __builtin_fmaf(dy.get(j), s.get(j) * rstd, sum[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) red[g][v * 8 + j] = sum[j];
+  __syncthreads();
+  const int c = block * 128 + threadIdx.x;
+  if (threadIdx.x < 128 && c < p.D) {
+    float d = 0.f;
+#pragma unroll
+    for (int k = 0; k < G; ++k) d += red[k][threadIdx.x];
+    p.dw[c] = d;
+  }
+}
+
 // A workgroup walks rows, its waves' sums for dw in registers until the end.
 template <typename T, typename R, bool RAG, int W, int NV>
 __global__ void __launch_bounds__(rms_threads<W>()) rms_bwd_kernel(const RmsGradParams p) {
   constexpr int kPer = rms_threads<W>() / (64 * W);
   __shared__ float red[rms_threads<W>() / 64];
   __shared__ float sums[kPer > 1 ? (kPer - 1) * NV * 64 * 8 : 1];
+  if ((int)blockIdx.x >= p.row_blocks) {
+    rms_columns<T, R, RAG, rms_threads<W>()>(p, blockIdx.x - p.row_blocks);
+    return;
+  }
   const int li = threadIdx.x % (64 * W), k = threadIdx.x / (64 * W);
   const int full = p.D >> 3, rest = p.D & 7;
   const float inv = 1.0f / (float)p.D;
@@ -229,7 +266,7 @@ __global__ void __launch_bounds__(rms_threads<W>()) rms_bwd_kernel(const RmsGrad
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[i][j] = p.w ? v.get(j) : 1.f, dw[i][j] = 0.f;
   }
-  for (int64_t row = (int64_t)blockIdx.x * kPer + k; row < p.rows; row += (int64_t)gridDim.x * kPer) {
+  for (int64_t row = (int64_t)blockIdx.x * kPer + k; row < p.rows; row += (int64_t)p.row_blocks * kPer) {
     const int64_t at = row * p.D;
     Vec<R, 8> s[NV], da[NV];
     Vec<T, 8> dy[NV];
