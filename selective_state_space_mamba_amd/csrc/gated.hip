@@ -40,7 +40,9 @@ ProductPlan plan_dw(const mamba_linear_dims* g) {
 }
 
 // Runs of rows of the backward's first pass: as many workgroups as the plain
-// product's takes (16384 x 2048: 512 runs, 103 us for 515 MB, 5.0 TB/s).
+// product's takes (16384 x 2048: 512 runs, 103 us for 515 MB, 5.0 TB/s).  Up to 32 rows are one run,
+// whose columns' sums need no second launch (with and without, 24 x 2048 6.1 and
+// 5.2 us, 8 x 4096 5.9 and 3.9; of 48 rows 6.6 and 7.4).
 struct GatedGradPlan {
   int chunk, chunks;
   size_t dp, part;  // bytes
@@ -49,11 +51,11 @@ GatedGradPlan plan_gated_grad(const mamba_linear_dims* g) {
   GatedGradPlan pl;
   int64_t chunks = 2048 / ceil_div(g->out_dim, 512);
   if (chunks > ceil_div(g->rows, 16)) chunks = ceil_div(g->rows, 16);
-  if (chunks < 1) chunks = 1;
+  if (chunks < 1 || g->rows <= 32) chunks = 1;
   pl.chunk = ceil_div(g->rows, chunks);
   pl.chunks = ceil_div(g->rows, pl.chunk);
   pl.dp = up256((size_t)g->rows * 2 * g->out_dim * (g->dtype == MAMBA_DTYPE_BF16 ? 2 : 4));
-  pl.part = up256((size_t)pl.chunks * g->out_dim * sizeof(float2));
+  pl.part = pl.chunks == 1 ? 0 : up256((size_t)pl.chunks * g->out_dim * sizeof(float2));
   return pl;
 }
 
@@ -125,11 +127,13 @@ int mamba_gated_linear_bwd(const void* x, const void* w_gate, const void* w_up, 
   const int M = (int)dims->rows, N = (int)dims->out_dim, K = (int)dims->in_dim;
   GatedGradParams g{};
   g.dout = dout, g.pre = pre, g.dp = dx || dw_gate ? ws : nullptr;
-  g.part = db_gate ? reinterpret_cast<float2*>(ws + gp.dp) : nullptr;
+  const bool one = gp.chunks == 1;
+  g.part = db_gate && !one ? reinterpret_cast<float2*>(ws + gp.dp) : nullptr;
+  g.db = ColStore{one ? db_gate : nullptr, one ? db_up : nullptr};
   g.M = M, g.N = N, g.chunk = gp.chunk;
   hipError_t e = bf16 ? gated_grad<uint16_t>(g, dims->act, (unsigned)gp.chunks, stream)
                       : gated_grad<float>(g, dims->act, (unsigned)gp.chunks, stream);
-  if (e == hipSuccess && db_gate) {
+  if (e == hipSuccess && g.part) {
     colsum_kernel<float2><<<(unsigned)((N + 15) / 16), 1024, 0, stream>>>(g.part, gp.chunks, N, ColStore{db_gate, db_up});
     e = hipGetLastError();
   }

@@ -883,6 +883,7 @@ struct GatedGradParams {
   const float* pre;  // [2][M][N]
   void* dp;          // [M][2N] or null
   float2* part;      // [chunks][N] or null
+  ColStore db;       // where the only chunk's sums are the columns', or nulls
   int M, N, chunk;
 };
 
@@ -920,7 +921,7 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const GatedGradParams p
       }
     }
   }
-  if (p.part) {
+  if (p.part || p.db.first) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) red[wave][lane * 8 + j] = make_float2(sg[j], su[j]);
     __syncthreads();
@@ -929,7 +930,9 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const GatedGradParams p
       float2 s = red[0][c];
 #pragma unroll
       for (int k = 1; k < 4; ++k) col_add(s, red[k][c]);
-      if (col < p.N) p.part[(int64_t)blockIdx.y * p.N + col] = s;
+      if (col >= p.N) break;
+      if (p.part) p.part[(int64_t)blockIdx.y * p.N + col] = s;
+      else p.db(col, s);
     }
   }
 }

@@ -37,6 +37,8 @@ CASES = [
     (8, 1000, 24, "f32", "gelu", (True, False)),
     (15, 72, 200, "bf16", "relu", (True, True)),
     (17, 4096, 40, "bf16", "silu", (False, False)),
+    (32, 264, 1032, "bf16", "silu", (True, True)),     # bias sums of one run of rows
+    (31, 40, 520, "f32", "gelu", (True, True)),
     (33, 264, 1032, "f32", "silu", (True, True)),
     (64, 40, 136, "bf16", "gelu", (True, True)),
     (65, 40, 136, "bf16", "gelu", (True, True)),
