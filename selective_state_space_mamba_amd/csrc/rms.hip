@@ -18,34 +18,38 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 constexpr int64_t kMaxD = 16384;
 
-// Waves of a row and vectors a lane.
+// Lanes of a row and vectors a lane.
 struct RmsPlan {
-  int w, nv;
+  int lanes, nv;
 };
 
 // One wave a row up to 2048 channels, unless the rows are so few that four
 // waves each leave the chip room (bfloat16 with a residual, one and four waves,
 // us: 256 rows of 768 3.3 and 3.0, of 2048 4.3 and 3.1; 1024 rows of 768 3.6 and
 // 3.6, 8-bit 3.9 and 4.3, of 2048 5.2 and 4.4; backward, whose workgroups each
-// leave a row of sums: 64 rows of 2048 6.6 and 5.2, 256 7.1 and 7.3).
+// leave a row of sums: 64 rows of 2048 6.6 and 5.2, 256 7.1 and 7.3).  Rows of up
+// to 256 channels, of single heads, share a wave (262144 rows of 64 forward 65 us
+// with a wave each, 21 so, backward 104 and 25; of 128 73 and 40, 114 and 43).
 RmsPlan plan_rows(int64_t rows, int64_t D, bool backward) {
   const int vecs = (int)((D + 7) / 8);
   if (vecs <= 256) {
     const int64_t few = backward ? 128 : vecs > 128 ? 1024 : 256;
-    if (rows <= few && vecs > 64) return RmsPlan{4, 1};
-    return RmsPlan{1, (vecs + 63) / 64};
+    if (rows <= few && vecs > 64) return RmsPlan{256, 1};
+    if (vecs <= 32) return RmsPlan{vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32, 1};
+    return RmsPlan{64, (vecs + 63) / 64};
   }
-  if (vecs <= 1024) return RmsPlan{4, (vecs + 255) / 256};
-  return RmsPlan{8, 4};
+  if (vecs <= 1024) return RmsPlan{256, (vecs + 255) / 256};
+  return RmsPlan{512, 4};
 }
 
 // Workgroups of the backward, each with a row of partial sums of dweight (16384
 // rows of 768, 1536, 2048 in bfloat16: 512 of them 21.5, 34.9, 46.6 us, 1024
-// 23.4, 37.1, 49.0, 2048 25.6, 41.7, 55.5).
+// 23.4, 37.1, 49.0, 2048 25.6, 41.7, 55.5; of rows that share a wave more, whose
+// sums are short: 262144 rows of 106 with 512 71, 1024 45, 2048 48, of 64 24, 25, 27).
 int bwd_blocks(const mamba_rms_dims* g) {
   const RmsPlan pl = plan_rows(g->rows, g->dim, true);
-  const int64_t per = pl.w == 1 ? 4 : 1, all = (g->rows + per - 1) / per;
-  return (int)(all < 512 ? all : 512);
+  const int64_t per = pl.lanes < 256 ? 256 / pl.lanes : 1, all = (g->rows + per - 1) / per, most = pl.lanes < 64 ? 1024 : 512;
+  return (int)(all < most ? all : most);
 }
 
 // Rows up to which dweight is added up column by column beside the rows, without
@@ -74,21 +78,27 @@ void by_types(const mamba_rms_dims* g, F f) {
   else if (g->residual_dtype == MAMBA_DTYPE_F32) f((uint16_t*)nullptr, (float*)nullptr);
   else f((uint16_t*)nullptr, (uint16_t*)nullptr);
 }
-// f(RAG, W, NV)
+// f(RAG, lanes of a row, NV)
 template <typename F>
 void by_shape(const RmsPlan& pl, bool rag, F f) {
   auto by_rag = [&](auto r) {
-    auto by_nv = [&](auto w) {
+    using std::integral_constant;
+    auto by_nv = [&](auto l) {
       switch (pl.nv) {
-        case 1: f(r, w, std::integral_constant<int, 1>{}); break;
-        case 2: f(r, w, std::integral_constant<int, 2>{}); break;
-        case 3: f(r, w, std::integral_constant<int, 3>{}); break;
-        default: f(r, w, std::integral_constant<int, 4>{});
+        case 1: f(r, l, integral_constant<int, 1>{}); break;
+        case 2: f(r, l, integral_constant<int, 2>{}); break;
+        case 3: f(r, l, integral_constant<int, 3>{}); break;
+        default: f(r, l, integral_constant<int, 4>{});
       }
     };
-    if (pl.w == 1) by_nv(std::integral_constant<int, 1>{});
-    else if (pl.w == 4) by_nv(std::integral_constant<int, 4>{});
-    else f(r, std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
+    switch (pl.lanes) {
+      case 8: f(r, integral_constant<int, 8>{}, integral_constant<int, 1>{}); break;
+      case 16: f(r, integral_constant<int, 16>{}, integral_constant<int, 1>{}); break;
+      case 32: f(r, integral_constant<int, 32>{}, integral_constant<int, 1>{}); break;
+      case 64: by_nv(integral_constant<int, 64>{}); break;
+      case 256: by_nv(integral_constant<int, 256>{}); break;
+      default: f(r, integral_constant<int, 512>{}, integral_constant<int, 4>{});
+    }
   };
   if (rag) by_rag(std::true_type{});
   else by_rag(std::false_type{});
@@ -112,14 +122,14 @@ int forward(const void* x, const void* residual, const float* weight, const mamb
   for (const void* q : {x, residual, (const void*)weight, (const void*)p.added}) rag |= !aligned(q, 16);
   rag |= !aligned(out, Q8 ? 8 : 16);
   const RmsPlan pl = plan_rows(g->rows, g->dim, false);
-  const int64_t per = pl.w == 1 ? 4 : 1;
+  const int64_t per = pl.lanes < 256 ? 256 / pl.lanes : 1;
   by_types(g, [&](auto* t, auto* r) {
     using T = std::remove_pointer_t<decltype(t)>;
     using R = std::remove_pointer_t<decltype(r)>;
-    by_shape(pl, rag, [&](auto rg, auto w, auto nv) {
-      constexpr int W = decltype(w)::value, NV = decltype(nv)::value;
-      rms_fwd_kernel<T, R, Q8, decltype(rg)::value, W, NV>
-          <<<wide_grid((p.rows + per - 1) / per), rms_threads<W>(), 0, stream>>>(p);
+    by_shape(pl, rag, [&](auto rg, auto l, auto nv) {
+      constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
+      rms_fwd_kernel<T, R, Q8, decltype(rg)::value, L, NV>
+          <<<wide_grid((p.rows + per - 1) / per), rms_threads<L>(), 0, stream>>>(p);
     });
   });
   return hipGetLastError() == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
@@ -172,9 +182,9 @@ int mamba_rms_norm_bwd(const void* s, const float* weight, const float* rstd, co
   by_types(dims, [&](auto* t, auto* r) {
     using T = std::remove_pointer_t<decltype(t)>;
     using R = std::remove_pointer_t<decltype(r)>;
-    by_shape(plan_rows(dims->rows, dims->dim, true), rag, [&](auto rg, auto w, auto nv) {
-      constexpr int W = decltype(w)::value, NV = decltype(nv)::value;
-      rms_bwd_kernel<T, R, decltype(rg)::value, W, NV><<<grid, rms_threads<W>(), 0, stream>>>(p);
+    by_shape(plan_rows(dims->rows, dims->dim, true), rag, [&](auto rg, auto l, auto nv) {
+      constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
+      rms_bwd_kernel<T, R, decltype(rg)::value, L, NV><<<grid, rms_threads<L>(), 0, stream>>>(p);
     });
   });
   if (hipGetLastError() != hipSuccess) return MAMBA_ERR_HIP;

@@ -10,9 +10,9 @@
 // that the backward, which reads the stored sum, differentiates the function
 // that the forward computed.
 //
-// Layout.  A row lies in the registers of W waves, NV vectors of 8 channels a
-// lane, so every tensor is read once; one wave a row up to 2048 channels where
-// there are rows enough, four or eight beyond.  Bound by bytes, at a large
+// Layout.  A row lies in the registers of L lanes, NV vectors of 8 channels a
+// lane, so every tensor is read once: a part of a wave up to 256 channels, one wave
+// up to 2048 where there are rows enough, four or eight beyond.  Bound by bytes, at a large
 // copy's rate: 32768 x 2048 bfloat16 with a residual to 8 bits 85 us (5.5 TB/s),
 // 16384 x 2048 on a float32 stream forward 72 (5.6), backward 106 (5.1), 16384 x
 // 768, which the last-level cache holds, 16.5 (6.1); one token's row 2.6.
@@ -128,11 +128,12 @@ struct AddOp {
 struct MaxOp {
   __device__ static __forceinline__ float of(float a, float b) { return a != a || a > b ? a : b; }
 };
-// Over the lanes of the W waves of a row, left in each of them; red: a float a wave.
-template <int W, typename OP>
+// Over the L lanes of a row, left in each of them; red: a float a wave.
+template <int L, typename OP>
 __device__ __forceinline__ float row_join(float v, float* red) {
+  constexpr int W = L / 64;
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = OP::of(v, __shfl_xor(v, o));
+  for (int o = (L < 64 ? L : 64) / 2; o > 0; o >>= 1) v = OP::of(v, __shfl_xor(v, o));
   if constexpr (W > 1) {
     __syncthreads();  // the last join's values have been read
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
@@ -145,16 +146,16 @@ __device__ __forceinline__ float row_join(float v, float* red) {
   return v;
 }
 
-template <int W>
-constexpr int rms_threads() { return W > 4 ? 64 * W : 256; }
+template <int L>
+constexpr int rms_threads() { return L > 256 ? L : 256; }
 
 // T: x's type, R: the residual's, Q8: 8-bit output
-template <typename T, typename R, bool Q8, bool RAG, int W, int NV>
-__global__ void __launch_bounds__(rms_threads<W>()) rms_fwd_kernel(const RmsParams p) {
-  __shared__ float red[rms_threads<W>() / 64];
-  constexpr int kPer = rms_threads<W>() / (64 * W);  // rows of a workgroup
-  const int li = threadIdx.x % (64 * W);
-  const int64_t row = wide_block() * kPer + threadIdx.x / (64 * W);
+template <typename T, typename R, bool Q8, bool RAG, int L, int NV>
+__global__ void __launch_bounds__(rms_threads<L>()) rms_fwd_kernel(const RmsParams p) {
+  __shared__ float red[rms_threads<L>() / 64];
+  constexpr int kPer = rms_threads<L>() / L;  // rows of a workgroup
+  const int li = threadIdx.x % L;
+  const int64_t row = wide_block() * kPer + threadIdx.x / L;
   if (row >= p.rows) return;  // (a row's waves, all of a workgroup's for W > 1)
   const int full = p.D >> 3, rest = p.D & 7;
   const int64_t at = row * p.D;
@@ -163,10 +164,10 @@ __global__ void __launch_bounds__(rms_threads<W>()) rms_fwd_kernel(const RmsPara
     Vec<T, 8> x[NV];
     Vec<R, 8> r[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) vec_load<RAG>(x[i], static_cast<const T*>(p.x) + at, li + i * 64 * W, full, rest);
+    for (int i = 0; i < NV; ++i) vec_load<RAG>(x[i], static_cast<const T*>(p.x) + at, li + i * L, full, rest);
     if (p.res) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) vec_load<RAG>(r[i], static_cast<const R*>(p.res) + at, li + i * 64 * W, full, rest);
+      for (int i = 0; i < NV; ++i) vec_load<RAG>(r[i], static_cast<const R*>(p.res) + at, li + i * L, full, rest);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(rms_threads<W>()) rms_fwd_kernel(const RmsPara
 #pragma unroll
         for (int j = 0; j < 8; ++j) s[i][j] += r[i].get(j);
         round_to(s[i], (R*)nullptr);
-        if (p.added) vec_store<RAG>(static_cast<R*>(p.added) + at, li + i * 64 * W, full, rest, s[i]);
+        if (p.added) vec_store<RAG>(static_cast<R*>(p.added) + at, li + i * L, full, rest, s[i]);
       }
     }
   }
@@ -185,30 +186,30 @@ __global__ void __launch_bounds__(rms_threads<W>()) rms_fwd_kernel(const RmsPara
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) q = __builtin_fmaf(s[i][j], s[i][j], q);
-  q = row_join<W, AddOp>(q, red);
+  q = row_join<L, AddOp>(q, red);
   const float rstd = 1.0f / __builtin_sqrtf(q / (float)p.D + p.eps);
   if (p.rstd && li == 0) p.rstd[row] = rstd;
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     Vec<float, 8> w;
-    if (p.w) vec_load<RAG>(w, p.w, li + i * 64 * W, full, rest);
+    if (p.w) vec_load<RAG>(w, p.w, li + i * L, full, rest);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       s[i][j] *= rstd;
       if (p.w) s[i][j] *= w.get(j);
       if (Q8) top = MaxOp::of(top, __builtin_fabsf(s[i][j]));
     }
-    if constexpr (!Q8) vec_store<RAG>(static_cast<T*>(p.out) + at, li + i * 64 * W, full, rest, s[i]);
+    if constexpr (!Q8) vec_store<RAG>(static_cast<T*>(p.out) + at, li + i * L, full, rest, s[i]);
   }
   if constexpr (Q8) {
-    const float scale = MaxOp::of(row_join<W, MaxOp>(top, red) / kTop8, kLeastScale), inv = 1.0f / scale;
+    const float scale = MaxOp::of(row_join<L, MaxOp>(top, red) / kTop8, kLeastScale), inv = 1.0f / scale;
     if (li == 0) p.scale[row] = scale;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) s[i][j] *= inv;
-      vec_store8<RAG>(static_cast<uint8_t*>(p.out) + at, li + i * 64 * W, full, rest, s[i]);
+      vec_store8<RAG>(static_cast<uint8_t*>(p.out) + at, li + i * L, full, rest, s[i]);
     }
   }
 }
@@ -246,23 +247,23 @@ __device__ __forceinline__ void rms_columns(const RmsGradParams& p, int block) {
 }
 
 // A workgroup walks rows, its waves' sums for dw in registers until the end.
-template <typename T, typename R, bool RAG, int W, int NV>
-__global__ void __launch_bounds__(rms_threads<W>()) rms_bwd_kernel(const RmsGradParams p) {
-  constexpr int kPer = rms_threads<W>() / (64 * W);
-  __shared__ float red[rms_threads<W>() / 64];
-  __shared__ float sums[kPer > 1 ? (kPer - 1) * NV * 64 * 8 : 1];
+template <typename T, typename R, bool RAG, int L, int NV>
+__global__ void __launch_bounds__(rms_threads<L>()) rms_bwd_kernel(const RmsGradParams p) {
+  constexpr int kPer = rms_threads<L>() / L, kJoin = L < 64 ? 4 : kPer;
+  __shared__ float red[rms_threads<L>() / 64];
+  __shared__ float sums[kJoin > 1 ? (kJoin - 1) * NV * L * 8 : 1];
   if ((int)blockIdx.x >= p.row_blocks) {
-    rms_columns<T, R, RAG, rms_threads<W>()>(p, blockIdx.x - p.row_blocks);
+    rms_columns<T, R, RAG, rms_threads<L>()>(p, blockIdx.x - p.row_blocks);
     return;
   }
-  const int li = threadIdx.x % (64 * W), k = threadIdx.x / (64 * W);
+  const int li = threadIdx.x % L, k = threadIdx.x / L;
   const int full = p.D >> 3, rest = p.D & 7;
   const float inv = 1.0f / (float)p.D;
   float w[NV][8], dw[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     Vec<float, 8> v;
-    if (p.w) vec_load<RAG>(v, p.w, li + i * 64 * W, full, rest);
+    if (p.w) vec_load<RAG>(v, p.w, li + i * L, full, rest);
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[i][j] = p.w ? v.get(j) : 1.f, dw[i][j] = 0.f;
   }
@@ -272,9 +273,9 @@ __global__ void __launch_bounds__(rms_threads<W>()) rms_bwd_kernel(const RmsGrad
     Vec<T, 8> dy[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      vec_load<RAG>(s[i], static_cast<const R*>(p.s) + at, li + i * 64 * W, full, rest);
-      vec_load<RAG>(dy[i], static_cast<const T*>(p.dout) + at, li + i * 64 * W, full, rest);
-      if (p.dadded) vec_load<RAG>(da[i], static_cast<const R*>(p.dadded) + at, li + i * 64 * W, full, rest);
+      vec_load<RAG>(s[i], static_cast<const R*>(p.s) + at, li + i * L, full, rest);
+      vec_load<RAG>(dy[i], static_cast<const T*>(p.dout) + at, li + i * L, full, rest);
+      if (p.dadded) vec_load<RAG>(da[i], static_cast<const R*>(p.dadded) + at, li + i * L, full, rest);
     }
     const float rstd = p.rstd[row];
     float c = 0.f;
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(rms_threads<W>()) rms_bwd_kernel(const RmsGrad
         c = __builtin_fmaf(g * w[i][j], xh, c);
         dw[i][j] = __builtin_fmaf(g, xh, dw[i][j]);
       }
-    c = row_join<W, AddOp>(c, red) * inv;
+    c = row_join<L, AddOp>(c, red) * inv;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float d[8];
@@ -295,30 +296,41 @@ __global__ void __launch_bounds__(rms_threads<W>()) rms_bwd_kernel(const RmsGrad
         d[j] = rstd * __builtin_fmaf(-(s[i].get(j) * rstd), c, dy[i].get(j) * w[i][j]);
         if (p.dadded) d[j] += da[i].get(j);
       }
-      vec_store<RAG>(static_cast<T*>(p.dx) + at, li + i * 64 * W, full, rest, d);
-      if (p.dres) vec_store<RAG>(static_cast<R*>(p.dres) + at, li + i * 64 * W, full, rest, d);
+      vec_store<RAG>(static_cast<T*>(p.dx) + at, li + i * L, full, rest, d);
+      if (p.dres) vec_store<RAG>(static_cast<R*>(p.dres) + at, li + i * L, full, rest, d);
     }
   }
   if (!p.part) return;
-  if constexpr (kPer > 1) {  // the waves' sums to the first one's, in order
-    if (k > 0) {
+  int from = k;
+  if constexpr (L < 64) {  // a wave's rows to its first lanes
+#pragma unroll
+    for (int o = 32; o >= L; o >>= 1)
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sums[(((k - 1) * NV + i) * 8 + j) * 64 + li] = dw[i][j];
+        for (int j = 0; j < 8; ++j) dw[i][j] += __shfl_xor(dw[i][j], o);
+    if (k % (64 / L) != 0) from = -1;
+    else from = k / (64 / L);
+  }
+  if constexpr (kJoin > 1) {  // the waves' sums to the first one's, in order
+    if (from > 0) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sums[(((from - 1) * NV + i) * 8 + j) * L + li] = dw[i][j];
     }
     __syncthreads();
-    if (k > 0) return;
+    if (from != 0) return;
 #pragma unroll
-    for (int q = 0; q < kPer - 1; ++q)
+    for (int q = 0; q < kJoin - 1; ++q)
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dw[i][j] += sums[((q * NV + i) * 8 + j) * 64 + li];
+        for (int j = 0; j < 8; ++j) dw[i][j] += sums[((q * NV + i) * 8 + j) * L + li];
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    vec_store<RAG>(p.part + (int64_t)blockIdx.x * p.D, li + i * 64 * W, full, rest, dw[i]);
+    vec_store<RAG>(p.part + (int64_t)blockIdx.x * p.D, li + i * L, full, rest, dw[i]);
 }
 
 }  // namespace mscan

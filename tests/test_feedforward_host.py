@@ -39,7 +39,7 @@ RMS_BAD = [(dict(rows=0), E.MAMBA_ERR_INVALID), (dict(dim=0), E.MAMBA_ERR_INVALI
 def test_rms_sizes(lib):
     assert ms.rms_norm_bwd_workspace_bytes(rms_dims()) == 0  # few rows: no scratch
     assert ms.rms_norm_bwd_workspace_bytes(rms_dims(rows=512)) == 0
-    assert ms.rms_norm_bwd_workspace_bytes(rms_dims(rows=513)) == 129 * 64 * 4
+    assert ms.rms_norm_bwd_workspace_bytes(rms_dims(rows=513)) == 17 * 64 * 4
     assert ms.rms_norm_bwd_workspace_bytes(rms_dims(rows=1 << 30)) == 512 * 64 * 4
     for bad, _ in RMS_BAD:
         with pytest.raises(ms.MambaError):
