@@ -40,7 +40,8 @@ def test_rms_sizes(lib):
     assert ms.rms_norm_bwd_workspace_bytes(rms_dims()) == 0  # few rows: no scratch
     assert ms.rms_norm_bwd_workspace_bytes(rms_dims(rows=512)) == 0
     assert ms.rms_norm_bwd_workspace_bytes(rms_dims(rows=513)) == 17 * 64 * 4
-    assert ms.rms_norm_bwd_workspace_bytes(rms_dims(rows=1 << 30)) == 512 * 64 * 4
+    assert ms.rms_norm_bwd_workspace_bytes(rms_dims(rows=1 << 30)) == 1024 * 64 * 4
+    assert ms.rms_norm_bwd_workspace_bytes(rms_dims(rows=1 << 30, dim=512)) == 512 * 512 * 4
     for bad, _ in RMS_BAD:
         with pytest.raises(ms.MambaError):
             ms.rms_norm_bwd_workspace_bytes(rms_dims(**bad))
