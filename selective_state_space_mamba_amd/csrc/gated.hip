@@ -22,7 +22,7 @@ int check(const mamba_linear_dims* g) {
 
 // The forward's plan, over the columns of both weights.
 ProductPlan plan_fwd(const mamba_linear_dims* g) {
-  return plan_product(g->rows, 2 * g->out_dim, g->in_dim, g->dtype == MAMBA_DTYPE_BF16, true);
+  return plan_product(g->rows, 2 * g->out_dim, g->in_dim, g->dtype == MAMBA_DTYPE_BF16, GATED);
 }
 // A round of 16 rows (K = 768, 1536, 4096 bfloat16: 5.1, 7.1, 14 us).  float32 beyond 64 rows is the tiles'.
 RowsPlan plan_few(const mamba_linear_dims* g, const ProductPlan& pl) {

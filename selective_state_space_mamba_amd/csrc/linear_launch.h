@@ -41,17 +41,25 @@ struct ProductPlan {
 // 3 rounds, 291).  Over 24 float32 products from 2 to 1536 tiles the number of
 // shares so chosen took 3 % longer on average than the best of 14 tried, at
 // worst 22 % (4096 x 1536 x 768, 125 us against 102 with four shares).
-// pair: the gated pair, N the columns of both weights; a wave's blocks go in
-// pairs, of which the 192 columns of two waves have one and a half.
-inline ProductPlan plan_product(int64_t M, int64_t N, int64_t K, bool bf16, bool pair = false) {
-  static const struct { int bm, bn, slots; double fix, per; } kTiles[3] = {
-      {128, 128, 512, 5.8, 0.0158}, {256, 192, 256, 7.8, 0.0217}, {256, 256, 256, 6.4, 0.0293}};
+// GATED (N the columns of both weights) and SCALED: the outputs of a workgroup
+// that has its compute unit to itself take longer than the plain product's,
+//   256 x 192   10 + 0.0217 K,   256 x 256   12 + 0.025 K
+// (over 300 products of 257 to 32768 rows the tiles and shares so chosen take
+// 0.8 % longer on average than the best tried, 19 % at worst; by the plain
+// product's times 2.3 and 32 %; 8-bit 21240 x 208 x 800 28 us against 36).  The
+// gated pair has no 192 columns: a wave's blocks go in pairs, of which they are
+// one and a half for two waves.
+inline ProductPlan plan_product(int64_t M, int64_t N, int64_t K, bool bf16, int mode = PLAIN) {
+  struct Tile { int bm, bn, slots; double fix, per; };
+  static const Tile kPlain[3] = {{128, 128, 512, 5.8, 0.0158}, {256, 192, 256, 7.8, 0.0217}, {256, 256, 256, 6.4, 0.0293}};
+  static const Tile kMore[3] = {{128, 128, 512, 5.8, 0.0158}, {256, 192, 256, 10.0, 0.0217}, {256, 256, 256, 12.0, 0.025}};
+  const Tile* const kTiles = mode == GATED || mode == SCALED ? kMore : kPlain;
   const int bk = bf16 ? 64 : 32;
   const int64_t kts = (K + bk - 1) / bk, least = bf16 ? 8 : 2;
   ProductPlan best{};
   double best_us = 1e300;
   for (int t = 0; t < (bf16 ? 3 : 1); ++t) {
-    if (pair && t == TILE_256x192) continue;
+    if (mode == GATED && t == TILE_256x192) continue;
     const int64_t tm = (M + kTiles[t].bm - 1) / kTiles[t].bm, tn = (N + kTiles[t].bn - 1) / kTiles[t].bn, tiles = tm * tn;
     int64_t most = tiles < kTiles[t].slots ? kTiles[t].slots / tiles : 1;
     if (most > kts / least) most = kts / least > 0 ? kts / least : 1;

@@ -19,7 +19,7 @@ int check(const mamba_linear_dims* g) {
 }
 
 // By the bytes of the contraction: two 8-bit elements take the place and the time of one bfloat16 one.
-ProductPlan plan(const mamba_linear_dims* g) { return plan_product(g->rows, g->out_dim, g->in_dim / 2, true); }
+ProductPlan plan(const mamba_linear_dims* g) { return plan_product(g->rows, g->out_dim, g->in_dim / 2, true, SCALED); }
 
 // (a round of 16 rows: K = 768, 1536, 4096: 3.5, 4.0, 6.4 us)
 RowsPlan plan_few(const mamba_linear_dims* g, const ProductPlan& pl) {

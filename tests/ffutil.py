@@ -132,3 +132,31 @@ def weights4(N, K, group, seed, zero, scale_type="bf16", device="cuda:0"):
     w = (q.double() - (8.0 if z is None else z.double()[:, at])) * scale.double()[:, at]
     packed = q[:, 0::2] | (q[:, 1::2] << 4)
     return packed.contiguous().to(device), scale.to(device), None if z is None else z.to(device), w.to(device)
+
+
+def planned(M, N, K, more=False, wide=True):
+    """(tile rows, tile columns, shares) of a product of bfloat16 rows, written from the rule beside the launch
+    (csrc/linear_launch.h): the least expected time.  more: of the gated pair (its N columns twice, without the
+    192 columns of wide) and of 8-bit operands (half their K)."""
+    best = None
+    for bm, bn, slots, fix, per in ((128, 128, 512, 5.8, 0.0158), (256, 192, 256, 10.0 if more else 7.8, 0.0217),
+                                    (256, 256, 256) + ((12.0, 0.025) if more else (6.4, 0.0293))):
+        if bn == 192 and not wide:
+            continue
+        tiles, stages = -(-M // bm) * -(-N // bn), -(-K // 64)
+        most = max(min(slots // tiles if tiles < slots else 1, stages // 8), 1)
+        s = 1
+        while True:
+            each = -(-stages // s)
+            shares = -(-stages // each)
+            rounds = -(-tiles * shares // slots)
+            last = 0.6 if bm == 128 and (tiles * shares - 1) % slots < 256 else 1.0
+            us = rounds * fix + (rounds - 1 + last) * per * each * 64
+            if shares > 1:
+                us += 4.0 + shares * M * N * 8 / 5.0e6
+            if best is None or us < best[0]:
+                best = (us, bm, bn, shares)
+            if s >= most:
+                break
+            s = min(2 * s, most)
+    return best[1:]

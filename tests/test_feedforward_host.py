@@ -3,13 +3,14 @@ refusals before any launch, and the float64 references' gradients against
 differences."""
 import ctypes
 import os
+import random
 
 import pytest
 
 import selective_state_space_mamba_amd as ms
 from selective_state_space_mamba_amd import _binding as E
 
-from ffutil import gated_ref, maker, rms_grads, rms_ref
+from ffutil import gated_ref, maker, planned, rms_grads, rms_ref
 
 FAKE = 0x100000  # 16-byte aligned stand-in pointer: every call below fails validation first
 
@@ -45,6 +46,21 @@ def test_rms_sizes(lib):
     for bad, _ in RMS_BAD:
         with pytest.raises(ms.MambaError):
             ms.rms_norm_bwd_workspace_bytes(rms_dims(**bad))
+
+
+def test_planned_tiles(lib):
+    """The tests' rule for tiles and shares is the library's: the plain product's own report, the others' workspaces."""
+    rng = random.Random(6)
+    for _ in range(500):
+        M, N, K = (int(2 ** rng.uniform(a, b)) for a, b in ((8.1, 16), (0, 11), (1, 11)))
+        N, K = 8 * N, 8 * K
+        d = ms.make_linear_dims(M, K, N, ms.DTYPE_BF16)
+        assert planned(M, N, K) == tuple(ms.linear_plan(d, 0)), (M, N, K)
+        shares = planned(M, 2 * N, K, True, False)[2]
+        assert ms.gated_linear_fwd_workspace_bytes(d) == (-(-shares * M * 2 * N * 4 // 256) * 256 if shares > 1 else 0)
+        shares = planned(M, N, K, True)[2]
+        d = ms.make_linear_dims(M, 2 * K, N, ms.DTYPE_BF16)
+        assert ms.linear_q8_workspace_bytes(d) == (-(-shares * M * N * 4 // 256) * 256 if shares > 1 else 0)
 
 
 def test_rms_refusals(lib):

@@ -9,7 +9,7 @@ import pytest
 
 import selective_state_space_mamba_amd as ms
 
-from ffutil import close, dtype_of, finish_ref, maker, mm, rows8, weights4
+from ffutil import close, dtype_of, finish_ref, maker, mm, planned, rows8, weights4
 from layerutil import ACTS
 from scanutil import torch
 
@@ -86,19 +86,20 @@ def test_8bit_exact_products():
 
 
 # Sizes at which the product takes each tile, whole and in shares of the contraction.
-TILED = [(300, 144, 64), (300, 2064, 64), (40000, 528, 136), (1000, 8208, 4104), (40000, 144, 136), (400, 8208, 8200)]
+TILED = [(300, 144, 64), (300, 2064, 64), (40000, 528, 136), (1000, 8208, 4104), (40000, 144, 136), (400, 8208, 8200),
+         (2000, 144, 6152), (9000, 12304, 136)]
 
 
 def test_8bit_every_tile():
     """Whole numbers through every tile, without a tolerance, for both types of output; and that TILED is what the
-    comment says (the plain product's plan for as many bytes of bfloat16)."""
+    comment says (the plan for as many bytes of bfloat16)."""
     t = torch()
     gen = t.Generator(device="cpu")
     gen.manual_seed(3)
     seen = set()
     for M, K, N in TILED:
         print("[gpu case] q8 tiles", M, K, N, flush=True)
-        rows, cols, shares = ms.linear_plan(ms.make_linear_dims(M, K // 2, N, ms.DTYPE_BF16), 0)
+        rows, cols, shares = planned(M, N, K // 2, True)
         seen.add((rows, cols, shares > 1))
         x = t.randint(-1, 2, (M, K), generator=gen).float().to("cuda:0")
         w = t.randint(-1, 2, (N, K), generator=gen).float().to("cuda:0")
