@@ -25,9 +25,9 @@ ProductPlan plan_fwd(const mamba_linear_dims* g) {
   return plan_product(g->rows, 2 * g->out_dim, g->in_dim, g->dtype == MAMBA_DTYPE_BF16, GATED);
 }
 // A round of 16 rows (K = 768, 1536, 4096 bfloat16: 5.1, 7.1, 14 us).  float32 beyond 64 rows is the tiles'.
-RowsPlan plan_few(const mamba_linear_dims* g, const ProductPlan& pl) {
-  const double us = g->dtype == MAMBA_DTYPE_BF16 ? 2.6 + 2.8e-3 * (double)g->in_dim : 1e300;
-  return rows_or_tiles(g->rows, g->out_dim, pl, us);
+FewPlan plan_few(const mamba_linear_dims* g, const ProductPlan& pl) {
+  if (g->dtype != MAMBA_DTYPE_BF16) return rows_or_tiles(g->rows, g->out_dim, pl, 1e30, LongPlan{0, 0.0});
+  return rows_or_tiles(g->rows, g->out_dim, pl, 2.6 + 2.8e-3 * (double)g->in_dim, plan_long(g->rows, 2 * g->out_dim, g->in_dim));
 }
 // dx: a contraction of whole stages over either weight's rows.
 int seg_stages(const mamba_linear_dims* g) { return ceil_div(g->out_dim, g->dtype == MAMBA_DTYPE_BF16 ? 64 : 32); }
@@ -78,7 +78,7 @@ extern "C" {
 size_t mamba_gated_linear_fwd_workspace_bytes(const mamba_linear_dims* dims) {
   if (check(dims) != MAMBA_OK) return (size_t)-1;
   const ProductPlan pl = plan_fwd(dims);
-  return plan_few(dims, pl).tiles > 0 ? 0 : pl.part;
+  return by_tiles(plan_few(dims, pl)) ? pl.part : 0;
 }
 
 size_t mamba_gated_linear_bwd_workspace_bytes(const mamba_linear_dims* dims) {
@@ -97,15 +97,15 @@ int mamba_gated_linear_fwd(const void* x, const void* w_gate, const void* w_up, 
     if (!aligned(q, 16)) return MAMBA_ERR_UNSUPPORTED;
   if (!aligned(b_gate, 4) || !aligned(b_up, 4)) return MAMBA_ERR_UNSUPPORTED;
   const ProductPlan pl = plan_fwd(dims);
-  const int tiles = plan_few(dims, pl).tiles;
-  if (tiles == 0 && pl.part > 0 && (!dims->workspace || dims->workspace_bytes < pl.part)) return MAMBA_ERR_WORKSPACE;
+  const FewPlan few = plan_few(dims, pl);
+  if (by_tiles(few) && pl.part > 0 && (!dims->workspace || dims->workspace_bytes < pl.part)) return MAMBA_ERR_WORKSPACE;
   LinearParams p{};
   p.a = x, p.b = w_gate, p.b2 = w_up, p.lda = p.ldb = dims->in_dim;
   p.M = (int)dims->rows, p.N = (int)dims->out_dim, p.K = (int)dims->in_dim;
   p.bias = b_gate, p.bias2 = b_up, p.out = out, p.pre = pre, p.act = dims->act;
   p.part = static_cast<float*>(dims->workspace);
-  const hipError_t e = dims->dtype == MAMBA_DTYPE_BF16 ? forward<uint16_t, uint16_t, GATED>(p, pl, tiles, stream)
-                                                       : forward<float, float, GATED>(p, pl, tiles, stream);
+  const hipError_t e = dims->dtype == MAMBA_DTYPE_BF16 ? forward<uint16_t, uint16_t, GATED>(p, pl, few, stream)
+                                                       : forward<float, float, GATED>(p, pl, few, stream);
   return e == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
 }
 

@@ -685,6 +685,75 @@ __global__ void __launch_bounds__(512) linear_large_kernel(const LinearParams p)
   linear_out<O, MODE, 32>(p, acc, cols, reinterpret_cast<float*>(lds) + wave * kWave, t.m0 + wm, n0, t.share, lane);
 }
 
+// ---- the long tile: 64 x 64, four waves ----
+// Some dozens or hundreds of rows: bound by how many bytes of the weights are on
+// their way, and by the start and end of few workgroups.  RING stages of LDS, a
+// turn takes two of them while the others fill: eight stages, one workgroup a
+// compute unit, where there are no more (a stage takes 0.25 us), four and two
+// workgroups where there are (0.41).  Two waves take 32 rows each of a turn's one
+// stage, two of the other; their sums are joined at the end.
+template <typename T, typename O, int MODE, int RING>
+__global__ void __launch_bounds__(256) linear_long_kernel(const LinearParams p) {
+  typedef Tile<T, MODE, false, false, 64, 64, 4> Tl;
+  typedef Elem<T> E;
+  constexpr bool kWide = sizeof(T) == 1 && sizeof(O) == 4;
+  // alone, a workgroup reads its fragments before it starts loads (256 x 2048 x 2048
+  // 14.2 -> 13.8 us); beside another after (512 x 2048 x 2048 18.5 -> 17.6)
+  constexpr bool kLate = RING > 4;
+  __shared__ __align__(1024) T lds[RING * Tl::kStage];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wm = (wave & 1) * 32, h = wave >> 1;
+  const Tl t(p, wave, lane);
+  const Cols<MODE> cols(p, t.n0 + linear_col<32>(lane % ((MODE == GATED ? 32 : 64) / 8)));
+  f32x16 acc[2][1];
+  acc_zero(acc);
+  // (past the end the loads drop what they fetch: as many are on their way in every turn)
+  auto fetch = [&](int kt) {
+    const bool on = kt < t.kt1;
+    const int k0 = on ? kt * E::BK : 0;
+    T* const to = lds + (kt - t.kt0) % RING * Tl::kStage;
+    t.sa.fetch(t.a + k0, t.a + k0, to, wave, on ? p.K - k0 : 0);
+    t.sb.fetch(t.b + k0, t.b2 + k0, to + Tl::SA::kElems, wave, on ? p.K - k0 : 0);
+  };
+#pragma unroll
+  for (int s = 0; s < RING - 2; ++s) fetch(t.kt0 + s);
+  for (int kt = t.kt0; kt < t.kt1; kt += 2) {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((RING - 4) * Tl::kLoads) : "memory");  // these two stages'
+    wait_lds();  // the last two's fragments, before anyone refills their buffers
+    meet();
+    if constexpr (!kLate) fetch(kt + RING - 2), fetch(kt + RING - 1);
+    const T* const la = lds + (kt - t.kt0 + h) % RING * Tl::kStage;
+    typename E::Frag fa[2][2][1], fb[2][2][2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      Tl::SA::template frags<1>(la, wm, q, lane, fa[q]);
+      Tl::SB::template frags<2>(la + Tl::SA::kElems, 0, q, lane, fb[q]);
+    }
+    if constexpr (kLate) {
+      __builtin_amdgcn_sched_barrier(0);
+      fetch(kt + RING - 2), fetch(kt + RING - 1);
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) mma_half<E, kWide>(fa[q], fb[q], acc);
+  }
+  wait_loads();
+  __syncthreads();
+  float* const sums = reinterpret_cast<float*>(lds) + (wave & 1) * 2048;
+  if (h == 1) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sums[(i * 16 + e) * 64 + lane] = acc[i][0][e];
+  }
+  __syncthreads();
+  if (h == 1) return;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[i][0][e] += sums[(i * 16 + e) * 64 + lane];
+  linear_out<O, MODE, 32>(p, acc, cols, reinterpret_cast<float*>(lds) + 4096 + wave * 32 * 68, t.m0 + wm, t.n0, t.share, lane);
+}
+
 // Joins the shares of a split contraction, in order, and finishes the output.
 template <typename T, int MODE>
 __global__ void __launch_bounds__(256) linear_join_kernel(const LinearParams p) {

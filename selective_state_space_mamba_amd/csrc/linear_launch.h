@@ -156,15 +156,43 @@ inline RowsPlan rows_plan(int64_t M, int64_t N) {
   }
   return best;
 }
-// For a product of these modes whose tiles are planned as pl and whose round of
-// 16 rows takes round_us: always up to 64 rows, up to 256 where it is expected
-// to be the faster (the tiles' expectation is a quarter long at so few rows;
-// 128 rows of 1536 x 768 bfloat16 in a gated pair 12.8 us in tiles, 9.1 so; 65
-// rows of 4096 x 2048 15.3 and 24.7).
-inline RowsPlan rows_or_tiles(int64_t M, int64_t N, const ProductPlan& pl, double round_us) {
-  if (M > 256) return RowsPlan{0, 0.0};
-  const RowsPlan rp = rows_plan(M, N);
-  return M <= kRowsMax || rp.time * round_us < 0.8 * pl.us ? rp : RowsPlan{0, 0.0};
+// The long tile over N columns (of the pair, of both weights) and a contraction
+// of K bfloat16 elements, or as many bytes: eight stages where every workgroup
+// has a compute unit and there is enough to fetch, else four, 512 workgroups a
+// round (gated pair of 64 x 4096 x 4096, eight and four stages 20.6 and 26.3 us, of
+// 256 x 768 x 2048 9.4 and 8.7, of 128 x 2048 x 8192 24.8 and 18.9).
+struct LongPlan {
+  int ring;
+  double us;  // expected
+};
+inline LongPlan plan_long(int64_t M, int64_t N, int64_t K) {
+  const int64_t wgs = ((M + 63) / 64) * ((N + 63) / 64);
+  if (wgs > 2048 || K < 256) return LongPlan{0, 1e300};
+  if (wgs <= 256) return K > 1024 ? LongPlan{8, 5.0 + 0.0039 * (double)K} : LongPlan{4, 6.0 + 0.003 * (double)K};
+  return LongPlan{4, 1.5 + (4.5 + 0.006 * (double)K) * (double)((wgs + 511) / 512)};
+}
+// How a product of these modes is run if not by the tiles planned as pl: N
+// outputs a row, a round of 16 rows of the few-rows kernel round_us, the long
+// tile as planned.  Up to 64 rows the former two alone, then whichever is
+// expected to be the fastest (the tiles' expectation is a tenth to a quarter
+// long at so few rows; 128 rows of 1536 x 768 bfloat16 in a gated pair 12.8 us in
+// tiles, 9.1 in rows, 65 rows of 4096 x 2048 15.3 and 24.7; over 400 products of
+// 17 to 4096 rows each, the long tile among the choices and not: gated pair 5.6 %
+// less time on average, 8-bit 4.9 %; 256 x 2048 x 2048 22.6 -> 13.8 us).
+struct FewPlan {
+  int tiles, ring;  // of linear_rows_kernel, or stages of linear_long_kernel; zeros: tiles
+};
+inline bool by_tiles(const FewPlan& f) { return f.tiles == 0 && f.ring == 0; }
+inline FewPlan rows_or_tiles(int64_t M, int64_t N, const ProductPlan& pl, double round_us, const LongPlan& lp) {
+  FewPlan best{0, 0};
+  double us = 0.9 * pl.us;
+  if (M <= 256) {
+    const RowsPlan rp = rows_plan(M, N);
+    const double rows_us = rp.time * round_us;
+    if (M <= kRowsMax || rows_us < 0.8 * pl.us) us = rows_us, best = FewPlan{rp.tiles, 0};
+  }
+  if (lp.ring > 0 && lp.us < us) best = FewPlan{0, lp.ring};
+  return best;
 }
 
 template <typename T, typename O, int MODE>
@@ -183,6 +211,24 @@ hipError_t product_rows(LinearParams p, int tiles, hipStream_t stream) {
 template <typename T, typename O, int MODE>
 hipError_t forward(const LinearParams& p, const ProductPlan& pl, int tiles, hipStream_t stream) {
   return tiles > 0 ? product_rows<T, O, MODE>(p, tiles, stream) : product<T, O, MODE, false, false>(p, pl, stream);
+}
+
+template <typename T, typename O, int MODE>
+hipError_t product_long(LinearParams p, int ring, hipStream_t stream) {
+  p.tiles_m = ceil_div(p.M, 64), p.tiles_n = ceil_div(p.N, MODE == GATED ? 32 : 64), p.splits = 1;
+  p.kt_per_split = ceil_div(p.K, Elem<T>::BK), p.part = nullptr;
+  const unsigned grid = (unsigned)(p.tiles_m * p.tiles_n);
+  if (ring == 8) linear_long_kernel<T, O, MODE, 8><<<grid, 256, 0, stream>>>(p);
+  else linear_long_kernel<T, O, MODE, 4><<<grid, 256, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+// The same for the gated pair and the 8-bit product, few: how, if not by tiles.
+template <typename T, typename O, int MODE>
+hipError_t forward(const LinearParams& p, const ProductPlan& pl, const FewPlan& few, hipStream_t stream) {
+  if constexpr (sizeof(T) < 4)
+    if (few.ring > 0) return product_long<T, O, MODE>(p, few.ring, stream);
+  return forward<T, O, MODE>(p, pl, few.tiles, stream);
 }
 
 }  // namespace mscan

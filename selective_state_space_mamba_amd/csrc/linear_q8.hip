@@ -22,8 +22,8 @@ int check(const mamba_linear_dims* g) {
 ProductPlan plan(const mamba_linear_dims* g) { return plan_product(g->rows, g->out_dim, g->in_dim / 2, true, SCALED); }
 
 // (a round of 16 rows: K = 768, 1536, 4096: 3.5, 4.0, 6.4 us)
-RowsPlan plan_few(const mamba_linear_dims* g, const ProductPlan& pl) {
-  return rows_or_tiles(g->rows, g->out_dim, pl, 2.7 + 0.9e-3 * (double)g->in_dim);
+FewPlan plan_few(const mamba_linear_dims* g, const ProductPlan& pl) {
+  return rows_or_tiles(g->rows, g->out_dim, pl, 2.7 + 0.9e-3 * (double)g->in_dim, plan_long(g->rows, g->out_dim, g->in_dim / 2));
 }
 
 }  // namespace
@@ -33,7 +33,7 @@ extern "C" {
 size_t mamba_linear_q8_workspace_bytes(const mamba_linear_dims* dims) {
   if (check(dims) != MAMBA_OK) return (size_t)-1;
   const ProductPlan pl = plan(dims);
-  return plan_few(dims, pl).tiles > 0 ? 0 : pl.part;
+  return by_tiles(plan_few(dims, pl)) ? pl.part : 0;
 }
 
 int mamba_linear_q8(const void* x, const float* x_scale, const void* weight, const float* w_scale, const float* bias,
@@ -46,15 +46,15 @@ int mamba_linear_q8(const void* x, const float* x_scale, const void* weight, con
   for (const float* q : {x_scale, w_scale, bias})
     if (!aligned(q, 4)) return MAMBA_ERR_UNSUPPORTED;
   const ProductPlan pl = plan(dims);
-  const int tiles = plan_few(dims, pl).tiles;
-  if (tiles == 0 && pl.part > 0 && (!dims->workspace || dims->workspace_bytes < pl.part)) return MAMBA_ERR_WORKSPACE;
+  const FewPlan few = plan_few(dims, pl);
+  if (by_tiles(few) && pl.part > 0 && (!dims->workspace || dims->workspace_bytes < pl.part)) return MAMBA_ERR_WORKSPACE;
   LinearParams p{};
   p.a = x, p.b = weight, p.lda = p.ldb = dims->in_dim;
   p.M = (int)dims->rows, p.N = (int)dims->out_dim, p.K = (int)dims->in_dim;
   p.sx = x_scale, p.sw = w_scale, p.bias = bias, p.residual = residual, p.out = out, p.act = dims->act;
   p.part = static_cast<float*>(dims->workspace);
-  const hipError_t e = dims->dtype == MAMBA_DTYPE_BF16 ? forward<uint8_t, uint16_t, SCALED>(p, pl, tiles, stream)
-                                                       : forward<uint8_t, float, SCALED>(p, pl, tiles, stream);
+  const hipError_t e = dims->dtype == MAMBA_DTYPE_BF16 ? forward<uint8_t, uint16_t, SCALED>(p, pl, few, stream)
+                                                       : forward<uint8_t, float, SCALED>(p, pl, few, stream);
   return e == hipSuccess ? MAMBA_OK : MAMBA_ERR_HIP;
 }
 

@@ -135,7 +135,7 @@ def weights4(N, K, group, seed, zero, scale_type="bf16", device="cuda:0"):
 
 
 def planned(M, N, K, more=False, wide=True):
-    """(tile rows, tile columns, shares) of a product of bfloat16 rows, written from the rule beside the launch
+    """(tile rows, tile columns, shares, us) of a product of bfloat16 rows, written from the rule beside the launch
     (csrc/linear_launch.h): the least expected time.  more: of the gated pair (its N columns twice, without the
     192 columns of wide) and of 8-bit operands (half their K)."""
     best = None
@@ -154,9 +154,33 @@ def planned(M, N, K, more=False, wide=True):
             us = rounds * fix + (rounds - 1 + last) * per * each * 64
             if shares > 1:
                 us += 4.0 + shares * M * N * 8 / 5.0e6
-            if best is None or us < best[0]:
-                best = (us, bm, bn, shares)
+            if best is None or us < best[3]:
+                best = (bm, bn, shares, us)
             if s >= most:
                 break
             s = min(2 * s, most)
-    return best[1:]
+    return best
+
+
+def planned_kind(op, M, K, N):
+    """How the forward of a "gated" pair of bfloat16 rows, or a product of "q8" operands, is run (the same rules):
+    ("rows", tiles), ("long", stages) or ("tile", rows, columns, shares)."""
+    gated = op == "gated"
+    cols, k = (2 * N, K) if gated else (N, K // 2)
+    tile = planned(M, cols, k, True, not gated)
+    kind, best = ("tile",) + tile[:3], 0.9 * tile[3]
+    if M <= 256:
+        rounds = {tiles: -(-(-(-M // (16 * tiles)) * -(-N // 16)) // 256) for tiles in (1, 2, 4)}
+        time, tiles = min((t * (1.0 + 0.6 * (rounds[n] - 1)), n) for n, t in ((1, 1.0), (2, 1.25), (4, 1.8)))
+        time *= 2.6 + 2.8e-3 * K if gated else 2.7 + 0.9e-3 * K
+        if M <= 64 or time < 0.8 * tile[3]:
+            kind, best = ("rows", tiles), time
+    groups = -(-M // 64) * -(-cols // 64)
+    if groups <= 2048 and k >= 256:
+        stages = 8 if groups <= 256 and k > 1024 else 4
+        us = 5.0 + 0.0039 * k if stages == 8 else 6.0 + 0.003 * k
+        if groups > 256:
+            us = 1.5 + (4.5 + 0.006 * k) * -(-groups // 512)
+        if us < best:
+            kind = ("long", stages)
+    return kind

@@ -10,7 +10,7 @@ import pytest
 import selective_state_space_mamba_amd as ms
 from selective_state_space_mamba_amd import _binding as E
 
-from ffutil import gated_ref, maker, planned, rms_grads, rms_ref
+from ffutil import gated_ref, maker, planned, planned_kind, rms_grads, rms_ref
 
 FAKE = 0x100000  # 16-byte aligned stand-in pointer: every call below fails validation first
 
@@ -51,16 +51,20 @@ def test_rms_sizes(lib):
 def test_planned_tiles(lib):
     """The tests' rule for tiles and shares is the library's: the plain product's own report, the others' workspaces."""
     rng = random.Random(6)
-    for _ in range(500):
-        M, N, K = (int(2 ** rng.uniform(a, b)) for a, b in ((8.1, 16), (0, 11), (1, 11)))
+    seen = set()
+    for _ in range(1500):
+        M, N, K = (int(2 ** rng.uniform(a, b)) for a, b in ((6.1, 16), (0, 11), (1, 11)))
         N, K = 8 * N, 8 * K
         d = ms.make_linear_dims(M, K, N, ms.DTYPE_BF16)
-        assert planned(M, N, K) == tuple(ms.linear_plan(d, 0)), (M, N, K)
-        shares = planned(M, 2 * N, K, True, False)[2]
-        assert ms.gated_linear_fwd_workspace_bytes(d) == (-(-shares * M * 2 * N * 4 // 256) * 256 if shares > 1 else 0)
-        shares = planned(M, N, K, True)[2]
-        d = ms.make_linear_dims(M, 2 * K, N, ms.DTYPE_BF16)
-        assert ms.linear_q8_workspace_bytes(d) == (-(-shares * M * N * 4 // 256) * 256 if shares > 1 else 0)
+        assert planned(M, N, K)[:3] == tuple(ms.linear_plan(d, 0)), (M, N, K)
+        for op, query, cols, k in (("gated", ms.gated_linear_fwd_workspace_bytes, 2 * N, K),
+                                   ("q8", ms.linear_q8_workspace_bytes, N, 2 * K)):
+            kind = planned_kind(op, M, k, N)
+            shares = kind[3] if kind[0] == "tile" else 1
+            need = -(-shares * M * cols * 4 // 256) * 256 if shares > 1 else 0
+            assert query(ms.make_linear_dims(M, k, N, ms.DTYPE_BF16)) == need, (op, M, N, k)
+            seen.add((op, kind[0], shares > 1))
+    assert len(seen) == 8, seen
 
 
 def test_rms_refusals(lib):

@@ -6,7 +6,7 @@ import pytest
 
 import selective_state_space_mamba_amd as ms
 
-from ffutil import close, gated_ref, maker, planned
+from ffutil import close, gated_ref, maker, planned_kind
 from layerutil import ACTS
 from scanutil import torch
 
@@ -118,11 +118,12 @@ def test_exact_products():
 # Sizes at which the three products of the pair take each tile, whole and in shares of the contraction.
 TILED = [(300, 136, 64), (300, 136, 512), (1000, 136, 64), (300, 1024, 4104), (300, 1536, 4104), (700, 4104, 4104),
          (8192, 136, 4104), (16384, 136, 2048), (16384, 200, 4104), (40000, 136, 64), (40000, 136, 128), (9000, 136, 1032),
-         (300, 1040, 64), (400, 4112, 4104)]
+         (300, 1040, 64), (300, 1040, 72), (400, 4112, 4104), (100, 4112, 64), (300, 528, 64), (300, 528, 200),
+         (130, 8208, 4104)]
 
 
 def test_every_tile():
-    """Whole numbers through every tile of the forward (128 and 256 columns), of dx (as the plain product with twice the rows of a weight, whole stages each)
+    """Whole numbers through every tile of the forward (128 and 256 columns, and the long one), of dx (as the plain product with twice the rows of a weight, whole stages each)
     and dW (with 2N rows), without a tolerance; and that TILED is what the comment says."""
     t = torch()
     gen = t.Generator(device="cpu")
@@ -135,8 +136,8 @@ def test_every_tile():
                               (2, ms.make_linear_dims(M, K, 2 * N, ms.DTYPE_BF16))):
             rows, cols, shares = ms.linear_plan(dims, product)
             seen.add((product, rows, cols, shares > 1))
-        rows, cols, shares = planned(M, 2 * N, K, True, False)
-        seen.add((0, rows, cols, shares > 1))
+        kind = planned_kind("gated", M, K, N)
+        seen.add((0,) + (kind if kind[0] == "long" else kind[1:3] + (kind[3] > 1,)))
 
         def ints(lo, hi, *shape):
             return t.randint(lo, hi, shape, generator=gen).double().to("cuda:0")
@@ -156,13 +157,13 @@ def test_every_tile():
             assert t.equal(got[k], v.float().to(got[k].dtype)), (M, K, N, k)
     tiles = [(128, 128), (256, 192), (256, 256)]
     assert seen >= {(p,) + tile + (split,) for p in (0, 1, 2) for tile in tiles for split in (False, True)
-                    if p > 0 or tile != (256, 192)}, seen
+                    if p > 0 or tile != (256, 192)} | {(0, "long", 4), (0, "long", 8)}, seen
 
 
-@pytest.mark.parametrize("M", [4, 500])
-def test_rows_stay_apart_and_stacked_weights(M):
+@pytest.mark.parametrize("M,K", [(4, 72), (500, 72), (500, 1096)])
+def test_rows_stay_apart_and_stacked_weights(M, K):
     t = torch()
-    v = make(M, 72, 80, "bf16", 12)
+    v = make(M, K, 80, "bf16", 12)
     v["x"][1, 71] = float("nan")
     v["x"][M - 1, 0] = float("inf")
     args = (v["wg"], v["wu"], v["bg"], v["bu"])

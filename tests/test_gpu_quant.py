@@ -9,7 +9,7 @@ import pytest
 
 import selective_state_space_mamba_amd as ms
 
-from ffutil import close, dtype_of, finish_ref, maker, mm, planned, rows8, weights4
+from ffutil import close, dtype_of, finish_ref, maker, mm, planned_kind, rows8, weights4
 from layerutil import ACTS
 from scanutil import torch
 
@@ -85,22 +85,22 @@ def test_8bit_exact_products():
         assert t.equal(got, x.float())
 
 
-# Sizes at which the product takes each tile, whole and in shares of the contraction.
+# Sizes at which the product takes each tile, whole and in shares of the contraction, and the long one.
 TILED = [(300, 144, 64), (300, 2064, 64), (40000, 528, 136), (1000, 8208, 4104), (40000, 144, 136), (400, 8208, 8200),
-         (2000, 144, 6152), (9000, 12304, 136)]
+         (2000, 144, 6152), (9000, 12304, 136), (100, 12304, 64), (300, 528, 64), (300, 528, 72), (1000, 4112, 200)]
 
 
 def test_8bit_every_tile():
     """Whole numbers through every tile, without a tolerance, for both types of output; and that TILED is what the
-    comment says (the plan for as many bytes of bfloat16)."""
+    comment says."""
     t = torch()
     gen = t.Generator(device="cpu")
     gen.manual_seed(3)
     seen = set()
     for M, K, N in TILED:
         print("[gpu case] q8 tiles", M, K, N, flush=True)
-        rows, cols, shares = planned(M, N, K // 2, True)
-        seen.add((rows, cols, shares > 1))
+        kind = planned_kind("q8", M, K, N)
+        seen.add(kind if kind[0] == "long" else kind[1:3] + (kind[3] > 1,))
         x = t.randint(-1, 2, (M, K), generator=gen).float().to("cuda:0")
         w = t.randint(-1, 2, (N, K), generator=gen).float().to("cuda:0")
         res = t.randint(-9, 10, (M, N), generator=gen).float().to("cuda:0")
@@ -109,15 +109,16 @@ def test_8bit_every_tile():
         for dt in (t.float32, t.bfloat16):
             got = ms.linear_q8(x.to(t.float8_e4m3fn), sx, w.to(t.float8_e4m3fn), sw, None, res.to(dt))
             assert t.equal(got, want.float().to(dt)), (M, K, N, dt)
-    assert seen == {tile + (split,) for tile in ((128, 128), (256, 192), (256, 256)) for split in (False, True)}, seen
+    assert seen == {tile + (split,) for tile in ((128, 128), (256, 192), (256, 256)) for split in (False, True)} | {
+        ("long", 4), ("long", 8)}, seen
 
 
-@pytest.mark.parametrize("M", [4, 300])
-def test_8bit_rows_stay_apart(M):
+@pytest.mark.parametrize("M,K", [(4, 96), (300, 96), (300, 528)])
+def test_8bit_rows_stay_apart(M, K):
     t = torch()
     n = maker(M)
-    x, sx = rows8(n((M, 96)))
-    w, sw = rows8(n((40, 96)))
+    x, sx = rows8(n((M, K)))
+    w, sw = rows8(n((40, K)))
     x.view(t.uint8)[1, 5] = 0x7f  # NaN
     sx[M - 1] = 0
     got = ms.linear_q8(x, sx, w, sw)
