@@ -26,14 +26,14 @@ struct RmsPlan {
 // One wave a row up to 2048 channels, unless the rows are so few that four
 // waves each leave the chip room (bfloat16 with a residual, one and four waves,
 // us: 256 rows of 768 3.3 and 3.0, of 2048 4.3 and 3.1; 1024 rows of 768 3.6 and
-// 3.6, 8-bit 3.9 and 4.3, of 2048 5.2 and 4.4; backward, whose workgroups each
-// leave a row of sums: 64 rows of 2048 6.6 and 5.2, 256 7.1 and 7.3).  Rows of up
+// 3.6, 8-bit 3.9 and 4.3, of 2048 5.2 and 4.4; backward: 256 rows
+// of 2048 3.8 and 3.2, 512 4.0 and 4.2, 256 of 1024 3.1 and 3.1).  Rows of up
 // to 256 channels, of single heads, share a wave (262144 rows of 64 forward 65 us
 // with a wave each, 21 so, backward 104 and 25; of 128 73 and 40, 114 and 43).
 RmsPlan plan_rows(int64_t rows, int64_t D, bool backward) {
   const int vecs = (int)((D + 7) / 8);
   if (vecs <= 256) {
-    const int64_t few = backward ? 128 : vecs > 128 ? 1024 : 256;
+    const int64_t few = backward ? (vecs > 128 ? 256 : 128) : vecs > 128 ? 1024 : 256;
     if (rows <= few && vecs > 64) return RmsPlan{256, 1};
     if (vecs <= 32) return RmsPlan{vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32, 1};
     return RmsPlan{64, (vecs + 63) / 64};
@@ -54,11 +54,10 @@ int bwd_blocks(const mamba_rms_dims* g) {
 
 // Rows up to which dweight is added up column by column beside the rows, without
 // a workspace and a second launch.  Bfloat16, with the second launch and without:
-// 8 x 1536 4.8 and 2.7 us, 256 x 2048 7.0 and 4.2, 256 x 8192 15.2 and 5.2; 512 x
-// 768 6.0 and 6.2, x 2048 7.7 and 6.5, x 8192 19 and 13; 1024 x 768 6.9 and 10.5,
-// x 8192 22 and 22: the columns' workgroups walk every row, so that more rows take
-// the longer the narrower they are.
-constexpr int64_t kFewRows = 512;
+// 8 x 1536 4.8 and 2.7 us, 256 x 2048 7.0 and 3.8, 1024 x 64 5.1 and 4.4, x 768
+// 7.0 and 4.7, x 8192 23 and 19; 1536 x 64 5.0 and 5.5, x 2048 11.5 and 12.7: the
+// columns' workgroups walk every row.
+constexpr int64_t kFewRows = 1024;
 
 int check(const mamba_rms_dims* g) {
   if (!g) return MAMBA_ERR_INVALID;
@@ -176,13 +175,15 @@ int mamba_rms_norm_bwd(const void* s, const float* weight, const float* rstd, co
   const bool few = dims->rows <= kFewRows;
   p.dw = dweight, p.row_blocks = blocks;
   p.part = dweight && !few ? static_cast<float*>(dims->workspace) : nullptr;
-  const unsigned grid = (unsigned)(blocks + (dweight && few ? (p.D + 127) / 128 : 0));
+  const RmsPlan pl = plan_rows(dims->rows, dims->dim, true);
+  const int cols = rms_cols(pl.lanes, pl.nv);
+  const unsigned grid = (unsigned)(blocks + (dweight && few ? (p.D + cols - 1) / cols : 0));
   bool rag = dims->dim % 8 != 0;
   for (const void* q : {s, (const void*)weight, dout, dadded, (const void*)dx, (const void*)dresidual, (const void*)p.part}) rag |= !aligned(q, 16);
   by_types(dims, [&](auto* t, auto* r) {
     using T = std::remove_pointer_t<decltype(t)>;
     using R = std::remove_pointer_t<decltype(r)>;
-    by_shape(plan_rows(dims->rows, dims->dim, true), rag, [&](auto rg, auto l, auto nv) {
+    by_shape(pl, rag, [&](auto rg, auto l, auto nv) {
       constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
       rms_bwd_kernel<T, R, decltype(rg)::value, L, NV><<<grid, rms_threads<L>(), 0, stream>>>(p);
     });

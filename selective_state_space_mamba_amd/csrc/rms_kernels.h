@@ -214,13 +214,16 @@ __global__ void __launch_bounds__(rms_threads<L>()) rms_fwd_kernel(const RmsPara
   }
 }
 
-// dw of few rows, which needs nothing of a row but its rstd: 128 channels a
-// workgroup, its threads 16 vectors wide down the rows, joined in order.
-template <typename T, typename R, bool RAG, int THREADS>
+// dw of few rows, which needs nothing of a row but its rstd: COLS channels a
+// workgroup, its threads so many vectors wide down the rows, joined in order.
+// 32 channels up to 2048, 64 of wider rows (32, 64 and 128: 512 rows of 768 3.6,
+// 4.4, 6.3 us, of 2048 4.0, 4.6, 6.4, of 8192 12.5, 10.7, 13.2).
+constexpr int rms_cols(int lanes, int nv) { return lanes * nv > 256 ? 64 : 32; }
+template <typename T, typename R, bool RAG, int COLS, int THREADS>
 __device__ __forceinline__ void rms_columns(const RmsGradParams& p, int block) {
-  constexpr int G = THREADS / 16;
-  __shared__ float red[G][128 + 4];
-  const int v = threadIdx.x & 15, g = threadIdx.x >> 4, full = p.D >> 3, rest = p.D & 7, i = block * 16 + v;
+  constexpr int VL = COLS / 8, G = THREADS / VL;
+  __shared__ float red[G][COLS + 4];
+  const int v = threadIdx.x % VL, g = threadIdx.x / VL, full = p.D >> 3, rest = p.D & 7, i = block * VL + v;
   float sum[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum[j] = 0.f;
@@ -237,8 +240,8 @@ __device__ __forceinline__ void rms_columns(const RmsGradParams& p, int block) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) red[g][v * 8 + j] = sum[j];
   __syncthreads();
-  const int c = block * 128 + threadIdx.x;
-  if (threadIdx.x < 128 && c < p.D) {
+  const int c = block * COLS + threadIdx.x;
+  if (threadIdx.x < COLS && c < p.D) {
     float d = 0.f;
 #pragma unroll
     for (int k = 0; k < G; ++k) d += red[k][threadIdx.x];
@@ -253,7 +256,7 @@ __global__ void __launch_bounds__(rms_threads<L>()) rms_bwd_kernel(const RmsGrad
   __shared__ float red[rms_threads<L>() / 64];
   __shared__ float sums[kJoin > 1 ? (kJoin - 1) * NV * L * 8 : 1];
   if ((int)blockIdx.x >= p.row_blocks) {
-    rms_columns<T, R, RAG, rms_threads<L>()>(p, blockIdx.x - p.row_blocks);
+    rms_columns<T, R, RAG, rms_cols(L, NV), rms_threads<L>()>(p, blockIdx.x - p.row_blocks);
     return;
   }
   const int li = threadIdx.x % L, k = threadIdx.x / L;

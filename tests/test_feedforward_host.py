@@ -39,8 +39,8 @@ RMS_BAD = [(dict(rows=0), E.MAMBA_ERR_INVALID), (dict(dim=0), E.MAMBA_ERR_INVALI
 
 def test_rms_sizes(lib):
     assert ms.rms_norm_bwd_workspace_bytes(rms_dims()) == 0  # few rows: no scratch
-    assert ms.rms_norm_bwd_workspace_bytes(rms_dims(rows=512)) == 0
-    assert ms.rms_norm_bwd_workspace_bytes(rms_dims(rows=513)) == 17 * 64 * 4
+    assert ms.rms_norm_bwd_workspace_bytes(rms_dims(rows=1024)) == 0
+    assert ms.rms_norm_bwd_workspace_bytes(rms_dims(rows=1025)) == 33 * 64 * 4
     assert ms.rms_norm_bwd_workspace_bytes(rms_dims(rows=1 << 30)) == 1024 * 64 * 4
     assert ms.rms_norm_bwd_workspace_bytes(rms_dims(rows=1 << 30, dim=512)) == 512 * 512 * 4
     for bad, _ in RMS_BAD:
@@ -90,10 +90,10 @@ def test_rms_refusals(lib):
         for k in odd:
             assert call(rms_dims(), **{k: FAKE + 2}) == E.MAMBA_ERR_UNSUPPORTED, (call, k)
     assert fwd(rms_dims(residual_dtype=ms.DTYPE_F32), res=FAKE + 2) == E.MAMBA_ERR_UNSUPPORTED
-    assert bwd(rms_dims(rows=600), dw=FAKE) == E.MAMBA_ERR_WORKSPACE
-    need = ms.rms_norm_bwd_workspace_bytes(rms_dims(rows=600))
-    assert bwd(rms_dims(rows=600, workspace=FAKE, workspace_bytes=need - 1), dw=FAKE) == E.MAMBA_ERR_WORKSPACE
-    assert bwd(rms_dims(rows=600, workspace=FAKE + 8, workspace_bytes=need), dw=FAKE) == E.MAMBA_ERR_UNSUPPORTED
+    assert bwd(rms_dims(rows=1100), dw=FAKE) == E.MAMBA_ERR_WORKSPACE
+    need = ms.rms_norm_bwd_workspace_bytes(rms_dims(rows=1100))
+    assert bwd(rms_dims(rows=1100, workspace=FAKE, workspace_bytes=need - 1), dw=FAKE) == E.MAMBA_ERR_WORKSPACE
+    assert bwd(rms_dims(rows=1100, workspace=FAKE + 8, workspace_bytes=need), dw=FAKE) == E.MAMBA_ERR_UNSUPPORTED
 
 
 def test_rms_reference_gradients_against_differences():

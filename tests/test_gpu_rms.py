@@ -56,7 +56,7 @@ CASES = [(M, D, ty, rt) for (M, D), types in {
     (1, 1): 3, (3, 7): 3, (5, 8): 3, (2, 40): 1, (300, 63): 3, (257, 512): 1, (9, 513): 2, (64, 1000): 3, (700, 1536): 1,
     (5, 1536): 3, (256, 520): 1, (257, 520): 1, (1000, 2048): 3, (1000, 2049): 3, (33, 4096): 1, (70, 5001): 3,
     (40, 6144): 2, (21, 8192): 3, (11, 8200): 3, (4, 16383): 3, (6, 16384): 3, (5003, 768): 3, (4097, 24): 1,
-    (3000, 1029): 2, (300, 777): 3, (1100, 1999): 2, (30, 7001): 2, (1025, 1280): 1, (130, 640): 2, (512, 776): 3, (513, 776): 3, (512, 129): 1,
+    (3000, 1029): 2, (300, 777): 3, (1100, 1999): 2, (30, 7001): 2, (1025, 1280): 1, (130, 640): 2, (1024, 776): 3, (1025, 776): 3, (512, 129): 1, (1024, 40): 1,
     (70001, 64): 1, (9001, 128): 3, (5003, 106): 3, (2001, 250): 3, (1203, 256): 3, (613, 9): 2}.items()
     for ty, rt in (("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"))[:types]]
 
