@@ -529,8 +529,9 @@ MAMBA_API int mamba_rms_norm_bwd(const void* s, const float* weight, const float
  * or NONE), in one kernel; mamba_linear_fwd is the second.  Sums, biases,
  * activation and product are taken in float32 and rounded once.  The sizes are
  * a mamba_linear_dims: M rows of K channels to N.  A row of x with a NaN is NaN
- * throughout, and one with an infinity may be; no other row is.  (Likewise a
- * row of a weight and its column.) */
+ * throughout, and one with an infinity may be (in float32 it is with more than
+ * 64 rows, and in the backward, whose tiles take each element as three terms);
+ * no other row is.  (Likewise a row of a weight and its column.) */
 
 /* Bytes of workspace; pure functions of the sizes, (size_t)-1 when the
  * arguments are invalid or unsupported.  The contents need not be initialised. */

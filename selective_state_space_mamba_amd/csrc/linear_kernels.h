@@ -455,7 +455,9 @@ struct Tile {
   }
 };
 
-// Eight float32 elements as three bfloat16 terms, 8 bits of the value each: their sum is the value.
+// Eight float32 elements as three bfloat16 terms whose sum is the value: its
+// upper bits (so nothing passes the range), at most 2^-7 of the value to the
+// nearest bfloat16, and the rest, 2^-16 at most and of either sign.
 __device__ __forceinline__ void three_terms(const f32x4v& lo, const f32x4v& hi, bf16x8 (&t)[3]) {
   float v[8];
 #pragma unroll
@@ -464,23 +466,30 @@ __device__ __forceinline__ void three_terms(const f32x4v& lo, const f32x4v& hi, 
   for (int k = 0; k < 3; ++k) {
     u32x4 w;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = __builtin_amdgcn_perm(__float_as_uint(v[2 * j + 1]), __float_as_uint(v[2 * j]), 0x07060302u);
+    for (int j = 0; j < 4; ++j)
+      w[j] = k == 1 ? pack_bf16x2(v[2 * j], v[2 * j + 1])
+                    : __builtin_amdgcn_perm(__float_as_uint(v[2 * j + 1]), __float_as_uint(v[2 * j]), 0x07060302u);
     t[k] = __builtin_bit_cast(bf16x8, w);
     if (k < 2) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] -= __uint_as_float(__float_as_uint(v[j]) & 0xffff0000u);
+      for (int j = 0; j < 4; ++j) v[2 * j] -= __uint_as_float(w[j] << 16), v[2 * j + 1] -= __uint_as_float(w[j] & 0xffff0000u);
     }
   }
 }
 
 // WIDE: 8-bit elements taken as bfloat16; float32 ones as three bfloat16 terms,
-// of whose nine products the six down to 2^-16 of the largest are taken: what is
-// left out is below a product's own rounding, and six products at the bfloat16
-// rate take less than one at float32's, a sixteenth of it (the gated pair of 1037
-// x 520 x 1384: forward 50 -> 42 us, dx 46 -> 33, dW 50 -> 35, error 6e-7 ->
-// 5e-7).  The terms' making, 44 instructions for 8 elements, is the other half
-// of the time.  An infinity becomes a NaN.  PLAIN keeps float32's own instructions
-// and with them its results.
+// of whose nine products six are taken.  What is left out, the second with the
+// third, is at most 2^-22 of the product and of either sign.  Six products at the
+// bfloat16 rate take less than one at float32's, a sixteenth of it (the gated pair
+// of 1037 x 520 x 1384: forward 50 -> 42 us, dx 46 -> 33, dW 50 -> 36).  The terms'
+// making, some 44 instructions for 8 elements, is the other half of the time.  The
+// five small products are added up for every 16 elements and then to the sum, at
+// once: one by one they would be lost in a long sum of one sign, in which each is
+// below half a step (values between 1 and 2 with a contraction of 4096: mean error
+// -1.2e-5, so 8e-10, and at most 2.0e-6 where float32's own instructions have
+// 2.1e-6; time 1 to 2 % at 1037 x 520 x 1384, 7 to 10 % at 4096 x 4096 x 768,
+// forward 316 -> 340 us).  An infinity becomes a NaN, which few rows, in
+// float32's own instructions, do not make of it.  PLAIN keeps those and with them its results.
 template <typename E, bool WIDE, int FM, int FN>
 __device__ __forceinline__ void mma_half(const typename E::Frag (&fa)[2][FM], const typename E::Frag (&fb)[2][FN], f32x16 (&acc)[FN][FM]) {
   if constexpr (WIDE && E::CH == 4) {
@@ -490,13 +499,23 @@ __device__ __forceinline__ void mma_half(const typename E::Frag (&fa)[2][FM], co
 #pragma unroll
     for (int i = 0; i < FN; ++i) three_terms(fb[0][i], fb[1][i], b[i]);
 #pragma unroll
-    for (int q = 2; q >= 0; --q)  // products of terms down to 2^-16 of the largest, the small ones first
+    for (int i = 0; i < FN; ++i) {
+      f32x16 low[FM];
 #pragma unroll
-      for (int r = 0; r <= q; ++r)
+      for (int j = 0; j < FM; ++j)
 #pragma unroll
-        for (int i = 0; i < FN; ++i)
+        for (int e = 0; e < 16; ++e) low[j][e] = 0.f;
 #pragma unroll
-          for (int j = 0; j < FM; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[i][r], a[j][q - r], acc[i][j], 0, 0, 0);
+      for (int q = 2; q > 0; --q)  // (the smallest first)
+#pragma unroll
+        for (int r = 0; r <= q; ++r)
+#pragma unroll
+          for (int j = 0; j < FM; ++j) low[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[i][r], a[j][q - r], low[j], 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < FM; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[i][0], a[j][0], acc[i][j], 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < FM; ++j) acc[i][j] += low[j];
+    }
     return;
   }
   if constexpr (WIDE && E::CH == 16) {
