@@ -500,7 +500,7 @@ MAMBA_API int mamba_rms_norm_fwd(const void* x, const void* residual, const floa
 /*
  * The same with y in 8 bits (e4m3, no infinities, largest 448), not rounded to
  * dtype between:  scale = max(max|y| / 448, 2^-100) of a row, out = y / scale,
- * rounded to nearest even.  out [rows][D] bytes, scale [rows] float32, written;
+ * the float32 quotient rounded to nearest even.  out [rows][D] bytes, scale [rows] float32, written;
  * a row of zeros has scale 2^-100, a row with a NaN is NaN throughout, its
  * scale too.  Errors as above, and MAMBA_ERR_INVALID for a NULL scale.
  */

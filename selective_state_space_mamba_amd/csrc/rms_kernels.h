@@ -2,7 +2,7 @@
 // residual's addition, over rows of D channels:
 //   s = round(x + residual)  (x without a residual),  rstd = 1/sqrt(mean(s²) + eps),  y = s·rstd·w
 // with y rounded to x's type, or to 8 bits (e4m3) by the row's own scale:
-//   scale = max(max|y|/448, 2^-100),  q = y/scale
+//   scale = max(max|y|/448, 2^-100),  q = y/scale  (the float32 quotient, rounded to nearest even)
 // Backward, with xh = s·rstd and t = dout·w:
 //   ds = rstd·(t - xh·mean(t·xh)) + dadded,  dw = Σ_rows dout·xh
 //
@@ -208,7 +208,12 @@ __global__ void __launch_bounds__(rms_threads<L>()) rms_fwd_kernel(const RmsPara
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[i][j] *= inv;
+      for (int j = 0; j < 8; ++j) {
+        // y / scale rounded once: the product with the rounded reciprocal, which alone would fall beside some borders of
+        // the codes, less what it is off by (so signed that a zero keeps its sign)
+        const float q = s[i][j] * inv, off = __builtin_fmaf(q, scale, -s[i][j]);
+        s[i][j] = __builtin_fmaf(-off, inv, q);
+      }
       vec_store8<RAG>(static_cast<uint8_t*>(p.out) + at, li + i * L, full, rest, s[i]);
     }
   }
