@@ -616,7 +616,7 @@ typedef struct {
 /*
  * x [M][K] dtype; weight [N][K/2] bytes, two weights q of 0..15 each, that of
  * the even element in the low four bits; scale [N][ceil(K/group)] scale_dtype;
- * zero [N][ceil(K/group)] bytes of 0..127, or NULL (8 throughout); bias [N]
+ * zero [N][ceil(K/group)] bytes, any of 0..255, or NULL (8 throughout); bias [N]
  * float32 or NULL; residual, out [M][N] dtype, residual NULL or out itself.  No
  * other output may alias an input.  Errors: MAMBA_ERR_INVALID (NULL x, weight,
  * scale or out, a size <= 0, an unknown type or act), MAMBA_ERR_UNSUPPORTED

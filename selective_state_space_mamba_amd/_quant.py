@@ -122,7 +122,7 @@ def linear_q4(x, weight, scale, zero=None, bias=None, residual=None, *, group=12
     """mamba_linear_q4 on torch tensors: x [..., K] float32 or bfloat16, weight
     [N][K/2] uint8 (two weights a byte, the even element's in the low four bits),
     scale [N][ceil(K/group)] float32 or bfloat16, zero of the same shape uint8
-    (None: 8), bias [N] float32, residual and out [..., N] of x's type (out may
+    (any byte; None: 8), bias [N] float32, residual and out [..., N] of x's type (out may
     be residual).  A weight stands for (q - zero)·scale.  Returns out."""
     import torch
     ts = None if stream is None else _b._foreign_stream(stream)

@@ -15,7 +15,7 @@
 // throughout: infinity less infinity.)
 //   float32 rows are taken as three bfloat16 terms, 8 bits of the value each,
 // whose sum is the value, and 1 + zero/128 is taken off each weight, which
-// leaves (q - zero)/128, a bfloat16 value too: 20 instructions more for 8
+// leaves (q - zero)/128, a bfloat16 value too for every byte of zero: 20 instructions more for 8
 // weights, beside the 44 that the terms of 8 elements of x take.
 //
 // Layout.  A turn is 128 elements of the contraction for 16 columns.  A lane
@@ -106,7 +106,7 @@ __device__ __forceinline__ void q4_table(const Q4Params& p, float2* table, int n
     const int64_t at = (int64_t)(n0 + col) * p.groups + first + g;
     const float sc = p.scale_f32 ? static_cast<const float*>(p.scale)[at] : load1(static_cast<const uint16_t*>(p.scale) + at);
     const uint32_t z = p.zero ? p.zero[at] : 8u;
-    table[g * W + col] = make_float2(128.0f * sc, __uint_as_float(0x3f800000u | (z & 127u) << 16));
+    table[g * W + col] = make_float2(128.0f * sc, 1.0f + (float)z * 0.0078125f);  // (exact for every byte)
   }
 }
 
