@@ -23,22 +23,24 @@ def _device():
     return getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-_current = _current_device = None
+# (both of the above): one name, so that a thread sees both or neither while another makes them
+_torch_calls = None
 
 
 def launch_stream(x, stream) -> int:
     """The raw stream to launch on (torch's current one where stream is None).
     x has to be on the current GPU: that is the device the library launches on."""
-    global _current, _current_device
+    global _torch_calls
     dev = x.get_device()
     if dev < 0 or not x.is_cuda:
         raise ValueError("x is on %s, a GPU is needed" % x.device)
-    if _current is None:
-        _current, _current_device = _raw_current(), _device()
-    if dev != _current_device():
-        raise ValueError("x is on cuda:%d, the current device is cuda:%d" % (dev, _current_device()))
+    if _torch_calls is None:
+        _torch_calls = _raw_current(), _device()
+    current, current_device = _torch_calls
+    if dev != current_device():
+        raise ValueError("x is on cuda:%d, the current device is cuda:%d" % (dev, current_device()))
     if stream is None:
-        return _current(dev)
+        return current(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
