@@ -568,16 +568,17 @@ MAMBA_API int mamba_gated_linear_bwd(const void* x, const void* w_gate, const vo
  *
  *   out[m][n] = act(x_scale[m]·w_scale[n]·Σ_k x[m][k]·weight[n][k] + bias[n]) + residual[m][n]
  * with x [M][K] and weight [N][K] in e4m3 (as mamba_rms_norm_q8 writes it) and
- * a float32 scale for each row of either.  Products are exact.  Where dtype is
- * float32 they are added in float32.  Where it is bfloat16 the 8-bit matrix
- * instructions add them, which take eight neighbouring products (k = 8j..8j+7)
- * at a time and cut each off, towards zero, at 2^-13 of the largest of the eight
- * (an element below 2^-6 counts as 2^-6 here), then add in float32.  A sum is so
- * off by less than 7·2^-13 (8.5e-4) of the eights' largest products, added up:
- * below the rounding of a bfloat16 output where products do not cancel, and of
- * operands (2^-4 of each) where they do.  Measured, whatever K: 1.3e-5 of the
- * result in the L2 norm for normal operands, and towards zero 2e-6 of a sum of
- * positive ones and 1e-4 where these span e4m3's range.
+ * a float32 scale for each row of either.  Products are exact.  They are added
+ * in float32 where dtype is float32, and for few rows (single tokens; up to some
+ * dozens, 256 at most).  Otherwise the 8-bit matrix instructions add them, which
+ * take eight neighbouring products (k = 8j..8j+7) at a time and cut each off,
+ * towards zero, at 2^-13 of the largest of the eight (an element below 2^-6
+ * counts as 2^-6 here), then add in float32.  A sum is so off by less than
+ * 7·2^-13 (8.5e-4) of the eights' largest products, added up: below the rounding
+ * of a bfloat16 output where products do not cancel, and of operands (2^-4 of
+ * each) where they do.  Measured, whatever K: 1.3e-5 of the result in the L2 norm
+ * for normal operands, and towards zero 2e-6 of a sum of positive ones and 1e-4
+ * where these span e4m3's range.
  * In the mamba_linear_dims dtype is that of residual and out; K is a multiple
  * of 16. */
 

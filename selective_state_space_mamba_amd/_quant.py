@@ -65,9 +65,9 @@ def linear_q8(x, x_scale, weight, w_scale, bias=None, residual=None, *, act=ACT_
     float8_e4m3fn, x_scale [...] and w_scale [N] float32 (a row is x·x_scale),
     bias [N] float32, residual and out [..., N] float32 or bfloat16 (out may be
     residual).  Returns out; its type is out's, residual's or dtype, bfloat16
-    where none is given.  Products are added in float32 where it is float32; for
-    a bfloat16 output each eight neighbouring ones lose what lies below 2^-13 of
-    the largest (mamba_scan.h)."""
+    where none is given.  Products are added in float32 where it is float32, and
+    for few rows; otherwise each eight neighbouring ones lose what lies below
+    2^-13 of the largest (mamba_scan.h)."""
     import torch
     ts = None if stream is None else _b._foreign_stream(stream)
     if ts is not None:
