@@ -602,7 +602,7 @@ MAMBA_API int mamba_linear_q8(const void* x, const float* x_scale, const void* w
  *
  *   out[m][n] = act(Σ_k (q[n][k] - zero[n][k/group])·scale[n][k/group]·x[m][k] + bias[n]) + residual[m][n]
  * for few rows (a token of each of some sequences): the weights are read once
- * for 16 or 32 rows.  Weights are not rounded on the way: products are exact, sums
+ * for 16 or 32 rows (more are taken, in time that grows with them).  Weights are not rounded on the way: products are exact, sums
  * float32.  A row of x with an infinity or a NaN is NaN throughout. */
 typedef struct {
   int64_t rows;        /* M in 1..2^18 */

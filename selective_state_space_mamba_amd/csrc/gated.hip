@@ -40,9 +40,9 @@ ProductPlan plan_dw(const mamba_linear_dims* g) {
 }
 
 // Runs of rows of the backward's first pass: as many workgroups as the plain
-// product's takes (16384 x 2048: 512 runs, 103 us for 515 MB, 5.0 TB/s).  Up to 32 rows are one run,
-// whose columns' sums need no second launch (with and without, 24 x 2048 6.1 and
-// 5.2 us, 8 x 4096 5.9 and 3.9; of 48 rows 6.6 and 7.4).
+// product's takes (16384 x 2048: 512 runs, 104 us for 470 MB, 4.5 TB/s).  Up to 32
+// rows are one run, whose columns' sums need no second launch (with and without,
+// 24 x 2048 6.1 and 5.2 us, 8 x 4096 5.9 and 3.9; of 48 rows 6.6 and 7.4).
 struct GatedGradPlan {
   int chunk, chunks;
   size_t dp, part;  // bytes

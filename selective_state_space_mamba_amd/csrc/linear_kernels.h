@@ -482,7 +482,7 @@ __device__ __forceinline__ void three_terms(const f32x4v& lo, const f32x4v& hi, 
 // of whose nine products six are taken.  What is left out, the second with the
 // third, is at most 2^-22 of the product and of either sign.  Six products at the
 // bfloat16 rate take less than one at float32's, a sixteenth of it (the gated pair
-// of 1037 x 520 x 1384: forward 50 -> 42 us, dx 46 -> 33, dW 50 -> 36).  The terms'
+// of 1037 x 520 x 1384: forward 50 -> 41 us, dx 46 -> 34, dW 50 -> 37).  The terms'
 // making, some 44 instructions for 8 elements, is the other half of the time.  The
 // five small products are added up for every 16 elements and then to the sum, at
 // once: one by one they would be lost in a long sum of one sign, in which each is
@@ -916,9 +916,9 @@ __global__ void __launch_bounds__(512) linear_rows_kernel(const LinearParams p) 
 
 // ---- backward's first pass ----
 // dP = dout·act'(pre), rounded to the element type (the matrix instructions
-// take no wider operand; it adds one rounding of 2^-9 a term in bf16), and the
+// take no wider operand; it adds one rounding, 2^-8 at most, a term in bf16), and the
 // column sums of the unrounded dP over a run of rows.  pre is float32: rounded
-// to bf16 it would put 2^-9 of error into act'(pre), and with it 3e-3 into
+// to bf16 it would put 2^-8 of error into act'(pre), and with it 3e-3 into
 // dbias, which is a float32 sum; it costs 2 bytes more an output, written and
 // read once.
 struct LinearGradParams {
@@ -970,8 +970,12 @@ __global__ void __launch_bounds__(256) linear_grad_kernel(const LinearGradParams
 // The gated pair's: with a = act(g) and the pair's sums g and u,
 //   dg = dout·u·act'(g),  du = dout·a,
 // side by side in rows of 2N, so that dx is one product over both and dW one
-// product with 2N rows; and both columns' sums over a run of rows.  pre is
-// float32, as the plain product's and for the same reason.
+// product with 2N rows; and both columns' sums, unrounded, over a run of rows.
+// pre is float32, as the plain product's and for the same reason.  dg and du are
+// rounded to the element type once, as the plain product's dP: in bf16 the
+// gradients behind them are off by 2.3e-3 in L2, 1.7e-3 of it their own rounding
+// (16384 x 768 x 2048).  Two terms each would leave that alone, at twice the
+// products' work, which is half of the training step (dx 123 us, dW 119 of 490).
 struct GatedGradParams {
   const void* dout;  // [M][N]
   const float* pre;  // [2][M][N]

@@ -187,8 +187,8 @@ __device__ __forceinline__ void q4_scales(const Q4Params& p, const float2* table
     for (int g = 0; g < GS; ++g) sg[c][g] = table[min(g0 + g, ng - 1) * W + c * 16 + col];
 }
 
-// The waves' shares of the sums joined, in order, and finished.  red: [KW][CW][CT][MT][256] floats, of KW shares of
-// the contraction and CW sets of CT·16 columns, lane l of a share's wave with its four values at 4l.
+// The waves' shares of the sums joined, in order, and finished.  red: [KW][TILES][MT][256] floats, of KW shares of the
+// contraction, TILES tiles of 16 columns and MT of 16 rows, lane l of a share's wave with its four values at 4l.
 template <typename T, int MT, int TILES, int KW>
 __device__ __forceinline__ void q4_finish(const Q4Params& p, const float* red, int64_t m0, int rows, int n0) {
   for (int u = threadIdx.x; u < TILES * MT * 32; u += 64 * kQ4Waves) {
