@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(rms_threads<L>()) rms_fwd_kernel(const RmsPara
   }
   if constexpr (Q8) {
     const float scale = MaxOp::of(row_join<L, MaxOp>(top, red) / kTop8, kLeastScale), inv = 1.0f / scale;
+    const float by = scale < __builtin_inff() ? scale : 0.f;  // (y of an infinite scale: 0, or NaN, as q below)
     if (li == 0) p.scale[row] = scale;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(rms_threads<L>()) rms_fwd_kernel(const RmsPara
       for (int j = 0; j < 8; ++j) {
         // y / scale rounded once: the product with the rounded reciprocal, which alone would fall beside some borders of
         // the codes, less what it is off by (so signed that a zero keeps its sign)
-        const float q = s[i][j] * inv, off = __builtin_fmaf(q, scale, -s[i][j]);
+        const float q = s[i][j] * inv, off = __builtin_fmaf(q, by, -s[i][j]);
         s[i][j] = __builtin_fmaf(-off, inv, q);
       }
       vec_store8<RAG>(static_cast<uint8_t*>(p.out) + at, li + i * L, full, rest, s[i]);

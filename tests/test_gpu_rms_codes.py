@@ -68,3 +68,19 @@ def test_codes_of_rows(M, D):
     top = (y.cpu().abs().amax(1) / 448).clamp(min=2.0 ** -100)
     assert t.equal(scale.cpu(), top)
     assert t.equal(q.cpu().view(t.uint8), codes(y, scale[:, None]))
+
+
+@pytest.mark.parametrize("D", [64, 300, 1536, 5000])
+def test_codes_of_an_infinite_row(D):
+    """An infinite y makes the scale infinite: the others' quotients are zeros, its own is NaN."""
+    t = torch()
+    n = maker(D)
+    x, w = n((3, D)), n((D,))
+    w[5] = float("inf")
+    q, scale, _ = ms.rms_norm_q8(x, w, eps=1e-5)
+    y, _, _ = ms.rms_norm_fwd(x, w, eps=1e-5)
+    want = codes(y, scale[:, None]).view(t.float8_e4m3fn).float()
+    assert bool(scale.isinf().all())
+    got = q.cpu().float()
+    assert t.equal(got.isnan(), want.isnan()) and t.equal(got.nan_to_num(), want.nan_to_num())
+    assert bool((got.isnan().sum(1) == 1).all()) and bool((got[:, :5] == 0).all())
