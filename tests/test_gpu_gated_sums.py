@@ -22,7 +22,7 @@ def _gpu():
     torch().cuda.empty_cache()
 
 
-def judge(name, got, want, K):
+def compare(name, got, want, K):
     """Each sum of 16 products is joined by two additions, each off by at most 2^-24 of the sum so far (whose terms are
     of one sign), and the shares' and rows' joins are a few more: their mean over the outputs within 4 roots of their
     number, over as many roots of the outputs, of 2^-24.  Outputs share their rows and columns, and roundings repeat
@@ -49,12 +49,12 @@ def test_mean_error_of_positive_sums(size):
     u = lambda *s: 1 + t.rand(*s, generator=g, device="cuda:0")  # noqa: E731
     x, wg, wu, dout = u(M, K), u(N, K), u(N, K), u(M, N)
     _, pre = ms.gated_linear_fwd(x, wg, wu, act=ms.ACT_NONE, want_pre=True)
-    judge("gate", pre[0], mm(x, wg), K)
-    judge("up", pre[1], mm(x, wu), K)
+    compare("gate", pre[0], mm(x, wg), K)
+    compare("up", pre[1], mm(x, wu), K)
     got = ms.gated_linear_bwd(x, wg, wu, dout=dout, pre=t.ones_like(pre), act=ms.ACT_NONE)
-    judge("dx", got["dx"], t.matmul(dout.double(), wg.double() + wu.double()), 2 * N)
+    compare("dx", got["dx"], t.matmul(dout.double(), wg.double() + wu.double()), 2 * N)
     dw = mm(dout.t(), x.t())
-    judge("dw_gate", got["dw_gate"], dw, M)
+    compare("dw_gate", got["dw_gate"], dw, M)
     assert t.equal(got["dw_gate"], got["dw_up"])
 
 
